@@ -20,6 +20,15 @@
  *                       or paged K/V ("spark_runtime/flashinfer.rs",
  *                       ragged_prefill_bf16_hd256; "paged_attn.py",
  *                       _forward_prefix_pytorch)
+ *   pa_tree_decode      verification of drafted tokens: the nodes of one token
+ *                       tree per sequence attend to the sequence's cache and to
+ *                       the nodes their tree mask names; pa_tree_commit then
+ *                       moves the K/V rows of the accepted path behind the
+ *                       context, in every layer (no page defines them)
+ *   pa_page_bounds, pa_select_pages, pa_decode_pages  decode over the pages that
+ *                       per-page bounds of the keys rank highest for the step's
+ *                       query, chosen per sequence and kv head (no page defines
+ *                       them)
  *   pa_block_table_sync upload of the changed rows of a block table, for
  *                       CUDA-graph replays of the decode ("libmir-cuda
  *                       attention/mod.rs", captured decode nodes)
@@ -287,6 +296,143 @@ int pa_ragged_prefill(void *o, const void *q, const void *k, const void *v,
                       int total_kv_rows, int num_q_heads, int num_kv_heads, int head_dim,
                       float sm_scale, int causal, int sliding_window, void *workspace,
                       size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens.  Each sequence b of a step carries a tree of
+ * T_b = qo_indptr[b+1] - qo_indptr[b] drafted nodes whose K/V rows are already in
+ * its cache (pa_write_cache) as its LAST T_b tokens: seq_lens[b] counts them, the
+ * context is the first C_b = seq_lens[b] - T_b tokens, node i is token C_b + i.
+ */
+
+/* Bytes of workspace pa_tree_decode needs (256-byte aligned; nothing in it has to be
+ * initialised, and no call leaves anything in it for the next). */
+size_t pa_tree_decode_workspace_size(int num_seqs, int max_tree_len, int num_q_heads,
+                                     int num_kv_heads, int head_dim);
+
+/*
+ * pa_tree_decode -- attention of every drafted node, all sequences in one call.
+ * Row qo_indptr[b] + i (node i of sequence b), head h, attends to
+ *   - the context tokens j < C_b (under a sliding window those with
+ *     j >= C_b + n_i - sliding_window, n_i the number of nodes its mask names), and
+ *   - the nodes j < T_b whose bit is set in its mask row: bit j % 64 of word
+ *     tree_mask[row][j / 64].  A node sees itself only if its own bit is set; any
+ *     mask is allowed, not only those of trees, and bits at or past T_b are ignored.
+ * A row that sees nothing is written as zeros.  Nodes it does not see and tokens past
+ * seq_lens[b] contribute nothing, whatever their K/V rows hold (NaN included).
+ *   out, q        [total_rows][num_q_heads][head_dim] bf16; rows outside
+ *                 [qo_indptr[0], qo_indptr[num_seqs]) are neither read nor written
+ *   qo_indptr     [num_seqs + 1] int32, device
+ *   tree_mask     [total_rows][mask_words] 64-bit words, device, 8-byte aligned;
+ *                 mask_words >= ceil(max_tree_len / 64)
+ *   max_tree_len  >= every T_b, at most PA_MAX_TREE_LEN
+ * A sequence whose T_b is negative, exceeds max_tree_len or seq_lens[b], or whose rows
+ * leave [0, total_rows) is skipped (its rows are not written) and sets
+ * PA_ERR_DEVICE_BOUNDS.  Block tables, pools, kv_dtype and scales are those of
+ * pa_decode; sm_scale must be positive and finite.  The call reads qo_indptr, lengths
+ * and masks on the device only, so a captured call can be replayed with new trees.
+ */
+#define PA_MAX_TREE_LEN 256
+int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
+                   const int32_t *block_tables, const int32_t *seq_lens,
+                   const int32_t *qo_indptr, const int64_t *tree_mask, int mask_words,
+                   int num_seqs, int total_rows, int max_tree_len, int num_q_heads,
+                   int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                   int64_t num_blocks, int64_t stride_block, int64_t stride_head,
+                   int64_t stride_token, float sm_scale, int sliding_window, int kv_dtype,
+                   float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * pa_tree_commit -- after verification: the K/V rows of the accepted nodes become the
+ * tokens right behind the context, in every one of the pools (all layers' K and V).
+ * For sequence b and i < accept_lens[b], token C_b + i of each pool becomes what token
+ * C_b + accepted[b][i] was, bit for bit, and new_seq_lens[b] = C_b + accept_lens[b].
+ *   pools         HOST array of num_pools device pointers, all with the same strides,
+ *                 kv_dtype and block tables (e.g. [k_0, v_0, k_1, v_1, ...])
+ *   accepted      [num_seqs][max_accept] int32 node indices, each greater than the one
+ *                 before it (a path from the root down); entries past accept_lens[b]
+ *                 are not read
+ *   accept_lens   [num_seqs] int32
+ *   new_seq_lens  [num_seqs] int32, written; must not be seq_lens itself
+ * A path is cut before its first entry that is out of range or not ascending, and
+ * before max_accept entries; a sequence whose T_b is negative or exceeds max_tree_len
+ * or seq_lens[b] keeps its length and rows; both set PA_ERR_DEVICE_BOUNDS.  A page id
+ * outside the pool is neither read nor written and sets it too.  Pages that hold
+ * drafted tokens must belong to one sequence only.  One launch per 128 pools.
+ */
+int pa_tree_commit(void *const *pools, int num_pools, const int32_t *block_tables,
+                   const int32_t *seq_lens, const int32_t *qo_indptr, const int32_t *accepted,
+                   const int32_t *accept_lens, int32_t *new_seq_lens, int num_seqs,
+                   int max_tree_len, int max_accept, int num_kv_heads, int head_dim,
+                   int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                   int64_t stride_block, int64_t stride_head, int64_t stride_token,
+                   int kv_dtype, void *stream);
+
+/*
+ * Decode over selected pages.  A long sequence's decode step reads only max_pages of
+ * its pages per kv head: the first and the newest ones, and those whose keys can match
+ * the step's query best by a bound kept per page.
+ *
+ * pa_page_bounds -- per page, kv head and channel the smallest and the largest key
+ * value: bounds[page][kh][0][d] = min, [1][d] = max over the rows of the page that lie
+ * inside the sequence (a NaN among them gives NaN).  Rewrites, for each sequence, the
+ * pages that hold a token >= first_tokens[b] (NULL: every page), so a step calls it
+ * with the lengths before its pa_write_cache.
+ *   bounds          [num_blocks][num_kv_heads][2][head_dim] of the pool's type (FP8
+ *                   pools: E4M3 codes, without k_scale)
+ *   max_new_tokens  >= seq_lens[b] - first_tokens[b] for every b (>= seq_lens[b] when
+ *                   first_tokens is NULL); bounds the launch.  Tokens beyond it are not
+ *                   covered and set PA_ERR_DEVICE_BOUNDS.
+ * A page that two sequences share must have the same rows in both.
+ */
+int pa_page_bounds(void *bounds, const void *k_cache, const int32_t *block_tables,
+                   const int32_t *seq_lens, const int32_t *first_tokens, int max_new_tokens,
+                   int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                   int max_blocks_per_seq, int64_t num_blocks, int64_t stride_block,
+                   int64_t stride_head, int64_t stride_token, int kv_dtype, void *stream);
+
+/* Bytes of workspace pa_select_pages needs (256-byte aligned, never initialised). */
+size_t pa_select_pages_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+
+/*
+ * pa_select_pages -- the pages each (sequence, kv head) reads this step.  With n =
+ * ceil(seq_lens[b] / block_size) pages, min(n, max_pages) are chosen: the first
+ * sink_pages, the last recent_pages, and of the others those of the largest score
+ *   score(p) = sum over the kv head's query heads h and the channels d of
+ *              max(q[b][h][d] * min_p[d], q[b][h][d] * max_p[d]),
+ * an upper bound of the sum of q . k over any key of the page (where a head's q is zero the
+ * channel adds nothing, an infinite bound included).  Scores are compared as
+ * exact numbers (candidates that 32 bits cannot tell apart are scored again in 64);
+ * equal scores go to the lower page, and a NaN score counts as the largest.
+ *   page_tables  [num_seqs][num_kv_heads][max_pages] int32, written whole: the chosen
+ *                pages' ids in the order of their tokens, then -1
+ *   page_lens    [num_seqs] int32, written: the number of tokens those pages hold
+ * max_pages > 0, sink_pages >= 0, recent_pages >= 1 (a newest page's bounds may lag its
+ * rows), sink_pages + recent_pages <= max_pages.  A page id outside the pool scores
+ * lowest and sets PA_ERR_DEVICE_BOUNDS.
+ */
+int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const void *q, const void *bounds,
+                    const int32_t *block_tables, const int32_t *seq_lens, int num_seqs,
+                    int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                    int max_blocks_per_seq, int64_t num_blocks, int max_pages, int sink_pages,
+                    int recent_pages, int kv_dtype, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * pa_decode_pages -- the split decode with one page list per (sequence, kv head): the
+ * query heads of kv head kh attend over the page_lens[b] tokens of the pages
+ * page_tables[b][kh], as pa_decode_split over a block table does.  Takes what
+ * pa_select_pages writes, or any lists whose pages are full but the last.
+ * workspace: pa_decode_split_workspace_size(num_seqs, num_q_heads, head_dim,
+ * max_pages * block_size) bytes, 256-byte aligned.
+ */
+int pa_decode_pages(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *page_tables, const int32_t *page_lens, int num_seqs,
+                    int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                    int max_pages, int64_t num_blocks, int64_t stride_block,
+                    int64_t stride_head, int64_t stride_token, float sm_scale, int kv_dtype,
+                    float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+                    void *stream);
 
 /*
  * Block-table upload for CUDA-graph replays ("libmir-cuda attention/mod.rs",

@@ -16,6 +16,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpa.so")
 PARTITION_TOKENS = 512
+PAGE_TOKENS = 16
 _lib = None
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE, PA_ERR_TIMEOUT, \
@@ -68,9 +69,21 @@ def load():
     lib.pa_copy_blocks.restype = I
     lib.pa_swap_blocks.argtypes = [P, P, I, P, L, L, L, L, P]
     lib.pa_swap_blocks.restype = I
+    lib.pa_decode_pages.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, L, L, L, L, F, I, F, F, P,
+                                    Z, P]
+    lib.pa_tree_decode_workspace_size.argtypes = [I, I, I, I, I]
+    lib.pa_tree_decode_workspace_size.restype = Z
+    lib.pa_tree_decode.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, L, L, L, L, F,
+                                   I, I, F, F, P, Z, P]
+    lib.pa_tree_commit.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, L, L, L, L, I, P]
+    lib.pa_page_bounds.argtypes = [P, P, P, P, P, I, I, I, I, I, I, L, L, L, L, I, P]
+    lib.pa_select_pages_workspace_size.argtypes = [I, I, I]
+    lib.pa_select_pages_workspace_size.restype = Z
+    lib.pa_select_pages.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, L, I, I, I, I, P, Z, P]
     lib.pa_last_error.restype = ctypes.c_char_p
     for name in ("pa_write_cache", "pa_decode", "pa_decode_split", "pa_decode_partitions",
-                 "pa_decode_merge", "pa_ragged_prefill",
+                 "pa_decode_merge", "pa_ragged_prefill", "pa_decode_pages", "pa_tree_decode",
+                 "pa_tree_commit", "pa_page_bounds", "pa_select_pages",
                  "pa_get_device_status"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -341,6 +354,102 @@ def pa_ragged_prefill(o, q, k, v, qo_indptr_h, kv_indptr_h, qo_indptr_d, kv_indp
         _ptr(block_tables), mb, bs, nb, sb, sh, st, batch, total_qo, total_kv, nq, nkv, hd,
         float(sm_scale), 1 if causal else 0, int(sliding_window), _ptr(workspace),
         workspace.numel(), _stream(stream)))
+
+
+def tree_decode_workspace_size(num_seqs, max_tree_len, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(load().pa_tree_decode_workspace_size(num_seqs, max_tree_len, num_q_heads,
+                                                    num_kv_heads, head_dim))
+
+
+def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, tree_mask, sm_scale,
+                   max_tree_len, workspace, layout="HND", stream=None, sliding_window=0,
+                   k_scale=1.0, v_scale=1.0):
+    """Attention of drafted token trees into out [rows, nq, hd].  Sequence b's nodes are rows
+    qo_indptr[b] .. qo_indptr[b + 1] - 1 of q and the last tokens of its cache (counted in
+    seq_lens); each sees the context and the nodes whose bits tree_mask [rows, words] (int64)
+    sets for it.  max_tree_len is at least the largest tree."""
+    nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
+    sb, sh, st = pool_strides(k_cache, layout)
+    rows, nq, _ = q.shape
+    assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and \
+        tree_mask.shape[0] == rows
+    _check(load().pa_tree_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
+                                 _ptr(tree_mask), tree_mask.shape[1], block_tables.shape[0], rows,
+                                 int(max_tree_len), nq, nkv, hd, bs, block_tables.shape[1], nb, sb,
+                                 sh, st, float(sm_scale), int(sliding_window),
+                                 kv_dtype_of(k_cache), float(k_scale), float(v_scale),
+                                 _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, accepted,
+                   accept_lens, new_seq_lens, max_tree_len, layout="HND", stream=None):
+    """Moves the K/V rows of each sequence's accepted nodes (accepted int32 [B, n], ascending,
+    accept_lens[b] of them) behind its context in every layer's pools, and writes the
+    sequences' new lengths into new_seq_lens (not seq_lens itself)."""
+    pools = [t for kv in zip(key_caches, value_caches) for t in kv]
+    nb, nkv, bs, hd = _pool_geometry(pools[0], layout)
+    sb, sh, st = pool_strides(pools[0], layout)
+    for t in pools:
+        assert t.shape == pools[0].shape and t.stride() == pools[0].stride() and \
+            t.dtype == pools[0].dtype, "pools differ in geometry"
+    assert accepted.dtype == torch.int32 and accepted.is_contiguous()
+    _check(load().pa_tree_commit(_pointer_array(pools), len(pools), _ptr(block_tables),
+                                 _ptr(seq_lens), _ptr(qo_indptr), _ptr(accepted),
+                                 _ptr(accept_lens), _ptr(new_seq_lens), block_tables.shape[0],
+                                 int(max_tree_len), accepted.shape[1], nkv, hd, bs,
+                                 block_tables.shape[1], nb, sb, sh, st, kv_dtype_of(pools[0]),
+                                 _stream(stream)))
+
+
+def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, first_tokens=None,
+                   layout="HND", stream=None):
+    """Rewrites bounds [num_blocks, nkv, 2, hd] (per-channel min and max of a page's keys, of the
+    pool's type) for the pages that hold a token >= first_tokens[b] (None: every page);
+    max_new_tokens is at least seq_lens[b] - first_tokens[b] for every sequence."""
+    nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
+    sb, sh, st = pool_strides(k_cache, layout)
+    assert bounds.is_contiguous() and tuple(bounds.shape) == (nb, nkv, 2, hd) and \
+        bounds.element_size() == k_cache.element_size()
+    _check(load().pa_page_bounds(_ptr(bounds), _ptr(k_cache), _ptr(block_tables), _ptr(seq_lens),
+                                 _ptr(first_tokens), int(max_new_tokens), block_tables.shape[0],
+                                 nkv, hd, bs, block_tables.shape[1], nb, sb, sh, st,
+                                 kv_dtype_of(k_cache), _stream(stream)))
+
+
+def select_pages_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
+    return int(load().pa_select_pages_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+def pa_select_pages(page_tables, page_lens, q, bounds, block_tables, seq_lens, workspace,
+                    sink_pages=0, recent_pages=1, stream=None):
+    """Chooses up to max_pages pages per (sequence, kv head) for the queries q [B, nq, hd] by the
+    pages' key bounds, into page_tables [B, nkv, max_pages] and page_lens [B] (int32); the
+    first sink_pages and the last recent_pages are always among them."""
+    nb, nkv, _, hd = bounds.shape
+    B, nq, _ = q.shape
+    assert bounds.is_contiguous() and page_tables.is_contiguous() and page_tables.shape[:2] == (B, nkv)
+    _check(load().pa_select_pages(_ptr(page_tables), _ptr(page_lens), _ptr(q), _ptr(bounds),
+                                  _ptr(block_tables), _ptr(seq_lens), B, nq, nkv, hd, PAGE_TOKENS,
+                                  block_tables.shape[1], nb, page_tables.shape[2], int(sink_pages),
+                                  int(recent_pages), kv_dtype_of(bounds), _ptr(workspace),
+                                  workspace.numel(), _stream(stream)))
+
+
+def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, workspace,
+                    layout="HND", stream=None, k_scale=1.0, v_scale=1.0):
+    """Split decode of q [B, nq, hd] over the pages page_tables [B, nkv, max_pages] lists per
+    (sequence, kv head), page_lens[b] tokens each; the workspace is that of a split decode
+    of max_pages pages."""
+    nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
+    sb, sh, st = pool_strides(k_cache, layout)
+    B, nq, _ = q.shape
+    assert page_tables.is_contiguous() and page_tables.shape[:2] == (B, nkv)
+    _check(load().pa_decode_pages(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(page_tables), _ptr(page_lens), B, nq, nkv, hd, bs,
+                                  page_tables.shape[2], nb, sb, sh, st, float(sm_scale),
+                                  kv_dtype_of(k_cache), float(k_scale), float(v_scale),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def selftest_wait_timeout(stream=None):

@@ -152,6 +152,7 @@ int decode_common(pa::DecodeParams &p, void *out, const void *q, const void *k_c
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
     p.kv_rep = 1;
+    p.table_heads = 1;
     p.pool_kv_heads = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
@@ -165,6 +166,20 @@ int decode_common(pa::DecodeParams &p, void *out, const void *q, const void *k_c
 }
 
 }  // namespace
+
+int pa::api_check_heads(int head_dim, int num_q_heads, int num_kv_heads) {
+    return check_heads(head_dim, num_q_heads, num_kv_heads);
+}
+
+int pa::api_check_kv_dtype(int kv_dtype, float k_scale, float v_scale) {
+    return check_kv_dtype(kv_dtype, k_scale, v_scale);
+}
+
+int pa::api_check_pool(int head_dim, int block_size, int64_t num_blocks, int num_kv_heads,
+                       int64_t sb, int64_t sh, int64_t st, int kv_dtype) {
+    return check_pool(head_dim, block_size, num_blocks, num_kv_heads, sb, sh, st,
+                      kv_elem_bytes(kv_dtype));
+}
 
 int pa::set_error(int code, const char *msg) { return fail(code, "%s", msg); }
 
@@ -430,6 +445,35 @@ int pa_decode_split(void *out, const void *q, const void *k_cache, const void *v
         if (e != cudaSuccess) return cuda_fail(e, "decode partition launch");
     }
     cudaError_t e = pa::launch_merge(p, head_dim, s);
+    if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+    return PA_OK;
+}
+
+int pa_decode_pages(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *page_tables, const int32_t *page_lens, int num_seqs,
+                    int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                    int max_pages, int64_t num_blocks, int64_t stride_block,
+                    int64_t stride_head, int64_t stride_token, float sm_scale, int kv_dtype,
+                    float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+    if (max_pages > INT32_MAX / 16) return fail(PA_ERR_UNSUPPORTED, "max_pages %d", max_pages);
+    pa::DecodeParams p;
+    int rc = decode_common(p, out, q, k_cache, v_cache, page_tables, page_lens, num_seqs,
+                           num_q_heads, num_kv_heads, head_dim, block_size, max_pages, num_blocks,
+                           stride_block, stride_head, stride_token, sm_scale, 0, kv_dtype, k_scale,
+                           v_scale);
+    if (rc) return rc;
+    p.table_heads = num_kv_heads;
+    rc = split_setup(p, num_seqs, num_q_heads, head_dim, max_pages, max_pages * 16, workspace,
+                     workspace_bytes);
+    if (rc) return rc;
+    if (num_seqs == 0) return PA_OK;
+    rc = status_ptr(&p.status);
+    if (rc) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = pa::launch_decode(p, head_dim, true, s);
+    if (e != cudaSuccess) return cuda_fail(e, "decode partition launch");
+    e = pa::launch_merge(p, head_dim, s);
     if (e != cudaSuccess) return cuda_fail(e, "merge launch");
     return PA_OK;
 }

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(DecodeCfg<HD, G, FP8>::NT, (HD == 256 || G == 
                 }
                 ++it;
             }
-            const int32_t *bt_row = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+            const int32_t *bt_row = decode_table_row(p, b, kh / p.kv_rep);
             for (int t0 = t_begin; t0 < t_end && !stop; t0 += kPartition) {
                 const int np = (min(kPartition, t_end - t0) + kBlockSize - 1) / kBlockSize;
                 const int pg_lo = max(0, ws - t0) / kBlockSize;   // first page in the window

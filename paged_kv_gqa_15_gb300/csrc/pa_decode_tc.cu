@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         prefetch_tensormap(&prm.tm_q);
     }
     if (warp >= 2 && warp < 6)   // the softmax warps are idle until the first scores
-        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, p.max_blocks,
+        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, p.table_heads, p.max_blocks,
                                static_cast<size_t>(p.num_seqs) * p.num_q_heads * HD * 2,
                                threadIdx.x - 64, 128);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -300,8 +300,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int np = (sp.n_tok + kBlockSize - 1) / kBlockSize;
             const int pg_lo = sp.t_lo / kBlockSize;
             int page = (lane >= pg_lo && lane < np)
-                           ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks +
-                                            t0 / kBlockSize + lane]
+                           ? decode_table_row(p, b, kvh)[t0 / kBlockSize + lane]
                            : -2;
             if (!is_v) {
                 const int qb = e & 1;

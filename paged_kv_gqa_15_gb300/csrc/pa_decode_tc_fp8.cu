@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&prm.tm_v);
     }
     if (warp >= 2 && warp < 6)   // the softmax warps are idle until the first scores
-        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, p.max_blocks,
+        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, p.table_heads, p.max_blocks,
                                static_cast<size_t>(p.num_seqs) * p.num_q_heads * kHD * 2,
                                threadIdx.x - 64, 128);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -333,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int np = (sp.n_tok + kBlockSize - 1) / kBlockSize;
             const int pg_lo = sp.t_lo / kBlockSize;
             int page = (lane >= pg_lo && lane < np)
-                           ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks +
-                                            sp.t0 / kBlockSize + lane]
+                           ? decode_table_row(p, b, kvh)[sp.t0 / kBlockSize + lane]
                            : -2;
             const bool bad = page != -2 && (page < 0 || page >= p.num_blocks);
             if (!is_v && __any_sync(kMask, bad) && lane == 0) atomicOr(p.status, kStatusBounds);

@@ -66,11 +66,12 @@ __device__ __forceinline__ void prefetch_l2_lines(const void *base, size_t bytes
 __device__ __forceinline__ void prefetch_decode_inputs(const int32_t *seq_lens,
                                                        const int32_t *block_tables,
                                                        const void *q, int num_seqs,
-                                                       int max_blocks, size_t q_bytes,
+                                                       int rows_per_seq, int max_blocks,
+                                                       size_t q_bytes,
                                                        unsigned t, unsigned nt) {
     const unsigned idx = blockIdx.x * nt + t, stride = gridDim.x * nt;
     prefetch_l2_lines(seq_lens, static_cast<size_t>(num_seqs) * 4, idx, stride);
-    const size_t tb = static_cast<size_t>(num_seqs) * max_blocks * 4;
+    const size_t tb = static_cast<size_t>(num_seqs) * rows_per_seq * max_blocks * 4;
     if (tb <= (4u << 20)) prefetch_l2_lines(block_tables, tb, idx, stride);
     if (q_bytes <= (4u << 20)) prefetch_l2_lines(q, q_bytes, idx, stride);
 }

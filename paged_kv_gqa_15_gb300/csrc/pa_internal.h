@@ -25,8 +25,11 @@ struct DecodeParams {
     void *out;                    // bf16 [B][nq][hd]        (single pass)
     const void *q;                // bf16 [B][nq][hd]
     const void *k_cache, *v_cache;
-    const int32_t *block_tables;  // [B][max_blocks]
+    const int32_t *block_tables;  // [B][table_heads][max_blocks]
     const int32_t *seq_lens;      // [B]
+    // 1: a sequence's kv heads share one table row; pool_kv_heads: a row per kv head
+    // (pa_decode_pages)
+    int table_heads;
     float *part_o, *part_m, *part_l;  // split partials (split pass only)
     int64_t num_blocks;
     int64_t s_block, s_head, s_token;
@@ -44,6 +47,12 @@ struct DecodeParams {
     float k_scale, v_scale;       // FP8: element value = code value * scale
     int *status;
 };
+
+// The block-table row of sequence b for pool kv head kvh.
+__host__ __device__ inline const int32_t *decode_table_row(const DecodeParams &p, int b, int kvh) {
+    return p.block_tables +
+           (static_cast<int64_t>(b) * p.table_heads + (p.table_heads > 1 ? kvh : 0)) * p.max_blocks;
+}
 
 // Work lists of up to this many query tiles are ordered on the host and passed inline
 // in the kernel's parameters (4 KB); longer ones are ordered by a one-CTA kernel.
@@ -79,6 +88,25 @@ struct PrefillLaunch {
     int head_dim;
 };
 
+struct TreeParams {
+    void *out;                    // bf16 [total_rows][nq][hd]
+    const void *q;
+    const void *k_cache, *v_cache;
+    const int32_t *block_tables;  // [B][max_blocks]
+    const int32_t *seq_lens;      // [B], drafted nodes included
+    const int32_t *qo_indptr;     // [B + 1]
+    const uint64_t *tree_mask;    // [total_rows][mask_words]
+    void *workspace;
+    int64_t num_blocks;
+    int64_t s_block, s_head, s_token;
+    int mask_words, num_seqs, total_rows, max_tree_len;
+    int num_q_heads, num_kv_heads, max_blocks;
+    int window;                   // sliding window in keys (> 0), or 0 for none
+    int kv_fp8;
+    float scale_log2, k_scale, v_scale;
+    int *status;
+};
+
 // Set the thread's last-error message and return `code` (or PA_ERR_CUDA).
 int api_fail(int code, const char *fmt, ...);
 int api_cuda_fail(cudaError_t e, const char *what);
@@ -108,6 +136,14 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, int head_dim, bool split,
                               cudaStream_t stream);
 cudaError_t launch_merge(const DecodeParams &p, int head_dim, cudaStream_t stream);
 cudaError_t launch_prefill(PrefillParams &p, const PrefillLaunch &L, cudaStream_t stream);
+
+cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t stream);
+
+// The argument checks of the entry points, shared by those in other translation units.
+int api_check_heads(int head_dim, int num_q_heads, int num_kv_heads);
+int api_check_kv_dtype(int kv_dtype, float k_scale, float v_scale);
+int api_check_pool(int head_dim, int block_size, int64_t num_blocks, int num_kv_heads, int64_t sb,
+                   int64_t sh, int64_t st, int kv_dtype);
 
 // Records `msg` as this thread's pa_last_error() text and returns `code`.
 int set_error(int code, const char *msg);
