@@ -111,7 +111,8 @@ struct TreeParams {
 int api_fail(int code, const char *fmt, ...);
 int api_cuda_fail(cudaError_t e, const char *what);
 
-// Tiled tensor map of a bf16 tensor with 128-byte swizzle, out-of-range reads as
+// Tiled tensor map of a bf16 tensor with 128-byte swizzle (64-byte for boxes with rows of 64
+// bytes), out-of-range reads as
 // zeros; false when the driver entry point or the encoding fails.
 bool encode_tensor_map_bf16(CUtensorMap *tm, const void *base, int rank, const cuuint64_t *dims,
                             const cuuint64_t *strides_bytes, const cuuint32_t *box);

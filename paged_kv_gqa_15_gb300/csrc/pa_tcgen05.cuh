@@ -68,6 +68,17 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// D[tmem] (+)= A[tmem] x B[smem desc]; kind::f8f6f4, A is M x 32 one-byte values packed four
+// per column.
+__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Instruction descriptor of kind::f16 with bf16 A and B and an fp32 accumulator.
 // a_mn / b_mn select MN-major (transposed) operands in shared memory.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, bool b_mn) {
@@ -117,6 +128,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
     d |= static_cast<uint64_t>(1) << 46;   // descriptor version for the sm_100 family
     d |= static_cast<uint64_t>(2) << 61;   // layout: SWIZZLE_128B
     return d;
+}
+
+// The same for rows of ROWB = 128 or 64 bytes under the swizzle of that width (64-byte rows:
+// atoms of 8 rows x 64 B on 512-byte boundaries).
+template <int ROWB>
+__device__ __forceinline__ uint64_t smem_desc_sw(uint32_t saddr, uint32_t lbo_bytes,
+                                                 uint32_t sbo_bytes) {
+    static_assert(ROWB == 128 || ROWB == 64, "128- or 64-byte swizzle");
+    const uint64_t d = smem_desc_sw128(saddr, lbo_bytes, sbo_bytes);
+    return ROWB == 128 ? d : (d & ~(static_cast<uint64_t>(7) << 61)) | static_cast<uint64_t>(4) << 61;
 }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, int c0, int c1,

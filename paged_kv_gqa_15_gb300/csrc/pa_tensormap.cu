@@ -84,8 +84,11 @@ bool encode_tensor_map(CUtensorMap *tm, CUtensorMapDataType dtype, const void *b
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    // the swizzle is as wide as the box's rows: 128 bytes, or 64 for 64-byte rows
+    const cuuint32_t row = box[0] * (dtype == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2);
+    const CUtensorMapSwizzle swizzle = row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     if (fn(tm, dtype, rank, const_cast<void *>(base), dims,
-           strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lock(cache_mu);

@@ -1,132 +1,1018 @@
-// pa_tree.cu -- attention of drafted token trees over the paged cache.
+// pa_tree.cu -- attention of drafted token trees over the paged cache, on the Blackwell
+// tensor cores.
 //
 // What it computes: sequence b's cache ends in its T drafted nodes (the last T of its L
 // tokens); row i of the tree and query head h attend to the C = L - T context tokens
 // (under a sliding window, those from C + n_i - window on, n_i the nodes the row sees) and
 // to the nodes named by the row's bit mask; softmax(sm_scale q . k) weighted sum of v.
 //
-// One warp per (row, query head): lanes own head_dim / 32 channels each, keys are taken one
-// at a time with the running maximum and sum of an online softmax in fp32.
+// The key axis is read once for all T rows and all query heads of a kv head, so up to about
+// 280 rows (T x group) the call is bound by streaming K and V (4 flops a row and element of
+// 4 bytes against 286 flops a byte of the GPU).  The design follows from that:
+//  * Rows are packed for the MMA's M = 128: row r of a tile is node r / g, query head r % g of
+//    one kv head, loaded by one TMA box (64 columns, g heads, 128 / g nodes).  A tree with
+//    more rows takes several row tiles, whose second read of the keys comes from L2.
+//  * The work is a line of key tiles: for every (sequence, kv head, row tile) its 64-key
+//    tiles, one after another.  CTA c of n takes an equal share of that line, whatever the
+//    lengths: no list is sorted, no counter claimed, and no CTA has more than one tile more
+//    than another.  A share is a run of segments; a segment that holds all tiles of its
+//    (sequence, kv head, row tile) writes the output, the others (at most two per CTA: its
+//    first and its last) write fp32 partial rows that a second kernel joins in a fixed order,
+//    so results do not depend on timing.
+//  * 6 warps: TMA producer (K, V pages through two rings, block tables a tile ahead), MMA
+//    issuer (S_j = Q K_j^T into TMEM, O += P_{j-1} V_{j-1} with P from TMEM), four softmax
+//    warps with a query row per thread.  Two CTAs share an SM at head_dim <= 128, so one
+//    streams and multiplies while the other's softmax runs.  Softmax warps whose rows are all
+//    empty skip the arithmetic: a tree of 8 nodes and 4 heads costs one warp's.
+//  * Only tiles that reach into the drafted nodes, the edge of a window or a bad page are
+//    masked: there each row's visible keys of a tile are one 64-bit word, put together from
+//    the context's run of keys and the row's mask words.
+//  * P is 0 for a key that a row does not see, but 0 x NaN would poison the row all the same,
+//    and rows see different nodes.  So in those tiles the softmax warps also clean V: rows
+//    past the sequence are zeroed, and non-finite elements of partly seen rows are zeroed and
+//    noted, to be added in the epilogue to the rows that do see them.
+//  * 8-bit caches (FP8): K and V tiles go to the 8-bit tensor cores as they are.  q is split
+//    into two E4M3 rows, q s = hi + lo with s a power of two that puts the row's largest |q s|
+//    in [128, 256), and P into hi + lo of 256 p, each pair good to 2^-8 of its value; two
+//    MMAs with the same B operand add up S (and O), at twice the bf16 rate each.  A row's
+//    maximum may then lag by a factor 1.75 at most, so 256 p stays within E4M3's 448.
+//  * Every mbarrier wait is bounded.
+#include <cuda.h>
+
 #include "../../include/pa.h"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRows = 128;          // rows of a tile (MMA M)
+constexpr int kKeys = 64;           // keys of a tile
+constexpr int kPages = kKeys / kBlockSize;
+constexpr int kTreeThreads = 192;
+constexpr int kMaxCtas = 304;       // two per SM of 152
+constexpr int kMaxSeqs = 1024;      // sequences per launch (their prefix is in shared memory)
 
-// Sequence b's drafted rows and lengths; ok is false (and the device status flagged by
-// `flag`) when its rows or lengths make no sense.
+constexpr uint32_t pow2_columns(uint32_t x) {
+    uint32_t v = 32;
+    while (v < x) v <<= 1;
+    return v;
+}
+
+template <int HD, bool FP8>
+struct TreeCfg {
+    static constexpr int ROWB = HD * (FP8 ? 1 : 2) < 128 ? HD * (FP8 ? 1 : 2) : 128;  // bytes of a chunk's row
+    static constexpr int CH = HD * (FP8 ? 1 : 2) / ROWB;          // column chunks of a row
+    static constexpr int COLS = HD / CH;                          // elements of a chunk's row
+    static constexpr uint32_t ATOM = 8 * ROWB;                    // swizzle atom (8 rows)
+    static constexpr uint32_t Q_CHUNK = kRows * ROWB;
+    static constexpr uint32_t Q_BYTES = (FP8 ? 2 : 1) * CH * Q_CHUNK;   // FP8: hi rows, then lo rows
+    static constexpr uint32_t KV_CHUNK = kKeys * ROWB;
+    static constexpr uint32_t KV_BYTES = CH * KV_CHUNK;
+    // Ring stages: as many tiles as two CTAs' (one at head_dim 256) shared memory holds
+    static constexpr int STAGES = HD == 256 ? (FP8 ? 4 : 2) : (HD == 128 ? (FP8 ? 4 : 2) : (FP8 ? 8 : 4));
+    static constexpr uint32_t OFF_K = Q_BYTES;
+    static constexpr uint32_t OFF_V = OFF_K + STAGES * KV_BYTES;
+    static constexpr uint32_t OFF_PREF = OFF_V + STAGES * KV_BYTES;    // int64 [kMaxSeqs + 1]
+    static constexpr uint32_t OFF_BAR = OFF_PREF + (kMaxSeqs + 1) * 8;
+    static constexpr uint32_t SMEM_USED = OFF_BAR + 1024;
+    static constexpr int CTAS_PER_SM = HD == 256 ? 1 : 2;
+    static constexpr uint32_t SMEM = SMEM_USED + 1024;           // + realignment of the base
+    static constexpr uint32_t TM_O = 2 * kKeys;                  // TMEM: S / P twice, then O
+    static constexpr uint32_t TMEM_COLS = pow2_columns(2 * kKeys + HD);
+    static_assert(CTAS_PER_SM * TMEM_COLS <= 512, "TMEM");
+    static_assert(CTAS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
+};
+
+struct TreeLaunch {
+    CUtensorMap tm_q, tm_k, tm_v;   // q only for bf16 caches (FP8 splits q itself)
+    TreeParams p;
+    float *part_o;                  // [2 grid][rows][HD], unnormalised
+    float2 *part_ml;                // [2 grid][rows]: maximum (log2 units) and sum
+    int group, kv_rep, heads;       // query heads per kernel group, groups per kv head, groups
+    int nodes;                      // nodes of a row tile (its rows: nodes * group)
+    int slot_rows;                  // rows of a partial slot
+    int min_tiles;                  // fewest tiles of a share
+};
+
+// Sequence b's drafted rows and lengths; T = 0 (and the device status set when `flag`) if
+// they make no sense.
 struct TreeSeq {
     int row0, T, L;
-    bool ok;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b, bool flag) {
     TreeSeq s;
     s.row0 = p.qo_indptr[b];
     const int row1 = p.qo_indptr[b + 1];
-    s.T = row1 - s.row0;
     s.L = max(p.seq_lens[b], 0);
     const int cap = p.max_blocks * kBlockSize;
-    bool bad = false;
-    if (s.L > cap) {
-        s.L = cap;
+    bool bad = s.L > cap;
+    s.L = min(s.L, cap);
+    s.T = 0;
+    if (s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && row1 - s.row0 <= p.max_tree_len &&
+        row1 - s.row0 <= s.L)
+        s.T = row1 - s.row0;
+    else
         bad = true;
-    }
-    s.ok = s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && s.T <= p.max_tree_len &&
-           s.T <= s.L;
-    if (flag && (bad || !s.ok)) atomicOr(p.status, kStatusBounds);
-    if (!s.ok) s.T = 0;
+    if (flag && bad) atomicOr(p.status, kStatusBounds);
     return s;
 }
 
-template <int HD, bool FP8>
-__global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int D = HD / 32;
-    const int b = blockIdx.z, i = blockIdx.x, lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const TreeSeq s = tree_seq(p, b, i == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-    if (i >= s.T || h >= p.num_q_heads) return;
-    const int kh = h / (p.num_q_heads / p.num_kv_heads);
-    const int64_t row = s.row0 + i;
-    const uint64_t *mask = p.tree_mask + row * p.mask_words;
-    const int C = s.L - s.T;
-    int lo = 0;
-    if (p.window > 0) {
-        int n = 0;
-        for (int w = 0; w * 64 < s.T; ++w) {
-            const int left = s.T - w * 64;
-            n += __popcll(left >= 64 ? mask[w] : mask[w] & ((1ull << left) - 1));
-        }
-        lo = max(0, min(C, C + n - p.window));
-    }
-    float q[D], acc[D], m = -INFINITY, l = 0.f;
-    const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + (row * p.num_q_heads + h) * HD;
-    for (int d = 0; d < D; ++d) {
-        q[d] = __bfloat162float(qr[lane * D + d]) * p.scale_log2 * p.k_scale;
-        acc[d] = 0.f;
-    }
-    const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
-    for (int j = lo; j < s.L; ++j) {
-        if (j >= C && !((mask[(j - C) >> 6] >> ((j - C) & 63)) & 1)) continue;
-        const int page = bt[j / kBlockSize];
-        if (page < 0 || page >= p.num_blocks) {
-            if (lane == 0) atomicOr(p.status, kStatusBounds);
-            continue;
-        }
-        const int64_t off = page * p.s_block + kh * p.s_head + (j % kBlockSize) * p.s_token + lane * D;
-        float k[D], v[D];
-        for (int d = 0; d < D; ++d) {
-            if constexpr (FP8) {
-                k[d] = e4m3x2_to_float2(static_cast<const uint8_t *>(p.k_cache)[off + d]).x;
-                v[d] = e4m3x2_to_float2(static_cast<const uint8_t *>(p.v_cache)[off + d]).x;
-            } else {
-                k[d] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.k_cache)[off + d]);
-                v[d] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v_cache)[off + d]);
-            }
-        }
-        float x = 0.f;
-        for (int d = 0; d < D; ++d) x = fmaf(q[d], k[d], x);
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
-        const float mn = fmaxf(m, x);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float e = x == -INFINITY ? 0.f : exp2f(x - mn);
-        l = l * f + e;
-        for (int d = 0; d < D; ++d) acc[d] = acc[d] * f + e * v[d];
-        m = mn;
-    }
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (row * p.num_q_heads + h) * HD;
-    const float inv = l > 0.f ? p.v_scale / l : 0.f;
-    for (int d = 0; d < D; ++d) o[lane * D + d] = __float2bfloat16_rn(acc[d] * inv);
+// First key any row could see (a row that sees no node sees from C - window on).
+__device__ __forceinline__ int tree_first_key(const TreeSeq &s, int window) {
+    return window > 0 ? max(0, s.L - s.T - window) : 0;
 }
 
+// Key tiles of one (sequence, kv head, row tile), and its row tiles.
+__device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
+    return s.T > 0 ? (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys : 0;
+}
+
+// pref[b] = tiles of the line before sequence b; all threads of the CTA call it.
+template <int NT>
+__device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, bool flag) {
+    const TreeParams &p = a.p;
+    for (int b = threadIdx.x; b < p.num_seqs; b += NT) {
+        const TreeSeq s = tree_seq(p, b, flag);
+        pref[b + 1] = static_cast<int64_t>(tree_tiles(s, p.window)) *
+                      ((s.T + a.nodes - 1) / a.nodes) * a.heads;
+    }
+    if (threadIdx.x == 0) pref[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        long long carry = 0;
+        for (int base = 1; base <= p.num_seqs; base += 32) {
+            const int i = base + lane;
+            long long v = i <= p.num_seqs ? pref[i] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(kAll, v, o);
+                if (lane >= o) v += u;
+            }
+            if (i <= p.num_seqs) pref[i] = v + carry;
+            carry += __shfl_sync(kAll, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// Shares that the line of `total` tiles is cut into, and where share c begins.
+__device__ __forceinline__ int tree_shares(const TreeLaunch &a, int64_t total, int grid) {
+    const int64_t n = (total + a.min_tiles - 1) / a.min_tiles;
+    return static_cast<int>(n < grid ? (n > 0 ? n : 1) : grid);
+}
+
+__device__ __forceinline__ int64_t tree_share_begin(int64_t total, int shares, int c) {
+    return c >= shares ? total : total * c / shares;
+}
+
+// One run of a share's tiles within one (sequence, kv head, row tile).
+struct TreeSegment {
+    int b, head, node0, n_nodes;   // kernel head group; first node of the row tile, nodes in it
+    int row0, T, L;
+    int j0, n;                     // first key tile (of the sequence) and tiles; n = -1: no more
+    int page_lo;                   // first page that any row sees (window)
+    int slot;                      // partial slot, or -1: all tiles are here
+};
+
+struct TreeQueue {
+    TreeSegment seg[4];
+    uint32_t bad_nodes[16];        // partly seen rows with non-finite values (see clean_values)
+    uint32_t bad_pages[16];        // ring by tile: pages whose ids are out of range
+};
+static_assert(48 * 8 + sizeof(TreeQueue) <= 1024, "queue fits behind the barriers");
+
+__device__ __forceinline__ uint64_t ones(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
+
+// Word w of a row's mask, without bits past the tree.
+__device__ __forceinline__ uint64_t mask_word(const uint64_t *mask, int w, int T) {
+    return w * 64 < T ? mask[w] & ones(T - w * 64) : 0ull;
+}
+
+__device__ __forceinline__ int mask_count(const uint64_t *mask, int T) {
+    int n = 0;
+    for (int w = 0; w * 64 < T; ++w) n += __popcll(mask_word(mask, w, T));
+    return n;
+}
+
+// The 64 mask bits from bit `at` (which may be negative) on.
+__device__ __forceinline__ uint64_t mask_bits_at(const uint64_t *mask, int at, int T) {
+    if (at <= -64 || at >= T) return 0;
+    if (at < 0) return mask_word(mask, 0, T) << -at;
+    const uint64_t lo = mask_word(mask, at >> 6, T) >> (at & 63);
+    return at & 63 ? lo | mask_word(mask, (at >> 6) + 1, T) << (64 - (at & 63)) : lo;
+}
+
+// Swizzled byte offset of 16-byte unit c of row r in a chunk whose rows have ROWB bytes.
+template <int ROWB>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    return ROWB == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Zeroes the non-finite elements of a 16-byte unit; whether there were any.
+template <bool FP8>
+__device__ __forceinline__ bool drop_non_finite(uint4 &v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t keep = 0xffffffffu;
+        if constexpr (FP8) {   // E4M3 has NaN alone: 0x7f, 0xff
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((w[i] >> 8 * e & 0x7f) == 0x7f) keep &= ~(0xffu << 8 * e);
+        } else {
+            if ((w[i] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+            if ((w[i] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+        }
+        any |= keep != 0xffffffffu;
+        w[i] &= keep;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+    return any;
+}
+
+// Two P values (at most 448) as E4M3 pairs: x = hi + lo to 2^-8 of x, by way of f16.
+__device__ __forceinline__ void split_e4m3x2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    unsigned short h, l;
+    uint32_t v, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(y), "f"(x));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(v));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(v));
+    hi = h;
+    lo = l;
+}
+
+template <int HD, bool FP8>
+__global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
+    tree_kernel(const __grid_constant__ TreeLaunch a) {
+    using C = TreeCfg<HD, FP8>;
+    const TreeParams &p = a.p;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    int64_t *pref = reinterpret_cast<int64_t *>(smem + C::OFF_PREF);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    // Tiles are numbered g over all segments of the CTA: ring stage g % STAGES, S buffer g % 2.
+    uint64_t *q_full = bars + 0;     // FP8: one arrival per softmax warp
+    uint64_t *q_empty = bars + 1;    // the segment's last S is done (commit)
+    uint64_t *o_free = bars + 2;     // the epilogue has read O (one arrival per softmax warp)
+    uint64_t *drain = bars + 3;
+    uint64_t *s_full = bars + 4;     // [2] S_g is done (commit)
+    uint64_t *p_full = bars + 6;     // [2] P_g is in TMEM, V_g is clean (one arrival per softmax warp)
+    uint64_t *k_full = bars + 8;     // [STAGES <= 8]
+    uint64_t *k_empty = bars + 16;   // [STAGES] (commit)
+    uint64_t *v_full = bars + 24;
+    uint64_t *v_empty = bars + 32;   // P_g V_g is done (commit)
+    uint64_t *seg_full = bars + 40;  // [4]
+    uint64_t *seg_empty = bars + 44; // [4]: the MMA thread and 4 softmax warps
+    TreeQueue *queue = reinterpret_cast<TreeQueue *>(bars + 48);
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    volatile int *abort_flag = &abort_word;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // rows of Q past the row tile stay zero, so that their scores are numbers
+    for (uint32_t i = threadIdx.x; i < C::Q_BYTES / 16; i += kTreeThreads)
+        reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x < 16) queue->bad_nodes[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, FP8 ? 4 : 1);
+        mbar_init(q_empty, 1);
+        mbar_init(o_free, 4);
+        mbar_init(drain, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+        }
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&seg_full[s], 1);
+            mbar_init(&seg_empty[s], 5);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&a.tm_k);
+        prefetch_tensormap(&a.tm_v);
+        if (!FP8) prefetch_tensormap(&a.tm_q);
+    }
+    fence_proxy_async_smem();   // the zeroed rows are read by the tensor core
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    // launched as a programmatic dependent: nothing before this point reads global memory
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tree_prefix<kTreeThreads>(a, pref, blockIdx.x == 0);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const int64_t total = pref[p.num_seqs];
+    const int shares = tree_shares(a, total, gridDim.x);
+    const int64_t u_begin = tree_share_begin(total, shares, blockIdx.x);
+    const int64_t u_end = tree_share_begin(total, shares, blockIdx.x + 1);
+
+    if (warp == 0) {
+        // ------------------------------- TMA producer -------------------------------
+        uint32_t g = 0, n_seg = 0;
+        uint32_t n_k = 0, n_v = 0, n_q = 0;   // copies issued (for the drain on an abort)
+        int stop = 0;
+        int64_t u = u_begin;
+        // Publishes the next segment of the share (or the end) and returns it.
+        auto next_segment = [&]() -> TreeSegment {
+            const int slot = n_seg & 3;
+            TreeSegment s = {};
+            s.n = -1;
+            if (u < u_end) {
+                int lo = 0, hi = p.num_seqs;      // largest b with pref[b] <= u
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (pref[mid] <= u) lo = mid; else hi = mid;
+                }
+                const TreeSeq q = tree_seq(p, lo, false);
+                const int tiles = tree_tiles(q, p.window);
+                const int row_tiles = (q.T + a.nodes - 1) / a.nodes;
+                const int64_t rel = u - pref[lo];
+                const int item = static_cast<int>(rel / tiles);
+                const int j = static_cast<int>(rel - static_cast<int64_t>(item) * tiles);
+                s.b = lo;
+                s.head = item / row_tiles;
+                s.node0 = item % row_tiles * a.nodes;
+                s.n_nodes = min(a.nodes, q.T - s.node0);
+                s.row0 = q.row0;
+                s.T = q.T;
+                s.L = q.L;
+                s.n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
+                s.j0 = tree_first_key(q, p.window) / kKeys + j;
+                s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                if (p.window > 0) {   // pages before the first key a row does see are not looked up
+                    int least = 1 << 30;
+                    for (int i = lane; i < q.T; i += 32)
+                        least = min(least, mask_count(p.tree_mask + static_cast<int64_t>(q.row0 + i) * p.mask_words, q.T));
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(kAll, least, o));
+                    s.page_lo = max(0, min(q.L - q.T, q.L - q.T + least - p.window)) / kBlockSize;
+                }
+                u += s.n;
+            }
+            if (lane == 0) {
+                if (!mbar_wait(&seg_empty[slot], ((n_seg >> 2) & 1) ^ 1u, p.status, abort_flag)) {
+                    stop = 1;
+                } else {
+                    queue->seg[slot] = s;
+                    mbar_arrive(&seg_full[slot]);
+                }
+            }
+            ++n_seg;
+            stop = __shfl_sync(kAll, stop, 0);
+            if (stop) s.n = -1;
+            return s;
+        };
+        // Block-table entry of page `lane` of key tile j; -2 for pages no row sees.
+        auto page_raw = [&](const TreeSegment &s, int j) -> int {
+            const int i = j * kPages + lane;
+            if (lane >= kPages || i * kBlockSize >= s.L || i < s.page_lo) return -2;
+            return p.block_tables[static_cast<int64_t>(s.b) * p.max_blocks + i];
+        };
+        const uint64_t policy = l2_policy_evict_first();
+        TreeSegment w = next_segment();
+        while (!stop && w.n >= 0) {
+            const int kvh = w.head / a.kv_rep;
+            if (!FP8) {
+                if (lane == 0) {
+                    if (n_q > 0 && !mbar_wait(q_empty, (n_q - 1) & 1, p.status, abort_flag)) stop = 1;
+                    else mbar_arrive_expect_tx(q_full, C::CH * a.nodes * a.group * C::ROWB);
+                }
+                stop = __shfl_sync(kAll, stop, 0);
+                if (stop) break;
+                if (lane < C::CH)
+                    tma_load_3d(smem + lane * C::Q_CHUNK, &a.tm_q, lane * C::COLS, w.head * a.group,
+                                w.row0 + w.node0, q_full);
+                ++n_q;
+            }
+            // Loads tile j's keys (kv = 0) or values (kv = 1); t is its number over all segments.
+            auto load = [&](int kv, uint32_t t, int page) {
+                const int s = t % C::STAGES;
+                const uint32_t ph = ((t / C::STAGES) & 1) ^ 1u;
+                uint64_t *full = kv ? &v_full[s] : &k_full[s];
+                if (lane == 0) {
+                    if (!mbar_wait(kv ? &v_empty[s] : &k_empty[s], ph, p.status, abort_flag)) stop = 1;
+                    else mbar_arrive_expect_tx(full, C::KV_BYTES);
+                }
+                stop = __shfl_sync(kAll, stop, 0);
+                if (stop) return;
+                ++(kv ? n_v : n_k);
+                const int pg = __shfl_sync(kAll, page, lane / C::CH);
+                if (lane < kPages * C::CH)   // lane l: chunk l % CH of page l / CH
+                    tma_load_4d_hint(smem + (kv ? C::OFF_V : C::OFF_K) + s * C::KV_BYTES +
+                                         (lane % C::CH) * C::KV_CHUNK + (lane / C::CH) * kBlockSize * C::ROWB,
+                                     kv ? &a.tm_v : &a.tm_k, (lane % C::CH) * C::COLS, 0, kvh, pg, full, policy);
+            };
+            // Ids out of range become an out-of-range box, which reads zeros; their keys are
+            // masked through bad_pages, which the softmax reads after S_t: the entry of tile t
+            // is written again with tile t + 16, long after (K runs at most STAGES + 1 ahead).
+            auto page_fix = [&](int raw, uint32_t t) -> int {
+                const bool bad = raw != -2 && (raw < 0 || raw >= p.num_blocks);
+                const unsigned which = __ballot_sync(kAll, bad);
+                if (lane == 0) {
+                    queue->bad_pages[t & 15] = which;
+                    if (which) atomicOr(p.status, kStatusBounds);
+                }
+                return raw == -2 || bad ? static_cast<int>(p.num_blocks) : raw;
+            };
+            int page = page_fix(page_raw(w, w.j0), g);
+            int raw = w.n > 1 ? page_raw(w, w.j0 + 1) : -2;
+            load(0, g, page);
+            const TreeSegment next = stop ? w : next_segment();
+            for (int j = 0; j < w.n && !stop; ++j) {
+                int page_next = 0;
+                if (j + 1 < w.n) {
+                    page_next = page_fix(raw, g + j + 1);
+                    if (j + 2 < w.n) raw = page_raw(w, w.j0 + j + 2);
+                    load(0, g + j + 1, page_next);
+                }
+                if (!stop) load(1, g + j, page);
+                page = page_next;
+            }
+            g += w.n;
+            w = next;
+        }
+        // never leave the CTA with copies still landing in its shared memory
+        if (lane == 0 && (stop || *abort_flag)) {
+            auto settle = [&](uint64_t *full, int ns, uint32_t n) {
+                for (uint32_t k = n > static_cast<uint32_t>(ns) ? n - ns : 0; k < n; ++k) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&full[k % ns], (k / ns) & 1u))
+                        if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                }
+            };
+            settle(q_full, 1, n_q);
+            settle(k_full, C::STAGES, n_k);
+            settle(v_full, C::STAGES, n_v);
+        }
+    } else if (warp == 1) {
+        // -------------------------------- MMA issuer --------------------------------
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = FP8 ? idesc_f32(kRows, kKeys, 0, 0, false, false)
+                                             : idesc_bf16_f32(kRows, kKeys, false, false);
+            constexpr uint32_t idesc_o = FP8 ? idesc_f32(kRows, HD, 0, 0, false, true)
+                                             : idesc_bf16_f32(kRows, HD, false, true);
+            constexpr int KB = 32;                         // bytes of K per MMA
+            constexpr int PER_CHUNK = C::ROWB / KB;        // MMAs per chunk of a row
+            constexpr int PV_ROWS = FP8 ? 32 : 16;         // keys per P.V MMA
+            constexpr uint32_t sbo = C::ATOM;
+            const uint64_t q_desc = smem_desc_sw<C::ROWB>(smem_addr(smem), 16, sbo);
+            const uint64_t k_desc = smem_desc_sw<C::ROWB>(smem_addr(smem + C::OFF_K), 16, sbo);
+            const uint64_t v_desc = smem_desc_sw<C::ROWB>(smem_addr(smem + C::OFF_V), C::KV_CHUNK, sbo);
+            uint32_t g = 0;
+            bool ok = true;
+            auto issue_pv = [&](uint32_t t, bool first, uint32_t segment) {
+                if (!ok) return;
+                const int s = t % C::STAGES;
+                if (first && segment > 0)   // the segment before has read O
+                    ok = mbar_wait(o_free, (segment - 1) & 1, p.status, abort_flag);
+                ok = ok && mbar_wait(&p_full[t & 1], (t >> 1) & 1, p.status, abort_flag) &&
+                     mbar_wait(&v_full[s], (t / C::STAGES) & 1, p.status, abort_flag);
+                if (!ok) return;
+                tc_fence_after_sync();
+                const uint64_t vd = v_desc + ((s * C::KV_BYTES) >> 4);
+                const uint32_t pt = tmem + (t & 1) * kKeys;
+#pragma unroll
+                for (int part = 0; part < (FP8 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / PV_ROWS; ++kk) {
+                        const uint64_t d = vd + ((kk * PV_ROWS * C::ROWB) >> 4);
+                        const uint32_t acc = !first || kk > 0 || part > 0 ? 1u : 0u;
+                        if constexpr (FP8) mma_f8_ts(tmem + C::TM_O, pt + part * 16 + kk * 8, d, idesc_o, acc);
+                        else mma_bf16_ts(tmem + C::TM_O, pt + kk * 8, d, idesc_o, acc);
+                    }
+                tc_commit(&v_empty[s]);
+            };
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k & 3;
+                ok = mbar_wait(&seg_full[slot], (k >> 2) & 1, p.status, abort_flag);
+                if (!ok) break;
+                const int n = queue->seg[slot].n;
+                mbar_arrive(&seg_empty[slot]);
+                if (n < 0) break;
+                ok = mbar_wait(q_full, k & 1, p.status, abort_flag);
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t t = g + j;
+                    const int s = t % C::STAGES;
+                    ok = mbar_wait(&k_full[s], (t / C::STAGES) & 1, p.status, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    // S buffer t % 2 held P_{t-2}, whose P.V was issued by this thread before
+                    const uint64_t kd = k_desc + ((s * C::KV_BYTES) >> 4);
+#pragma unroll
+                    for (int part = 0; part < (FP8 ? 2 : 1); ++part)
+#pragma unroll
+                        for (int kk = 0; kk < C::CH * PER_CHUNK; ++kk) {
+                            const uint32_t c = kk / PER_CHUNK, in = (kk % PER_CHUNK) * KB;
+                            const uint64_t qd = q_desc + (((part * C::CH + c) * C::Q_CHUNK + in) >> 4);
+                            const uint64_t d = kd + ((c * C::KV_CHUNK + in) >> 4);
+                            const uint32_t acc = kk > 0 || part > 0 ? 1u : 0u;
+                            if constexpr (FP8) mma_f8_ss(tmem + (t & 1) * kKeys, qd, d, idesc_s, acc);
+                            else mma_bf16_ss(tmem + (t & 1) * kKeys, qd, d, idesc_s, acc);
+                        }
+                    tc_commit(&s_full[t & 1]);
+                    tc_commit(&k_empty[s]);
+                    if (j == n - 1) tc_commit(q_empty);
+                    if (j > 0) issue_pv(t - 1, j == 1, k);
+                }
+                issue_pv(g + n - 1, n == 1, k);
+                g += n;
+            }
+            tc_commit(drain);   // never release TMEM or shared memory with MMAs in flight
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(drain, 0)) {
+                if (global_timer_ns() - t0 > kWaitLimitNs) {
+                    atomicOr(p.status, kStatusTimeout);
+                    break;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ----------------------------- softmax and epilogue -----------------------------
+        const int quad = warp & 3;                 // TMEM lane quadrant of this warp
+        const int row = quad * 32 + lane;          // row of the tile
+        const int tid = threadIdx.x - 64;          // 0 .. 127 over the softmax warps
+        const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
+        // A row's maximum moves only when it grows by more than `lag` (log2 units): O is then
+        // rescaled rarely.  bf16 holds any P; E4M3 holds 256 p <= 448 only.
+        constexpr float lag = FP8 ? 0.8f : 8.f;
+        constexpr float lift = FP8 ? 8.f : 0.f;    // P is 2^(x - m + lift)
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const int slot = k & 3;
+            ok = mbar_wait(&seg_full[slot], (k >> 2) & 1, p.status, abort_flag);
+            // the four warps leave the loop at the same barrier, after a wait that ran out too
+            if (named_barrier_or(1, 128, !ok)) break;
+            const TreeSegment w = queue->seg[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[slot]);
+            if (w.n < 0) break;
+            const int rows = w.n_nodes * a.group;
+            const bool busy = quad * 32 < rows;    // this warp has rows
+            const bool mine = row < rows;
+            const int node = w.node0 + (mine ? row / a.group : 0);
+            const int head = w.head * a.group + (mine ? row % a.group : 0);
+            const int ctx = w.L - w.T;
+            const uint64_t *mask = p.tree_mask + static_cast<int64_t>(w.row0 + node) * p.mask_words;
+            int low = 0;                           // first context token this row sees
+            if (p.window > 0) low = max(0, min(ctx, ctx + mask_count(mask, w.T) - p.window));
+            const int seen_by_all = p.window > 0 ? max(0, min(ctx, ctx + w.T - p.window)) : 0;
+            const int first_key = p.window > 0 ? max(0, ctx - p.window) : 0;
+            float scale = p.scale_log2;
+            if constexpr (FP8) {
+                // q's rows as E4M3 pairs, once the segment before has finished with Q
+                if (k > 0) ok = mbar_wait(q_empty, (k - 1) & 1, p.status, abort_flag);
+                ok = !__any_sync(kAll, !ok);
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(p.q) +
+                    (static_cast<int64_t>(w.row0 + node) * p.num_q_heads + head) * HD);
+                float most = 0.f;
+                if (mine) {
+#pragma unroll 4
+                    for (int c = 0; c < HD / 8; ++c) {
+                        float f[8];
+                        unpack_bf16x8(__ldg(src + c), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+                    }
+                }
+                // s: the power of two with most * s in [128, 256); an infinite row becomes NaN, as
+                // its scores are
+                const int ex = static_cast<int>(__float_as_uint(most) >> 23 & 0xff);
+                const float s = ex == 255 ? NAN : ex > 0 ? __uint_as_float(static_cast<uint32_t>(min(max(127 + 7 + 127 - ex, 1), 254)) << 23) : 1.f;
+                scale = p.scale_log2 * p.k_scale / s;
+                if (busy) {
+#pragma unroll 2
+                    for (int c = 0; c < HD / 16; ++c) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            float f[8];
+                            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                            if (mine) raw = __ldg(src + 2 * c + v);
+                            unpack_bf16x8(raw, f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t h[2], l[2];
+#pragma unroll
+                                for (int d = 0; d < 2; ++d) {
+                                    const float x = f[4 * e + 2 * d] * s, y = f[4 * e + 2 * d + 1] * s;
+                                    h[d] = float2_to_e4m3x2(x, y);
+                                    const float2 b = e4m3x2_to_float2(h[d]);
+                                    l[d] = float2_to_e4m3x2(x - b.x, y - b.y);
+                                }
+                                hi[2 * v + e] = h[0] | h[1] << 16;
+                                lo[2 * v + e] = l[0] | l[1] << 16;
+                            }
+                        }
+                        constexpr int UNITS = C::ROWB / 16;
+                        uint8_t *dst = smem + (c / UNITS) * C::Q_CHUNK + swizzled<C::ROWB>(row, c % UNITS);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(dst + C::CH * C::Q_CHUNK) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            float m = -INFINITY, l = 0.f;          // running maximum (log2 units) and sum
+            for (int j = 0; j < w.n && ok; ++j) {
+                const uint32_t t = g + j;
+                const uint32_t s_col = (t & 1) * kKeys;
+                ok = mbar_wait(&s_full[t & 1], (t >> 1) & 1, p.status, abort_flag);
+                if (__any_sync(kAll, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const int base = (w.j0 + j) * kKeys;
+                const uint32_t bad_pages = *static_cast<volatile uint32_t *>(&queue->bad_pages[t & 15]);
+                const bool edge = base + kKeys > ctx || base < seen_by_all || bad_pages;
+                if (edge && (base + kKeys > ctx || base < seen_by_all)) {
+                    // Clean V: rows that no row sees are zeroed (past the sequence, before the
+                    // window), partly seen ones lose and note what is not finite.
+                    const int s = t % C::STAGES;
+                    ok = mbar_wait(&v_full[s], (t / C::STAGES) & 1, p.status, abort_flag);
+                    if (__any_sync(kAll, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *vt = smem + C::OFF_V + s * C::KV_BYTES;
+                    for (int i = tid; i < static_cast<int>(C::KV_BYTES / 16); i += 128) {
+                        const int key = base + i % static_cast<int>(C::KV_CHUNK / 16) / (C::ROWB / 16);
+                        if (key >= seen_by_all && key < ctx) continue;
+                        uint4 *unit = reinterpret_cast<uint4 *>(vt) + i;
+                        if (key >= w.L || key < first_key) {
+                            *unit = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            uint4 v = *unit;
+                            if (drop_non_finite<FP8>(v)) {
+                                *unit = v;
+                                const int at = key >= ctx ? key - ctx : 256 + key - first_key;
+                                atomicOr(&queue->bad_nodes[at >> 5], 1u << (at & 31));
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (busy) {
+                    uint32_t sr[kKeys];
+                    tmem_load_64(tmem + t_lane + s_col, sr);
+                    if (edge) {
+                        uint64_t see = 0;
+                        if (mine) {
+                            see = (ones(ctx - base) & ~ones(low - base)) | mask_bits_at(mask, base - ctx, w.T);
+#pragma unroll
+                            for (int e = 0; e < kPages; ++e)
+                                if (bad_pages >> e & 1) see &= ~(0xffffull << e * kBlockSize);
+                        }
+                        const uint32_t see_lo = static_cast<uint32_t>(see), see_hi = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            if (!((c < 32 ? see_lo : see_hi) >> (c & 31) & 1)) sr[c] = __float_as_uint(-INFINITY);
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx[e] = fmaxf(__uint_as_float(sr[e]), __uint_as_float(sr[8 + e]));
+#pragma unroll
+                    for (int c = 16; c < kKeys; c += 16)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            mx[e] = fmax3(mx[e], __uint_as_float(sr[c + e]), __uint_as_float(sr[c + 8 + e]));
+                    const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                    const float m_new = fmaxf(m, top * scale);
+                    const bool grow = m_new > m + lag;
+                    const float corr = !grow ? 1.f : (m == -INFINITY ? 0.f : fast_exp2(m - m_new));
+                    if (j > 0 && __any_sync(kAll, grow)) {
+                        // O holds the tiles before: wait for the last P.V, then rescale in TMEM
+                        const uint32_t b = t - 1;
+                        ok = mbar_wait(&v_empty[b % C::STAGES], (b / C::STAGES) & 1, p.status, abort_flag);
+                        if (__any_sync(kAll, !ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_load_32(tmem + t_lane + C::TM_O + c * 32, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                            tmem_store_32(tmem + t_lane + C::TM_O + c * 32, o);
+                        }
+                        tmem_store_wait();
+                    }
+                    if (grow) {
+                        l *= corr;
+                        m = m_new;
+                    }
+                    // P = 2^(s scale - m + lift); the sum takes the unrounded values
+                    const float sub = m == -INFINITY ? 0.f : m - lift;
+                    uint32_t pk[32];
+                    float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                     make_float2(0.f, 0.f)};
+                    const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-sub, -sub);
+#pragma unroll
+                    for (int c = 0; c < kKeys / 2; ++c) {
+                        const float2 x = __ffma2_rn(
+                            make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2);
+                        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum[c & 3] = __fadd2_rn(sum[c & 3], e);
+                        if constexpr (FP8) {
+                            uint32_t hi, lo;
+                            split_e4m3x2(e.x, e.y, hi, lo);
+                            if (c & 1) {
+                                pk[c / 2] |= hi << 16;
+                                pk[16 + c / 2] |= lo << 16;
+                            } else {
+                                pk[c / 2] = hi;
+                                pk[16 + c / 2] = lo;
+                            }
+                        } else {
+                            pk[c] = pack_bf16x2(e.x, e.y);
+                        }
+                    }
+                    const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
+                    const float2 st = __fadd2_rn(s01, s23);
+                    l += st.x + st.y;
+                    tmem_store_32(tmem + t_lane + s_col, pk);
+                    tmem_store_wait();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t & 1]);
+            }
+            g += w.n;
+            // O is final once the segment's last P.V is done
+            ok = ok && mbar_wait(&v_empty[(g - 1) % C::STAGES], ((g - 1) / C::STAGES) & 1, p.status, abort_flag);
+            if (named_barrier_or(1, 128, !ok)) break;
+            tc_fence_after_sync();
+            const bool whole = w.slot < 0;
+            const float inv = l > 0.f ? p.v_scale / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
+                                 (static_cast<int64_t>(w.row0 + node) * p.num_q_heads + head) * HD;
+            float *part = a.part_o + (static_cast<int64_t>(max(w.slot, 0)) * a.slot_rows + row) * HD;
+            if (busy) {
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_load_32(tmem + t_lane + C::TM_O + c * 32, o);
+                    if (mine && whole) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4 *>(out + c * 32)[e] =
+                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    } else if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<uint4 *>(part + c * 32)[e] =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (mine && !whole) a.part_ml[static_cast<int64_t>(w.slot) * a.slot_rows + row] = make_float2(m, l);
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            // What the clean-up took out of V goes to the rows that see it (rare: a non-finite
+            // value in a drafted node's row).  P.V of every tile is done, so every warp has
+            // noted what it found.
+            uint32_t found = 0;
+            if (lane < 16) found = *static_cast<volatile uint32_t *>(&queue->bad_nodes[lane]);
+            if (__any_sync(kAll, found != 0)) {
+                if (mine) {
+                    for (int at = 0; at < 512; ++at) {
+                        if (!(*static_cast<volatile uint32_t *>(&queue->bad_nodes[at >> 5]) >> (at & 31) & 1)) continue;
+                        const int key = at < 256 ? ctx + at : first_key + at - 256;
+                        const bool see = at < 256 ? (mask_word(mask, at >> 6, w.T) >> (at & 63) & 1) : key >= low;
+                        if (!see) continue;
+                        const int page = p.block_tables[static_cast<int64_t>(w.b) * p.max_blocks + key / kBlockSize];
+                        const int64_t off = page * p.s_block + (w.head / a.kv_rep) * p.s_head +
+                                            (key % kBlockSize) * p.s_token;
+                        for (int d = 0; d < HD; ++d) {
+                            const float v = FP8 ? e4m3x2_to_float2(static_cast<const uint8_t *>(p.v_cache)[off + d]).x
+                                                : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v_cache)[off + d]);
+                            if (isfinite(v)) continue;
+                            if (whole) out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + v);
+                            else part[d] += v;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // the notes are the segment's own: all four warps have read them before they are cleared
+            const bool clear = named_barrier_or(1, 128, found != 0);
+            if (clear) {
+                if (tid < 16) queue->bad_nodes[tid] = 0;
+                named_barrier(1, 128);
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partial rows of every (sequence, kernel head group, row tile) that was cut: one
+// warp per row, the shares' partials in order, so the result does not depend on timing.
+// Grid: x = (sequence, head group, row tile), y = eight rows.
 template <int HD>
-cudaError_t launch_hd(const TreeParams &p, cudaStream_t stream) {
-    const dim3 grid(p.max_tree_len, (p.num_q_heads + 3) / 4, p.num_seqs);
-    if (p.kv_fp8) tree_kernel<HD, true><<<grid, 128, 0, stream>>>(p);
-    else tree_kernel<HD, false><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a, int shares_grid,
+                                                        int row_tiles_max) {
+    constexpr int D = HD / 32;
+    __shared__ int64_t pref[kMaxSeqs + 1];
+    const TreeParams &p = a.p;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tree_prefix<256>(a, pref, false);
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int rt = blockIdx.x % row_tiles_max;
+    const int head = blockIdx.x / row_tiles_max % a.heads;
+    const int b = blockIdx.x / row_tiles_max / a.heads;
+    const TreeSeq s = tree_seq(p, b, false);
+    const int row_tiles = (s.T + a.nodes - 1) / a.nodes;
+    if (rt >= row_tiles) return;
+    const int n_nodes = min(a.nodes, s.T - rt * a.nodes);
+    if (row >= n_nodes * a.group) return;
+    const int64_t total = pref[p.num_seqs];
+    const int shares = tree_shares(a, total, shares_grid);
+    const int tiles = tree_tiles(s, p.window);
+    const int64_t begin = pref[b] + (static_cast<int64_t>(head) * row_tiles + rt) * tiles, end = begin + tiles;
+    int c = static_cast<int>(begin * shares / total);
+    while (tree_share_begin(total, shares, c + 1) <= begin) ++c;
+    while (tree_share_begin(total, shares, c) > begin) --c;
+    if (tree_share_begin(total, shares, c + 1) >= end) return;   // whole: already written
+    float m = -INFINITY, l = 0.f, acc[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] = 0.f;
+    // the run begins in share c (its slot 1) and goes on in the next ones (their slot 0)
+    for (int slot = 2 * c + 1;;) {
+        const int64_t at = static_cast<int64_t>(slot) * a.slot_rows + row;
+        const float2 ml = a.part_ml[at];
+        float o[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] = a.part_o[at * HD + d * 32 + lane];
+        const float top = fmaxf(m, ml.x);
+        if (top != -INFINITY) {
+            const float fa = m == -INFINITY ? 0.f : exp2f(m - top), fb = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            l = l * fa + ml.y * fb;
+#pragma unroll
+            for (int d = 0; d < D; ++d) acc[d] = acc[d] * fa + o[d] * fb;
+            m = top;
+        }
+        ++c;
+        if (tree_share_begin(total, shares, c) >= end) break;
+        slot = 2 * c;
+    }
+    const int node = rt * a.nodes + row / a.group, h = head * a.group + row % a.group;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
+                         (static_cast<int64_t>(s.row0 + node) * p.num_q_heads + h) * HD;
+    const float inv = l > 0.f ? p.v_scale / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+    for (int d = 0; d < D; ++d) out[d * 32 + lane] = __float2bfloat16_rn(acc[d] * inv);
+}
+
+// ---- host side ------------------------------------------------------------------------------
+
+// The kernel's groups of query heads: the whole group of a kv head, or its largest divisor
+// that fits the row tile.
+int tree_group(int num_q_heads, int num_kv_heads) {
+    const int G = num_q_heads / num_kv_heads;
+    int g = G < kRows ? G : kRows;
+    while (G % g) --g;
+    return g;
+}
+
+int tree_nodes(int group, int max_tree_len) {
+    const int n = kRows / group;
+    return n < max_tree_len ? n : max_tree_len;
+}
+
+template <int HD, bool FP8>
+cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
+    using C = TreeCfg<HD, FP8>;
+    const TreeParams &p = a.p;
+    if (!FP8) {
+        const cuuint64_t dims[3] = {HD, static_cast<cuuint64_t>(p.num_q_heads),
+                                    static_cast<cuuint64_t>(p.total_rows)};
+        const cuuint64_t str[2] = {HD * 2, static_cast<cuuint64_t>(p.num_q_heads) * HD * 2};
+        const cuuint32_t box[3] = {C::COLS, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(a.nodes)};
+        if (!encode_tensor_map_bf16(&a.tm_q, p.q, 3, dims, str, box)) return cudaErrorInvalidValue;
+    }
+    {
+        constexpr int E = FP8 ? 1 : 2;
+        const cuuint64_t dims[4] = {HD, kBlockSize, static_cast<cuuint64_t>(p.num_kv_heads),
+                                    static_cast<cuuint64_t>(p.num_blocks)};
+        const cuuint64_t str[3] = {static_cast<cuuint64_t>(p.s_token) * E, static_cast<cuuint64_t>(p.s_head) * E,
+                                   static_cast<cuuint64_t>(p.s_block) * E};
+        const cuuint32_t box[4] = {C::COLS, kBlockSize, 1, 1};
+        auto encode = FP8 ? encode_tensor_map_u8 : encode_tensor_map_bf16;
+        if (!encode(&a.tm_k, p.k_cache, 4, dims, str, box) || !encode(&a.tm_v, p.v_cache, 4, dims, str, box))
+            return cudaErrorInvalidValue;
+    }
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    auto kern = tree_kernel<HD, FP8>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than the longest possible line has tiles
+    const int row_tiles = (p.max_tree_len + a.nodes - 1) / a.nodes;
+    const int64_t line = static_cast<int64_t>(p.num_seqs) * a.heads * row_tiles *
+                         ((static_cast<int64_t>(p.max_blocks) * kBlockSize + kKeys - 1) / kKeys);
+    int grid = sms * C::CTAS_PER_SM < kMaxCtas ? sms * C::CTAS_PER_SM : kMaxCtas;
+    if (line < grid) grid = static_cast<int>(line);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs * a.heads * row_tiles),
+                       static_cast<unsigned>((a.slot_rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a, grid, row_tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t stream) {
-    switch (head_dim) {
-        case 64: return launch_hd<64>(p, stream);
-        case 128: return launch_hd<128>(p, stream);
-        case 256: return launch_hd<256>(p, stream);
-        default: return cudaErrorNotSupported;
+    TreeLaunch a = {};
+    a.group = tree_group(p.num_q_heads, p.num_kv_heads);
+    a.kv_rep = p.num_q_heads / p.num_kv_heads / a.group;
+    a.heads = p.num_q_heads / a.group;
+    a.nodes = tree_nodes(a.group, p.max_tree_len);
+    a.slot_rows = a.nodes * a.group;
+    a.min_tiles = 1;
+    const size_t slots = 2 * kMaxCtas;
+    a.part_o = static_cast<float *>(p.workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots * a.slot_rows * head_dim);
+    // the line's prefix holds kMaxSeqs sequences: more go in several launches, one after another
+    for (int at = 0; at < p.num_seqs; at += kMaxSeqs) {
+        a.p = p;
+        a.p.num_seqs = p.num_seqs - at < kMaxSeqs ? p.num_seqs - at : kMaxSeqs;
+        a.p.seq_lens = p.seq_lens + at;
+        a.p.qo_indptr = p.qo_indptr + at;
+        a.p.block_tables = p.block_tables + static_cast<int64_t>(at) * p.max_blocks;
+        cudaError_t e;
+        switch (head_dim) {
+            case 64: e = p.kv_fp8 ? launch_tree<64, true>(a, stream) : launch_tree<64, false>(a, stream); break;
+            case 128: e = p.kv_fp8 ? launch_tree<128, true>(a, stream) : launch_tree<128, false>(a, stream); break;
+            case 256: e = p.kv_fp8 ? launch_tree<256, true>(a, stream) : launch_tree<256, false>(a, stream); break;
+            default: return cudaErrorNotSupported;
+        }
+        if (e != cudaSuccess) return e;
     }
+    return cudaSuccess;
 }
 
 }  // namespace pa
 
 extern "C" size_t pa_tree_decode_workspace_size(int num_seqs, int max_tree_len, int num_q_heads,
                                                 int num_kv_heads, int head_dim) {
-    (void)num_seqs, (void)max_tree_len, (void)num_q_heads, (void)num_kv_heads, (void)head_dim;
-    return 256;
+    if (num_seqs <= 0 || max_tree_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        num_q_heads % num_kv_heads)
+        return 0;
+    const int group = pa::tree_group(num_q_heads, num_kv_heads);
+    const size_t rows = static_cast<size_t>(2 * pa::kMaxCtas) * pa::tree_nodes(group, max_tree_len) * group;
+    return rows * (static_cast<size_t>(head_dim) * 4 + 8);
 }
 
 extern "C" int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
