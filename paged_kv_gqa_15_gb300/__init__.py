@@ -170,10 +170,7 @@ def _page_geometry(pools):
 
 
 def _pointer_array(tensors):
-    arr = (ctypes.c_void_p * max(1, len(tensors)))()
-    for i, t in enumerate(tensors):
-        arr[i] = t.data_ptr()
-    return arr
+    return (ctypes.c_void_p * max(1, len(tensors)))(*[t.data_ptr() for t in tensors])
 
 
 def pa_copy_blocks(key_caches, value_caches, block_mapping, stream=None):
@@ -390,9 +387,8 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
     pools = [t for kv in zip(key_caches, value_caches) for t in kv]
     nb, nkv, bs, hd = _pool_geometry(pools[0], layout)
     sb, sh, st = pool_strides(pools[0], layout)
-    for t in pools:
-        assert t.shape == pools[0].shape and t.stride() == pools[0].stride() and \
-            t.dtype == pools[0].dtype, "pools differ in geometry"
+    first = (pools[0].shape, pools[0].stride(), pools[0].dtype)
+    assert all([(t.shape, t.stride(), t.dtype) == first for t in pools]), "pools differ in geometry"
     assert accepted.dtype == torch.int32 and accepted.is_contiguous()
     _check(load().pa_tree_commit(_pointer_array(pools), len(pools), _ptr(block_tables),
                                  _ptr(seq_lens), _ptr(qo_indptr), _ptr(accepted),

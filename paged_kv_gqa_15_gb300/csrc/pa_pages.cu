@@ -10,9 +10,10 @@
 // than one head, and the pass is bound by reading the bounds (2 head_dim elements a page).
 //
 // Selection is by exact scores.  A score computed in fp32 is off by at most
-//     E = (group + 16) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
-// (P and N are sums of `group` terms, a lane adds 16 products at most and five shuffles join
-// the lanes: fewer than group + 16 ... roundings act on any product).  With T the f-th
+//     E = (group + 24) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
+// (P and N are sums of `group` terms; a product is rounded, added in a chain of four, joined
+// by three more sums in the lane and five across lanes; S itself is as far off and T +- 2E
+// is rounded: fewer than group + 24 roundings act on any term).  With T the f-th
 // largest computed score, a page above T + 2E is among the f best and one below T - 2E is
 // not; the band between is scored again in fp64 and ranked by (score, page).
 #include "../../include/pa.h"
@@ -146,7 +147,7 @@ cudaError_t launch_bounds(const BoundsParams &p, bool fp8, cudaStream_t stream) 
 
 // ---- scores ---------------------------------------------------------------------------------
 
-constexpr int kScorePages = 64;   // pages per CTA of the score kernel
+constexpr int kLeastChunk = 64;   // fewest pages per CTA
 
 struct SelectParams {
     int32_t *page_tables, *page_lens;
@@ -158,7 +159,7 @@ struct SelectParams {
     int32_t *band;      // [B][nkv][max_blocks]
     double *exact;      // [B][nkv][max_blocks]
     int64_t num_blocks;
-    int num_seqs, nq, nkv, max_blocks, chunks, max_pages, sink, recent;
+    int num_seqs, nq, nkv, max_blocks, chunk, chunks, max_pages, sink, recent;   // chunk: pages per CTA
     int *status;
 };
 
@@ -191,62 +192,152 @@ __device__ __forceinline__ float bound_value(const uint8_t *row, int d) {
     else return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[d]);
 }
 
-// Grid (chunk, kv head, sequence); a warp per page.  Lane l holds channels l * HD / 32 on of
-// P and N.
+// The 8 bf16 or 16 E4M3 values of 16 bytes.
+template <bool FP8>
+__device__ __forceinline__ void unpack16(const uint4 &raw, float (&f)[FP8 ? 16 : 8]) {
+    if constexpr (FP8) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = e4m3x2_to_float2(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    } else {
+        unpack_bf16x8(raw, f);
+    }
+}
+
+// Grid (chunk, kv head, sequence), an eighth of the chunk's pages (at most 32) per warp.  A
+// page's bounds (min row, then max row) are UNITS units of 16 bytes, so a warp reads
+// 32 / UNITS pages with one load instruction (at head_dim 256 in bf16 a page takes two).
+// Everything that does not wait for something else is issued first: the page ids (one per
+// lane, one load), then kLoads groups of bounds, and only then the query heads, whose sums
+// go through shared memory; the next groups are loaded while the last are multiplied.  The
+// pass reads 2 head_dim elements a page and multiplies each once, so streaming them is its
+// bound.
 template <int HD, bool FP8>
-__global__ void __launch_bounds__(256) score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int ROW = HD * (FP8 ? 1 : 2), D = HD / 32;
+__global__ void __launch_bounds__(256, 2) score_kernel(const __grid_constant__ SelectParams p) {
+    constexpr int PAGE = 2 * HD * (FP8 ? 1 : 2);
+    constexpr int UNITS = PAGE / 16;
+    constexpr int LANES = UNITS < 32 ? UNITS : 32;
+    constexpr int PARTS = UNITS / LANES;          // loads per page
+    constexpr int PER = 32 / LANES;               // pages per load
+    constexpr int E = FP8 ? 16 : 8;               // elements of a unit
+    constexpr int kLoads = 8 / PARTS;             // page groups in flight
+    constexpr int STEP = kLoads * PER;            // pages of a step
+    __shared__ __align__(16) float weight[2 * HD];              // N, then P: in the order of a page's rows
     __shared__ float span[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.z, kh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = select_len(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
     const int np = (L + kBlockSize - 1) / kBlockSize;
-    const int first = blockIdx.x * kScorePages;
-    if (np <= p.max_pages || first >= np) return;
-    const int g = p.nq / p.nkv;
-    float P[D], N[D];
-    for (int d = 0; d < D; ++d) P[d] = N[d] = 0.f;
-    for (int h = 0; h < g; ++h)
-        for (int d = 0; d < D; ++d) {
-            const float x = __bfloat162float(
-                p.q[(static_cast<int64_t>(b) * p.nq + kh * g + h) * HD + lane * D + d]);
-            P[d] += x >= 0.f || isnan(x) ? x : 0.f;
-            N[d] += x < 0.f ? x : 0.f;
-        }
+    if (np <= p.max_pages || static_cast<int>(blockIdx.x) * p.chunk >= np) return;
+    const int each = p.chunk / 8;
+    const int first = blockIdx.x * p.chunk + warp * each;
+    const int n = min(each, np - first);          // may be negative
     const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
+    const int id = lane < n ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + first + lane] : 0;
+    const bool known = id >= 0 && id < p.num_blocks;
+    if (!known) atomicOr(p.status, kStatusBounds);
+    const unsigned unknown = __ballot_sync(kAll, !known);
+    const int page = known ? id : 0;
+    const int unit = lane % LANES, sub = lane / LANES;
+    uint4 raw[kLoads][PARTS];
+    auto load = [&](int at) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int i = at + k * PER + sub;
+            const int64_t pg = __shfl_sync(kAll, page, i & 31);
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (pg * p.nkv + kh) * PAGE) + unit;
+#pragma unroll
+            for (int v = 0; v < PARTS; ++v) raw[k][v] = i < n ? __ldg(src + v * LANES) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    load(0);
+    const int g = p.nq / p.nkv;
+    for (int d = threadIdx.x; d < HD; d += 256) {
+        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
+        float lo = 0.f, hi = 0.f;
+#pragma unroll 8
+        for (int h = 0; h < g; ++h) {
+            const float x = __bfloat162float(q[h * HD]);
+            lo += x < 0.f ? x : 0.f;
+            hi += x < 0.f ? 0.f : x;              // a NaN goes to P
+        }
+        weight[d] = lo;
+        weight[HD + d] = hi;
+    }
+    __syncthreads();
+    float w[PARTS][E];
+#pragma unroll
+    for (int v = 0; v < PARTS; ++v)
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&weight[(v * LANES + unit) * E + e]);
+            w[v][e] = x.x, w[v][e + 1] = x.y, w[v][e + 2] = x.z, w[v][e + 3] = x.w;
+        }
     float most = 0.f;
-    for (int i = first + warp; i < min(first + kScorePages, np); i += 8) {
-        const int id = p.block_tables[static_cast<int64_t>(b) * p.max_blocks + i];
-        float s = 0.f, a = 0.f;
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) atomicOr(p.status, kStatusBounds);
-            s = -INFINITY;
-        } else {
-            const uint8_t *lo = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
-            for (int d = 0; d < D; ++d) {
-                const float x = weighed(P[d], bound_value<FP8>(lo + ROW, lane * D + d));
-                const float y = weighed(N[d], bound_value<FP8>(lo, lane * D + d));
-                s += x + y;
-                a += fabsf(x) + fabsf(y);
+    for (int at = 0; at < n; at += STEP) {
+        float s[kLoads], a[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            s[k] = a[k] = 0.f;
+#pragma unroll
+            for (int v = 0; v < PARTS; ++v) {
+                float f[E];
+                unpack16<FP8>(raw[k][v], f);
+                // four chains of E / 4 products each
+                float c[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float x = w[v][e] * f[e];
+                    c[e & 3] += x;
+                    t[e & 3] += fabsf(x);
+                }
+                s[k] += (c[0] + c[1]) + (c[2] + c[3]);
+                a[k] += (t[0] + t[1]) + (t[2] + t[3]);
             }
-            for (int o = 16; o; o >>= 1) {
-                s += __shfl_xor_sync(kAll, s, o);
-                a += __shfl_xor_sync(kAll, a, o);
+            if (a[k] != a[k]) {   // a zero weight met an infinity, or there is a NaN: the exact rule
+                s[k] = a[k] = 0.f;
+#pragma unroll
+                for (int v = 0; v < PARTS; ++v) {
+                    float f[E];
+                    unpack16<FP8>(raw[k][v], f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float x = weighed(w[v][e], f[e]);
+                        s[k] += x;
+                        a[k] += fabsf(x);
+                    }
+                }
             }
         }
-        most = max_nan(most, a);
-        if (lane == 0) p.score[row * p.max_blocks + i] = s;
+        if (at + STEP < n) load(at + STEP);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+#pragma unroll
+            for (int o = LANES / 2; o; o >>= 1) {
+                s[k] += __shfl_xor_sync(kAll, s[k], o);
+                a[k] += __shfl_xor_sync(kAll, a[k], o);
+            }
+            const int i = at + k * PER + sub;
+            most = max_nan(most, a[k]);
+            if (unit == 0 && i < n) p.score[row * p.max_blocks + first + i] = unknown >> i & 1 ? -INFINITY : s[k];
+        }
     }
+#pragma unroll
+    for (int o = 16; o >= LANES; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
     if (lane == 0) span[warp] = most;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) most = max_nan(most, span[w]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) most = max_nan(most, span[i]);
         p.span[row * p.chunks + blockIdx.x] = most;
     }
 }
 
 // ---- selection ------------------------------------------------------------------------------
-
-constexpr int kSelThreads = 1024;
 
 // Order-preserving whole numbers of floating scores; a NaN is the largest.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -261,8 +352,46 @@ __device__ __forceinline__ uint64_t key_of(double x) {
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-// Exclusive prefix of x over the CTA, and the total.
-__device__ __forceinline__ int block_scan(int x, int *warps, int &total) {
+// Sums of three counts over the CTA's NT threads; sh holds two halves, used in turn.
+template <int NT>
+struct BlockSums {
+    static constexpr int W = NT / 32;
+    int *sh;   // [2][3][32]
+    int turn;
+    __device__ __forceinline__ void operator()(int (&x)[3]) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        int *at = sh + turn * 96;
+        turn ^= 1;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int v = __reduce_add_sync(kAll, x[i]);
+            if (lane == 0) at[i * 32 + warp] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) x[i] = __reduce_add_sync(kAll, lane < W ? at[i * 32 + lane] : 0);
+    }
+};
+
+// The f-th largest (f >= 1) of the keys that count(t, c) counts (c += this thread's keys that
+// are >= t): the largest t with at least f keys >= t, found two bits at a time below `shift`;
+// `t` holds the bits from `shift` on, which the f-th largest is known to have.
+template <typename Key, typename Sums, typename Count>
+__device__ __forceinline__ Key nth_largest(Key t, int shift, int f, Sums &sums, Count count) {
+    for (shift -= 2; shift >= 0; shift -= 2) {
+        int c[3] = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) count(static_cast<Key>(t | static_cast<Key>(i + 1) << shift), c[i]);
+        sums(c);
+        const int digit = c[2] >= f ? 3 : (c[1] >= f ? 2 : (c[0] >= f ? 1 : 0));
+        t |= static_cast<Key>(digit) << shift;
+    }
+    return t;
+}
+
+// Exclusive prefix of x over the CTA's NT threads.
+template <int NT>
+__device__ __forceinline__ int block_scan(int x, int *warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int v = x;
 #pragma unroll
@@ -270,57 +399,28 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int &total) {
         const int u = __shfl_up_sync(kAll, v, o);
         if (lane >= o) v += u;
     }
+    __syncthreads();
     if (lane == 31) warps[warp] = v;
     __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += warps[w];
-        total += warps[w];
-    }
-    __syncthreads();
-    return before + v - x;
+    return __reduce_add_sync(kAll, lane < warp ? warps[lane] : 0) + v - x;
 }
 
-// The f-th largest (f >= 1) of n keys, and how many exceed it: radix select, a byte a pass.
-template <typename Key, typename Get>
-__device__ __forceinline__ Key nth_largest(int n, int f, int *hist, Get get, int &greater) {
-    __shared__ int pick[2];
-    Key prefix = 0;
-    int above = 0;
-    for (int shift = static_cast<int>(sizeof(Key)) * 8 - 8; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kSelThreads) {
-            const Key k = get(i);
-            const bool in = shift + 8 >= static_cast<int>(sizeof(Key)) * 8 ||
-                            (k >> (shift + 8)) == (prefix >> (shift + 8));
-            if (in) atomicAdd(&hist[static_cast<int>(k >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int c = above, d = 255;
-            while (d > 0 && c + hist[d] < f) c += hist[d--];
-            pick[0] = d;
-            pick[1] = c;
-        }
-        __syncthreads();
-        prefix |= static_cast<Key>(pick[0]) << shift;
-        above = pick[1];
-        __syncthreads();
-    }
-    greater = above;
-    return prefix;
-}
-
-// One CTA per (kv head, sequence).
-template <int HD, bool FP8>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p) {
+// One CTA per (kv head, sequence).  Thread t owns the K consecutive pages from t K on, so that
+// one scan over the threads gives every chosen page its place; their scores stay in
+// registers (K > 0, up to NT K pages) or are read again from the workspace (K = 0).  The
+// border score is found by counting, two bits a step and below the bits that all
+// candidates share: one barrier a step, no histogram and no atomics.
+template <int HD, bool FP8, int NT, int K>
+__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
-    __shared__ int hist[256];
-    __shared__ int warps[kSelThreads / 32];
-    __shared__ float span_sh;
+    constexpr int W = NT / 32;
+    constexpr int kSmallBand = 32;
+    __shared__ int sums_sh[2 * 3 * 32];
+    __shared__ int warps[32];
+    __shared__ uint32_t ends[2][32];
     __shared__ double P[HD], N[HD];
+    __shared__ uint64_t small_key[kSmallBand];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = select_len(p, b, false);
     const int np = (L + kBlockSize - 1) / kBlockSize;
@@ -329,58 +429,98 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
     int32_t *out = p.page_tables + row * p.max_pages;
     if (kh == 0 && tid == 0) p.page_lens[b] = kept * kBlockSize - (np * kBlockSize - L);
-    for (int i = kept + tid; i < p.max_pages; i += kSelThreads) out[i] = -1;
+    for (int i = kept + tid; i < p.max_pages; i += NT) out[i] = -1;
     if (np <= p.max_pages) {
-        for (int i = tid; i < np; i += kSelThreads) out[i] = bt[i];
+        for (int i = tid; i < np; i += NT) out[i] = bt[i];
         return;
     }
     // f pages of [lo, hi) join the sinks and the newest ones
     const int lo = p.sink, hi = np - p.recent, f = p.max_pages - p.sink - p.recent;
     const float *score = p.score + row * p.max_blocks;
+    const int per = K > 0 ? K : (np + NT - 1) / NT;
+    const int mine = tid * per;
+    uint32_t key[K > 0 ? K : 1];                // 0 for pages that are not candidates
+    if constexpr (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            key[i] = mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
+    }
+    auto key_at = [&](int i) -> uint32_t {      // of page mine + i
+        if constexpr (K > 0) return key[i];
+        else return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
+    };
+    BlockSums<NT> sums{sums_sh, 0};
+    // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
+    uint32_t above = 0xffffffffu, below = 0xffffffffu;
+    bool all = true;                            // the whole band wins
+    uint64_t edge = 0;                          // else the weakest exact score that wins ...
+    int ties = 0;                               // ... and how many equal to it do
+    int band_at = 0, n_band = 0;                // band members before this thread's, and in all
     int32_t *band = p.band + row * p.max_blocks;
     double *exact = p.exact + row * p.max_blocks;
-    float above = INFINITY, below = INFINITY;   // sure winners exceed `above`, losers miss `below`
-    int take = 0;                               // winners that come from the band
-    uint64_t edge = 0;                          // the band's weakest winner ...
-    int ties = 0;                               // ... and how many equal to it win
-    bool all = true;                            // the whole band wins
     if (f > 0) {
-        int greater;
-        const uint32_t t =
-            nth_largest<uint32_t>(hi - lo, f, hist, [&](int i) { return key_of(score[lo + i]); }, greater);
-        if (tid == 0) {
-            float s = 0.f;
-            for (int i = 0; i < (np + kScorePages - 1) / kScorePages; ++i)
-                s = max_nan(s, p.span[row * p.chunks + i]);
-            span_sh = s;
+        uint32_t least = 0xffffffffu, top = 0u;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const uint32_t k = key_at(i);
+            if (k) least = min(least, k), top = max(top, k);
         }
+        least = __reduce_min_sync(kAll, least);
+        top = __reduce_max_sync(kAll, top);
+        if (lane == 0) ends[0][warp] = least, ends[1][warp] = top;
         __syncthreads();
+        least = __reduce_min_sync(kAll, lane < W ? ends[0][lane] : 0xffffffffu);
+        top = __reduce_max_sync(kAll, lane < W ? ends[1][lane] : 0u);
+        const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
+        const uint32_t t = nth_largest<uint32_t>(
+            bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
+                if constexpr (K > 0) {
+#pragma unroll
+                    for (int i = 0; i < K; ++i) c += key[i] >= x;
+                } else {
+                    for (int i = 0; i < per; ++i) c += key_at(i) >= x;
+                }
+            });
+        float s = 0.f;
+        for (int i = lane; i < (np + p.chunk - 1) / p.chunk; i += 32) s = max_nan(s, p.span[row * p.chunks + i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s = max_nan(s, __shfl_xor_sync(kAll, s, o));
         const float T = t == 0xffffffffu ? NAN
                                          : __uint_as_float(t & 0x80000000u ? t & 0x7fffffffu : ~t);
-        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 16) * 0x1p-24f * span_sh;
-        above = T + E2;
-        below = T - E2;
-        // the band in page order
-        int n_band = 0, n_above = 0;
-        for (int base = lo; base < hi; base += kSelThreads) {
-            const int i = base + tid;
-            const float s = i < hi ? score[i] : 0.f;
-            const bool win = i < hi && s > above, in = i < hi && !win && !(s < below);
-            int total;
-            const int at = block_scan((in ? 1 : 0) | (win ? 1 << 16 : 0), warps, total);
-            if (in) band[n_band + (at & 0xffff)] = i;
-            n_band += total & 0xffff;
-            n_above += total >> 16;
+        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 24) * 0x1p-24f * s;
+        if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
+            above = key_of(T + E2);
+            below = key_of(T - E2);
+        } else {
+            below = 1u;
         }
-        take = f - n_above;
+        int c[3] = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const uint32_t k = key_at(i);
+            c[0] += k > above;
+            c[1] += k >= below && k <= above;
+        }
+        const int in = c[1];
+        sums(c);
+        const int take = f - c[0];               // winners that come from the band
+        n_band = c[1];
         all = take == n_band;
         if (!all) {
+            band_at = block_scan<NT>(in, warps);
+            int to = band_at;
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const uint32_t k = key_at(i);
+                if (k >= below && k <= above) band[to++] = mine + i;
+            }
             const int g = p.nq / p.nkv;
-            for (int d = tid; d < HD; d += kSelThreads) {
+            for (int d = tid; d < HD; d += NT) {
+                const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
                 double x = 0.0, y = 0.0;
+#pragma unroll 8
                 for (int h = 0; h < g; ++h) {
-                    const float v = __bfloat162float(
-                        p.q[(static_cast<int64_t>(b) * p.nq + kh * g + h) * HD + d]);
+                    const float v = __bfloat162float(q[h * HD]);
                     if (v < 0.f) y += v;
                     else x += v;
                 }
@@ -388,64 +528,111 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
                 N[d] = y;
             }
             __syncthreads();
-            for (int i = warp; i < n_band; i += kSelThreads / 32) {
+            for (int i = warp; i < n_band; i += W) {
                 const int id = bt[band[i]];
-                double s = 0.0;
+                double e = -INFINITY;
                 if (id >= 0 && id < p.num_blocks) {
+                    e = 0.0;
                     const uint8_t *r = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
-                    for (int d = lane; d < HD; d += 32)
-                        s += weighed<double>(P[d], bound_value<FP8>(r + ROW, d)) +
-                             weighed<double>(N[d], bound_value<FP8>(r, d));
-                    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-                } else {
-                    s = -INFINITY;
+#pragma unroll
+                    for (int d = 0; d < HD; d += 32)
+                        e += weighed<double>(P[d + lane], bound_value<FP8>(r + ROW, d + lane)) +
+                             weighed<double>(N[d + lane], bound_value<FP8>(r, d + lane));
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(kAll, e, o);
                 }
-                if (lane == 0) exact[i] = s;
+                if (lane == 0) {
+                    if (n_band <= kSmallBand) small_key[i] = key_of(e);
+                    else exact[i] = e;
+                }
             }
             __syncthreads();
-            int more;
-            edge = nth_largest<uint64_t>(n_band, take, hist, [&](int i) { return key_of(exact[i]); }, more);
-            ties = take - more;
+            if (n_band <= kSmallBand) {
+                // the take-th of the band in the order (score, lower page first): a member's
+                // place is the number of those before it
+                const uint64_t k = lane < n_band ? small_key[lane] : 0ull;
+                int place = 0;
+                for (int i = 0; i < n_band; ++i) {
+                    const uint64_t o = small_key[i];
+                    place += o > k || (o == k && i < lane);
+                }
+                const int who = __ffs(__ballot_sync(kAll, lane < n_band && place == take - 1)) - 1;
+                edge = small_key[who];
+                ties = take - __popc(__ballot_sync(kAll, lane < n_band && k > edge));
+            } else {
+                edge = nth_largest<uint64_t>(0ull, 64, take, sums, [&](uint64_t x, int &n) {
+                    for (int i = tid; i < n_band; i += NT) n += key_of(exact[i]) >= x;
+                });
+                int n[3] = {0, 0, 0};
+                for (int i = tid; i < n_band; i += NT) n[0] += key_of(exact[i]) > edge;
+                sums(n);
+                ties = take - n[0];
+            }
         }
     }
-    // the chosen pages in order
-    int n_out = 0, n_band = 0, n_tie = 0;
-    for (int base = 0; base < np; base += kSelThreads) {
-        const int i = base + tid;
-        const bool held = i < np && (i < lo || i >= hi);
-        bool win = held, in = false;
-        if (i < np && !held && f > 0) {
-            const float s = score[i];
-            win = s > above;
-            in = !win && !(s < below);
+    auto exact_key = [&](int i) -> uint64_t { return n_band <= kSmallBand ? small_key[i] : key_of(exact[i]); };
+    // Which of a thread's pages win, in order; a tie at the edge goes to the lower pages.
+    int tie_at = 0;
+    if (!all) {
+        int n = 0, at = band_at;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const uint32_t k = key_at(i);
+            if (k >= below && k <= above) n += exact_key(at++) == edge;
         }
-        int total;
-        const int at = block_scan(in ? 1 : 0, warps, total);
-        bool tie = false;
-        if (in) {
-            const uint64_t k = all ? 1 : key_of(exact[n_band + at]);
-            win = all || k > edge;
-            tie = !all && k == edge;
-        }
-        n_band += total;
-        const int nth = block_scan(tie ? 1 : 0, warps, total);
-        if (tie && n_tie + nth < ties) win = true;
-        n_tie += total;
-        const int to = block_scan(win ? 1 : 0, warps, total);
-        if (win) out[n_out + to] = bt[i];
-        n_out += total;
+        tie_at = block_scan<NT>(n, warps);
     }
+    auto walk = [&](auto emit) {
+        int at = band_at, tie = tie_at;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const int page = mine + i;
+            const uint32_t k = key_at(i);
+            bool win = page < np && (page < lo || page >= hi);
+            if (!win && f > 0 && k > above) win = true;
+            if (!win && f > 0 && k >= below && k <= above) {
+                win = all;
+                if (!all) {
+                    const uint64_t e = exact_key(at++);
+                    win = e > edge || (e == edge && tie++ < ties);
+                }
+            }
+            if (win) emit(page);
+        }
+    };
+    int n = 0;
+    walk([&](int) { ++n; });
+    int to = block_scan<NT>(n, warps);
+    walk([&](int page) { out[to++] = bt[page]; });
+}
+
+// Launches a kernel as a programmatic dependent of the work before it in the stream.
+template <typename Kernel>
+cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int HD, bool FP8>
 cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
     if (p.max_blocks > p.max_pages) {
-        score_kernel<HD, FP8><<<dim3(p.chunks, p.nkv, p.num_seqs), 256, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_after(score_kernel<HD, FP8>, dim3(p.chunks, p.nkv, p.num_seqs), 256, p, stream);
         if (e != cudaSuccess) return e;
     }
-    select_kernel<HD, FP8><<<dim3(p.nkv, p.num_seqs), kSelThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    // as many threads as a table's pages need at 8 a thread; past 8192 pages (131072 tokens) the
+    // scores no longer fit the registers
+    const dim3 grid(p.nkv, p.num_seqs);
+    if (p.max_blocks <= 2048) return launch_after(select_kernel<HD, FP8, 256, 8>, grid, 256, p, stream);
+    if (p.max_blocks <= 8192) return launch_after(select_kernel<HD, FP8, 1024, 8>, grid, 1024, p, stream);
+    return launch_after(select_kernel<HD, FP8, 1024, 0>, grid, 1024, p, stream);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -456,7 +643,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t select_layout(int num_seqs, int nkv, int max_blocks, size_t off[4]) {
     const size_t rows = static_cast<size_t>(num_seqs > 0 ? num_seqs : 0) * (nkv > 0 ? nkv : 0);
     const size_t n = rows * (max_blocks > 0 ? max_blocks : 0);
-    const size_t chunks = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kScorePages - 1) / kScorePages;
+    const size_t chunks = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kLeastChunk - 1) / kLeastChunk;
     off[0] = 0;
     off[1] = off[0] + round256(n * 4);
     off[2] = off[1] + round256(rows * chunks * 4);
@@ -583,7 +770,12 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     p.nq = num_q_heads;
     p.nkv = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
-    p.chunks = (max_blocks_per_seq + kScorePages - 1) / kScorePages;
+    // Pages per CTA of the score pass: 64 (one round of loads at head_dim 128 in bf16) while
+    // that gives the GPU's 152 SMs fewer than 16 CTAs each, else 256.
+    p.chunk = kLeastChunk;
+    if (static_cast<int64_t>(num_seqs) * num_kv_heads * (max_blocks_per_seq / kLeastChunk) > 16 * 152)
+        p.chunk = 4 * kLeastChunk;
+    p.chunks = (max_blocks_per_seq + p.chunk - 1) / p.chunk;
     p.max_pages = max_pages;
     p.sink = sink_pages;
     p.recent = recent_pages;

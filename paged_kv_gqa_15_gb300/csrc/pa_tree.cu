@@ -86,11 +86,19 @@ struct TreeCfg {
     static_assert(CTAS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
 };
 
+// A run of tiles that was cut, as the share of its second piece notes it (pieces = 0: none).
+struct TreeCut {
+    int pieces;        // shares it lies in, from the one before on
+    int rows, head;    // rows of its row tile, kernel head group
+    int node0;         // first row of q and out
+};
+
 struct TreeLaunch {
     CUtensorMap tm_q, tm_k, tm_v;   // q only for bf16 caches (FP8 splits q itself)
     TreeParams p;
     float *part_o;                  // [2 grid][rows][HD], unnormalised
     float2 *part_ml;                // [2 grid][rows]: maximum (log2 units) and sum
+    TreeCut *cuts;                  // [grid]
     int group, kv_rep, heads;       // query heads per kernel group, groups per kv head, groups
     int nodes;                      // nodes of a row tile (its rows: nodes * group)
     int slot_rows;                  // rows of a partial slot
@@ -330,6 +338,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         uint32_t n_k = 0, n_v = 0, n_q = 0;   // copies issued (for the drain on an abort)
         int stop = 0;
         int64_t u = u_begin;
+        bool joined = false;                  // this share joins a cut run
         // Publishes the next segment of the share (or the end) and returns it.
         auto next_segment = [&]() -> TreeSegment {
             const int slot = n_seg & 3;
@@ -357,6 +366,13 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 s.n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
                 s.j0 = tree_first_key(q, p.window) / kKeys + j;
                 s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                if (j > 0 && u - j >= tree_share_begin(total, shares, blockIdx.x - 1)) {
+                    // the share before holds the run's first piece: this one has it joined
+                    TreeCut cut = {2, s.n_nodes * a.group, s.head, s.row0 + s.node0};
+                    while (tree_share_begin(total, shares, blockIdx.x - 1 + cut.pieces) < u - j + tiles) ++cut.pieces;
+                    if (lane == 0) a.cuts[blockIdx.x] = cut;
+                    joined = true;
+                }
                 if (p.window > 0) {   // pages before the first key a row does see are not looked up
                     int least = 1 << 30;
                     for (int i = lane; i < q.T; i += 32)
@@ -388,6 +404,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         };
         const uint64_t policy = l2_policy_evict_first();
         TreeSegment w = next_segment();
+        if (!joined && lane == 0) a.cuts[blockIdx.x] = TreeCut{};
         while (!stop && w.n >= 0) {
             const int kvh = w.head / a.kv_rep;
             if (!FP8) {
@@ -841,59 +858,63 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
 }
 
 // Joins the partial rows of every (sequence, kernel head group, row tile) that was cut: one
-// warp per row, the shares' partials in order, so the result does not depend on timing.
-// Grid: x = (sequence, head group, row tile), y = eight rows.
+// warp per row, the shares' partials in a fixed order, so the result does not depend on
+// timing.  Grid: x = share, y = eight rows; the share that holds a cut run's second piece
+// joins it.  The maxima and sums of up to 32 pieces are read at once, one per lane, and the
+// partial rows four at a time: a row costs a few memory round trips, not one per piece.
 template <int HD>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a, int shares_grid,
-                                                        int row_tiles_max) {
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a) {
     constexpr int D = HD / 32;
-    __shared__ int64_t pref[kMaxSeqs + 1];
     const TreeParams &p = a.p;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    tree_prefix<256>(a, pref, false);
+    const int share = static_cast<int>(blockIdx.x) + 1;
+    const TreeCut cut = a.cuts[share];
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int rt = blockIdx.x % row_tiles_max;
-    const int head = blockIdx.x / row_tiles_max % a.heads;
-    const int b = blockIdx.x / row_tiles_max / a.heads;
-    const TreeSeq s = tree_seq(p, b, false);
-    const int row_tiles = (s.T + a.nodes - 1) / a.nodes;
-    if (rt >= row_tiles) return;
-    const int n_nodes = min(a.nodes, s.T - rt * a.nodes);
-    if (row >= n_nodes * a.group) return;
-    const int64_t total = pref[p.num_seqs];
-    const int shares = tree_shares(a, total, shares_grid);
-    const int tiles = tree_tiles(s, p.window);
-    const int64_t begin = pref[b] + (static_cast<int64_t>(head) * row_tiles + rt) * tiles, end = begin + tiles;
-    int c = static_cast<int>(begin * shares / total);
-    while (tree_share_begin(total, shares, c + 1) <= begin) ++c;
-    while (tree_share_begin(total, shares, c) > begin) --c;
-    if (tree_share_begin(total, shares, c + 1) >= end) return;   // whole: already written
+    if (cut.pieces == 0 || row >= cut.rows) return;
+    // piece 0 is the last run of the share before, the others are the first runs of theirs
+    auto slot_of = [&](int i) -> int64_t {
+        return static_cast<int64_t>(i == 0 ? 2 * (share - 1) + 1 : 2 * (share - 1 + i)) * a.slot_rows + row;
+    };
     float m = -INFINITY, l = 0.f, acc[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) acc[d] = 0.f;
-    // the run begins in share c (its slot 1) and goes on in the next ones (their slot 0)
-    for (int slot = 2 * c + 1;;) {
-        const int64_t at = static_cast<int64_t>(slot) * a.slot_rows + row;
-        const float2 ml = a.part_ml[at];
-        float o[D];
+    for (int base = 0; base < cut.pieces; base += 32) {
+        const int n = min(32, cut.pieces - base);
+        const float2 ml = lane < n ? a.part_ml[slot_of(base + lane)] : make_float2(-INFINITY, 0.f);
+        float top = fmaxf(m, ml.x);
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = a.part_o[at * HD + d * 32 + lane];
-        const float top = fmaxf(m, ml.x);
-        if (top != -INFINITY) {
-            const float fa = m == -INFINITY ? 0.f : exp2f(m - top), fb = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-            l = l * fa + ml.y * fb;
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+        const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2f(ml.x - top);   // keeps a NaN
+        float sum = w * ml.y;
 #pragma unroll
-            for (int d = 0; d < D; ++d) acc[d] = acc[d] * fa + o[d] * fb;
-            m = top;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        l = l * f + sum;
+#pragma unroll
+        for (int d = 0; d < D; ++d) acc[d] *= f;
+        m = top;
+        for (int i = 0; i < n; i += 4) {
+            float o[4][D];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float *src = a.part_o + slot_of(base + min(i + u, n - 1)) * HD;
+#pragma unroll
+                for (int d = 0; d < D; ++d) o[u][d] = src[d * 32 + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float wu = __shfl_sync(kAll, w, min(i + u, n - 1));
+                if (i + u < n && wu != 0.f) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d) acc[d] = fmaf(o[u][d], wu, acc[d]);
+                }
+            }
         }
-        ++c;
-        if (tree_share_begin(total, shares, c) >= end) break;
-        slot = 2 * c;
     }
-    const int node = rt * a.nodes + row / a.group, h = head * a.group + row % a.group;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
-                         (static_cast<int64_t>(s.row0 + node) * p.num_q_heads + h) * HD;
+    const int64_t node = cut.node0 + row / a.group;
+    const int h = cut.head * a.group + row % a.group;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (node * p.num_q_heads + h) * HD;
     const float inv = l > 0.f ? p.v_scale / l : (l == 0.f ? 0.f : l);
 #pragma unroll
     for (int d = 0; d < D; ++d) out[d * 32 + lane] = __float2bfloat16_rn(acc[d] * inv);
@@ -964,11 +985,11 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs * a.heads * row_tiles),
-                       static_cast<unsigned>((a.slot_rows + 7) / 8));
+    if (grid == 1) return cudaSuccess;   // nothing is cut
+    cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), static_cast<unsigned>((a.slot_rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a, grid, row_tiles);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a);
 }
 
 }  // namespace
@@ -984,6 +1005,7 @@ cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t s
     const size_t slots = 2 * kMaxCtas;
     a.part_o = static_cast<float *>(p.workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots * a.slot_rows * head_dim);
+    a.cuts = reinterpret_cast<TreeCut *>(a.part_ml + slots * a.slot_rows);
     // the line's prefix holds kMaxSeqs sequences: more go in several launches, one after another
     for (int at = 0; at < p.num_seqs; at += kMaxSeqs) {
         a.p = p;
@@ -1012,7 +1034,7 @@ extern "C" size_t pa_tree_decode_workspace_size(int num_seqs, int max_tree_len, 
         return 0;
     const int group = pa::tree_group(num_q_heads, num_kv_heads);
     const size_t rows = static_cast<size_t>(2 * pa::kMaxCtas) * pa::tree_nodes(group, max_tree_len) * group;
-    return rows * (static_cast<size_t>(head_dim) * 4 + 8);
+    return rows * (static_cast<size_t>(head_dim) * 4 + 8) + pa::kMaxCtas * sizeof(pa::TreeCut);
 }
 
 extern "C" int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
