@@ -12,8 +12,8 @@
 // Selection is by exact scores.  A score computed in fp32 is off by at most
 //     E = (group + 24) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
 // (P and N are sums of `group` terms; a product is rounded, added in a chain of four, joined
-// by three more sums in the lane and five across lanes; S itself is as far off and T +- 2E
-// is rounded: fewer than group + 24 roundings act on any term).  With T the f-th
+// by three more sums in the lane and five across lanes; S itself may be 32 roundings off and
+// T +- 2E is rounded: fewer than group + 24 roundings act on any term).  With T the f-th
 // largest computed score, a page above T + 2E is among the f best and one below T - 2E is
 // not; the band between is scored again in fp64 and ranked by (score, page).
 #include "../../include/pa.h"
@@ -147,7 +147,7 @@ cudaError_t launch_bounds(const BoundsParams &p, bool fp8, cudaStream_t stream) 
 
 // ---- scores ---------------------------------------------------------------------------------
 
-constexpr int kLeastChunk = 64;   // fewest pages per CTA
+constexpr int kChunk = 32;   // pages per warp of the score pass
 
 struct SelectParams {
     int32_t *page_tables, *page_lens;
@@ -159,7 +159,7 @@ struct SelectParams {
     int32_t *band;      // [B][nkv][max_blocks]
     double *exact;      // [B][nkv][max_blocks]
     int64_t num_blocks;
-    int num_seqs, nq, nkv, max_blocks, chunk, chunks, max_pages, sink, recent;   // chunk: pages per CTA
+    int num_seqs, nq, nkv, max_blocks, chunks, max_pages, sink, recent;
     int *status;
 };
 
@@ -208,43 +208,64 @@ __device__ __forceinline__ void unpack16(const uint4 &raw, float (&f)[FP8 ? 16 :
     }
 }
 
-// Grid (chunk, kv head, sequence), an eighth of the chunk's pages (at most 32) per warp.  A
-// page's bounds (min row, then max row) are UNITS units of 16 bytes, so a warp reads
+// One warp per (sequence, kv head, 32 pages); nothing is shared, so no warp waits for another.
+// A page's bounds (min row, then max row) are UNITS units of 16 bytes, so a warp reads
 // 32 / UNITS pages with one load instruction (at head_dim 256 in bf16 a page takes two).
-// Everything that does not wait for something else is issued first: the page ids (one per
-// lane, one load), then kLoads groups of bounds, and only then the query heads, whose sums
-// go through shared memory; the next groups are loaded while the last are multiplied.  The
-// pass reads 2 head_dim elements a page and multiplies each once, so streaming them is its
-// bound.
+// What does not wait for something else is issued first: the page ids (one per lane, one
+// load) and the query heads, then kLoads groups of bounds at a time.  The pass reads
+// 2 head_dim elements a page and multiplies each once, so streaming them is its bound.
 template <int HD, bool FP8>
-__global__ void __launch_bounds__(256, 2) score_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(256, 3) score_kernel(const __grid_constant__ SelectParams p) {
     constexpr int PAGE = 2 * HD * (FP8 ? 1 : 2);
     constexpr int UNITS = PAGE / 16;
     constexpr int LANES = UNITS < 32 ? UNITS : 32;
     constexpr int PARTS = UNITS / LANES;          // loads per page
     constexpr int PER = 32 / LANES;               // pages per load
     constexpr int E = FP8 ? 16 : 8;               // elements of a unit
-    constexpr int kLoads = 8 / PARTS;             // page groups in flight
-    constexpr int STEP = kLoads * PER;            // pages of a step
-    __shared__ __align__(16) float weight[2 * HD];              // N, then P: in the order of a page's rows
-    __shared__ float span[8];
+    constexpr int kLoads = (FP8 ? 4 : 8) / PARTS; // page groups in flight
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.z, kh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = select_len(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
+    const int lane = threadIdx.x & 31;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = item / p.chunks;          // b * nkv + kh
+    const int chunk = static_cast<int>(item - row * p.chunks);
+    if (row >= static_cast<int64_t>(p.num_seqs) * p.nkv) return;
+    const int b = static_cast<int>(row / p.nkv), kh = static_cast<int>(row - static_cast<int64_t>(b) * p.nkv);
+    const int L = select_len(p, b, chunk == 0 && kh == 0 && lane == 0);
     const int np = (L + kBlockSize - 1) / kBlockSize;
-    if (np <= p.max_pages || static_cast<int>(blockIdx.x) * p.chunk >= np) return;
-    const int each = p.chunk / 8;
-    const int first = blockIdx.x * p.chunk + warp * each;
-    const int n = min(each, np - first);          // may be negative
-    const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
+    const int first = chunk * kChunk;
+    const int n = min(kChunk, np - first);
+    if (np <= p.max_pages || n <= 0) return;
     const int id = lane < n ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + first + lane] : 0;
+    const int unit = lane % LANES, sub = lane / LANES;
+    // this lane's weights: N for the units of the min row (the page's first half), P for the others
+    float w[PARTS][E];
+    const int g = p.nq / p.nkv;
+#pragma unroll
+    for (int v = 0; v < PARTS; ++v) {
+        const int u = v * LANES + unit;
+        const bool low = u < UNITS / 2;
+        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + (low ? u : u - UNITS / 2) * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[v][e] = 0.f;
+#pragma unroll 4
+        for (int h = 0; h < g; ++h) {
+#pragma unroll
+            for (int e0 = 0; e0 < E; e0 += 8) {
+                float f[8];
+                unpack_bf16x8(*reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(h) * HD + e0), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)   // a NaN goes to P
+                    w[v][e0 + e] += (f[e] < 0.f) == low ? f[e] : 0.f;
+            }
+        }
+    }
     const bool known = id >= 0 && id < p.num_blocks;
     if (!known) atomicOr(p.status, kStatusBounds);
     const unsigned unknown = __ballot_sync(kAll, !known);
     const int page = known ? id : 0;
-    const int unit = lane % LANES, sub = lane / LANES;
-    uint4 raw[kLoads][PARTS];
-    auto load = [&](int at) {
+    float most = 0.f;
+    for (int at = 0; at < n; at += kLoads * PER) {
+        uint4 raw[kLoads][PARTS];
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             const int i = at + k * PER + sub;
@@ -253,53 +274,25 @@ __global__ void __launch_bounds__(256, 2) score_kernel(const __grid_constant__ S
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) raw[k][v] = i < n ? __ldg(src + v * LANES) : make_uint4(0u, 0u, 0u, 0u);
         }
-    };
-    load(0);
-    const int g = p.nq / p.nkv;
-    for (int d = threadIdx.x; d < HD; d += 256) {
-        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
-        float lo = 0.f, hi = 0.f;
-#pragma unroll 8
-        for (int h = 0; h < g; ++h) {
-            const float x = __bfloat162float(q[h * HD]);
-            lo += x < 0.f ? x : 0.f;
-            hi += x < 0.f ? 0.f : x;              // a NaN goes to P
-        }
-        weight[d] = lo;
-        weight[HD + d] = hi;
-    }
-    __syncthreads();
-    float w[PARTS][E];
-#pragma unroll
-    for (int v = 0; v < PARTS; ++v)
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&weight[(v * LANES + unit) * E + e]);
-            w[v][e] = x.x, w[v][e + 1] = x.y, w[v][e + 2] = x.z, w[v][e + 3] = x.w;
-        }
-    float most = 0.f;
-    for (int at = 0; at < n; at += STEP) {
-        float s[kLoads], a[kLoads];
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
-            s[k] = a[k] = 0.f;
+            // four chains of E / 4 products a unit; the sum of magnitudes needs no better than
+            // its own roundings
+            float s = 0.f, a = 0.f;
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) {
-                float f[E];
+                float f[E], c[4] = {0.f, 0.f, 0.f, 0.f};
                 unpack16<FP8>(raw[k][v], f);
-                // four chains of E / 4 products each
-                float c[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float x = w[v][e] * f[e];
                     c[e & 3] += x;
-                    t[e & 3] += fabsf(x);
+                    a += fabsf(x);
                 }
-                s[k] += (c[0] + c[1]) + (c[2] + c[3]);
-                a[k] += (t[0] + t[1]) + (t[2] + t[3]);
+                s += (c[0] + c[1]) + (c[2] + c[3]);
             }
-            if (a[k] != a[k]) {   // a zero weight met an infinity, or there is a NaN: the exact rule
-                s[k] = a[k] = 0.f;
+            if (a != a) {   // a zero weight met an infinity, or there is a NaN: the exact rule
+                s = a = 0.f;
 #pragma unroll
                 for (int v = 0; v < PARTS; ++v) {
                     float f[E];
@@ -307,34 +300,24 @@ __global__ void __launch_bounds__(256, 2) score_kernel(const __grid_constant__ S
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         const float x = weighed(w[v][e], f[e]);
-                        s[k] += x;
-                        a[k] += fabsf(x);
+                        s += x;
+                        a += fabsf(x);
                     }
                 }
             }
-        }
-        if (at + STEP < n) load(at + STEP);
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
 #pragma unroll
             for (int o = LANES / 2; o; o >>= 1) {
-                s[k] += __shfl_xor_sync(kAll, s[k], o);
-                a[k] += __shfl_xor_sync(kAll, a[k], o);
+                s += __shfl_xor_sync(kAll, s, o);
+                a += __shfl_xor_sync(kAll, a, o);
             }
             const int i = at + k * PER + sub;
-            most = max_nan(most, a[k]);
-            if (unit == 0 && i < n) p.score[row * p.max_blocks + first + i] = unknown >> i & 1 ? -INFINITY : s[k];
+            most = max_nan(most, a);
+            if (unit == 0 && i < n) p.score[row * p.max_blocks + first + i] = unknown >> i & 1 ? -INFINITY : s;
         }
     }
 #pragma unroll
     for (int o = 16; o >= LANES; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
-    if (lane == 0) span[warp] = most;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) most = max_nan(most, span[i]);
-        p.span[row * p.chunks + blockIdx.x] = most;
-    }
+    if (lane == 0) p.span[row * p.chunks + chunk] = most;
 }
 
 // ---- selection ------------------------------------------------------------------------------
@@ -411,7 +394,7 @@ __device__ __forceinline__ int block_scan(int x, int *warps) {
 // border score is found by counting, two bits a step and below the bits that all
 // candidates share: one barrier a step, no histogram and no atomics.
 template <int HD, bool FP8, int NT, int K>
-__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
     constexpr int W = NT / 32;
     constexpr int kSmallBand = 32;
@@ -440,11 +423,16 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     const int per = K > 0 ? K : (np + NT - 1) / NT;
     const int mine = tid * per;
     uint32_t key[K > 0 ? K : 1];                // 0 for pages that are not candidates
+    int id[K > 0 ? K : 1];
     if constexpr (K > 0) {
 #pragma unroll
-        for (int i = 0; i < K; ++i)
+        for (int i = 0; i < K; ++i) {
+            id[i] = mine + i < np ? bt[mine + i] : 0;
             key[i] = mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
+        }
     }
+    float s = 0.f;                              // S of the bound E
+    for (int i = lane; i < (np + kChunk - 1) / kChunk; i += 32) s = max_nan(s, p.span[row * p.chunks + i]);
     auto key_at = [&](int i) -> uint32_t {      // of page mine + i
         if constexpr (K > 0) return key[i];
         else return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
@@ -481,8 +469,6 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
                     for (int i = 0; i < per; ++i) c += key_at(i) >= x;
                 }
             });
-        float s = 0.f;
-        for (int i = lane; i < (np + p.chunk - 1) / p.chunk; i += 32) s = max_nan(s, p.span[row * p.chunks + i]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s = max_nan(s, __shfl_xor_sync(kAll, s, o));
         const float T = t == 0xffffffffu ? NAN
@@ -597,13 +583,13 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
                     win = e > edge || (e == edge && tie++ < ties);
                 }
             }
-            if (win) emit(page);
+            if (win) emit(i);
         }
     };
     int n = 0;
     walk([&](int) { ++n; });
     int to = block_scan<NT>(n, warps);
-    walk([&](int page) { out[to++] = bt[page]; });
+    walk([&](int i) { out[to++] = K > 0 ? id[i] : bt[mine + i]; });
 }
 
 // Launches a kernel as a programmatic dependent of the work before it in the stream.
@@ -624,13 +610,16 @@ cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams
 template <int HD, bool FP8>
 cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
     if (p.max_blocks > p.max_pages) {
-        const cudaError_t e = launch_after(score_kernel<HD, FP8>, dim3(p.chunks, p.nkv, p.num_seqs), 256, p, stream);
+        const cudaError_t e = launch_after(
+            score_kernel<HD, FP8>,
+            dim3(static_cast<unsigned>((static_cast<int64_t>(p.num_seqs) * p.nkv * p.chunks + 7) / 8)), 256, p, stream);
         if (e != cudaSuccess) return e;
     }
     // as many threads as a table's pages need at 8 a thread; past 8192 pages (131072 tokens) the
     // scores no longer fit the registers
     const dim3 grid(p.nkv, p.num_seqs);
     if (p.max_blocks <= 2048) return launch_after(select_kernel<HD, FP8, 256, 8>, grid, 256, p, stream);
+    if (p.max_blocks <= 4096) return launch_after(select_kernel<HD, FP8, 512, 8>, grid, 512, p, stream);
     if (p.max_blocks <= 8192) return launch_after(select_kernel<HD, FP8, 1024, 8>, grid, 1024, p, stream);
     return launch_after(select_kernel<HD, FP8, 1024, 0>, grid, 1024, p, stream);
 }
@@ -643,7 +632,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t select_layout(int num_seqs, int nkv, int max_blocks, size_t off[4]) {
     const size_t rows = static_cast<size_t>(num_seqs > 0 ? num_seqs : 0) * (nkv > 0 ? nkv : 0);
     const size_t n = rows * (max_blocks > 0 ? max_blocks : 0);
-    const size_t chunks = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kLeastChunk - 1) / kLeastChunk;
+    const size_t chunks = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kChunk - 1) / kChunk;
     off[0] = 0;
     off[1] = off[0] + round256(n * 4);
     off[2] = off[1] + round256(rows * chunks * 4);
@@ -742,6 +731,8 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     if (num_seqs > 65535 || num_kv_heads > 65535)
         return api_fail(PA_ERR_UNSUPPORTED, "num_seqs %d, num_kv_heads %d: at most 65535", num_seqs,
                         num_kv_heads);
+    if (static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_blocks_per_seq + kChunk - 1) / kChunk) / 8 >= INT32_MAX)
+        return api_fail(PA_ERR_UNSUPPORTED, "too many pages for one launch");
     if (num_seqs == 0) return PA_OK;
     if (!page_tables || !page_lens || !q || !bounds || !block_tables || !seq_lens)
         return api_fail(PA_ERR_INVALID, "null pointer argument");
@@ -770,12 +761,7 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     p.nq = num_q_heads;
     p.nkv = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
-    // Pages per CTA of the score pass: 64 (one round of loads at head_dim 128 in bf16) while
-    // that gives the GPU's 152 SMs fewer than 16 CTAs each, else 256.
-    p.chunk = kLeastChunk;
-    if (static_cast<int64_t>(num_seqs) * num_kv_heads * (max_blocks_per_seq / kLeastChunk) > 16 * 152)
-        p.chunk = 4 * kLeastChunk;
-    p.chunks = (max_blocks_per_seq + p.chunk - 1) / p.chunk;
+    p.chunks = (max_blocks_per_seq + kChunk - 1) / kChunk;
     p.max_pages = max_pages;
     p.sink = sink_pages;
     p.recent = recent_pages;

@@ -55,6 +55,8 @@ constexpr int kTreeThreads = 192;
 constexpr int kMaxCtas = 304;       // two per SM of 152
 constexpr int kMaxSeqs = 1024;      // sequences per launch (their prefix is in shared memory)
 
+constexpr int kCutTiles = 12;
+
 constexpr uint32_t pow2_columns(uint32_t x) {
     uint32_t v = 32;
     while (v < x) v <<= 1;
@@ -76,7 +78,8 @@ struct TreeCfg {
     static constexpr uint32_t OFF_K = Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + STAGES * KV_BYTES;
     static constexpr uint32_t OFF_PREF = OFF_V + STAGES * KV_BYTES;    // int64 [kMaxSeqs + 1]
-    static constexpr uint32_t OFF_BAR = OFF_PREF + (kMaxSeqs + 1) * 8;
+    static constexpr uint32_t OFF_RUN = OFF_PREF + (kMaxSeqs + 1) * 8; // int [kMaxSeqs + 1]
+    static constexpr uint32_t OFF_BAR = OFF_RUN + (kMaxSeqs + 2) * 4;
     static constexpr uint32_t SMEM_USED = OFF_BAR + 1024;
     static constexpr int CTAS_PER_SM = HD == 256 ? 1 : 2;
     static constexpr uint32_t SMEM = SMEM_USED + 1024;           // + realignment of the base
@@ -102,7 +105,6 @@ struct TreeLaunch {
     int group, kv_rep, heads;       // query heads per kernel group, groups per kv head, groups
     int nodes;                      // nodes of a row tile (its rows: nodes * group)
     int slot_rows;                  // rows of a partial slot
-    int min_tiles;                  // fewest tiles of a share
 };
 
 // Sequence b's drafted rows and lengths; T = 0 (and the device status set when `flag`) if
@@ -139,19 +141,23 @@ __device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
     return s.T > 0 ? (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys : 0;
 }
 
-// pref[b] = tiles of the line before sequence b; all threads of the CTA call it.
-template <int NT>
-__device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, bool flag) {
+// pref[b] = tiles of the line before sequence b, run[b] the tiles of its runs, run[n] those of
+// the longest; all threads of the CTA call it.
+__device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, int *run, bool flag) {
     const TreeParams &p = a.p;
-    for (int b = threadIdx.x; b < p.num_seqs; b += NT) {
+    for (int b = threadIdx.x; b < p.num_seqs; b += kTreeThreads) {
         const TreeSeq s = tree_seq(p, b, flag);
-        pref[b + 1] = static_cast<int64_t>(tree_tiles(s, p.window)) *
-                      ((s.T + a.nodes - 1) / a.nodes) * a.heads;
+        run[b] = tree_tiles(s, p.window);
+        pref[b + 1] = static_cast<int64_t>(run[b]) * ((s.T + a.nodes - 1) / a.nodes) * a.heads;
     }
     if (threadIdx.x == 0) pref[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
+        int longest = 0;
+        for (int b = lane; b < p.num_seqs; b += 32) longest = max(longest, run[b]);
+        longest = __reduce_max_sync(kAll, longest);
+        if (lane == 0) run[p.num_seqs] = longest;
         long long carry = 0;
         for (int base = 1; base <= p.num_seqs; base += 32) {
             const int i = base + lane;
@@ -168,15 +174,33 @@ __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, 
     __syncthreads();
 }
 
-// Shares that the line of `total` tiles is cut into, and where share c begins.
-__device__ __forceinline__ int tree_shares(const TreeLaunch &a, int64_t total, int grid) {
-    const int64_t n = (total + a.min_tiles - 1) / a.min_tiles;
-    return static_cast<int>(n < grid ? (n > 0 ? n : 1) : grid);
-}
+// How the line of tiles is cut into shares: evenly, or at the run boundaries nearest to the
+// even cuts, which needs no joining.
+struct TreeShares {
+    const int64_t *pref;   // [n + 1] tiles before sequence b
+    const int *run;        // [n] tiles of each of sequence b's runs
+    int64_t total;
+    int n, shares;
+    bool whole;
 
-__device__ __forceinline__ int64_t tree_share_begin(int64_t total, int shares, int c) {
-    return c >= shares ? total : total * c / shares;
-}
+    // the largest b with pref[b] <= u
+    __device__ __forceinline__ int sequence(int64_t u) const {
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pref[mid] <= u) lo = mid; else hi = mid;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ int64_t begin(int c) const {
+        if (c >= shares) return total;
+        const int64_t u = total * c / shares;
+        if (!whole || u <= 0) return u;
+        const int b = sequence(u);
+        const int r = static_cast<int>((u - pref[b]) % run[b]);
+        return 2 * r >= run[b] ? u - r + run[b] : u - r;
+    }
+};
 
 // One run of a share's tiles within one (sequence, kv head, row tile).
 struct TreeSegment {
@@ -266,6 +290,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     int64_t *pref = reinterpret_cast<int64_t *>(smem + C::OFF_PREF);
+    int *run = reinterpret_cast<int *>(smem + C::OFF_RUN);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     // Tiles are numbered g over all segments of the CTA: ring stage g % STAGES, S buffer g % 2.
     uint64_t *q_full = bars + 0;     // FP8: one arrival per softmax warp
@@ -322,15 +347,24 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     }
     // launched as a programmatic dependent: nothing before this point reads global memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    tree_prefix<kTreeThreads>(a, pref, blockIdx.x == 0);
+    tree_prefix(a, pref, run, blockIdx.x == 0);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    const int64_t total = pref[p.num_seqs];
-    const int shares = tree_shares(a, total, gridDim.x);
-    const int64_t u_begin = tree_share_begin(total, shares, blockIdx.x);
-    const int64_t u_end = tree_share_begin(total, shares, blockIdx.x + 1);
+    TreeShares line{pref, run, pref[p.num_seqs], p.num_seqs, static_cast<int>(gridDim.x), false};
+    if (line.total < line.shares) line.shares = max(1, static_cast<int>(line.total));
+    {
+        // Shares of whole runs hold at most one run when there are no more runs than shares, else
+        // an even share and a run; cutting costs a partial tile's round trip and the join,
+        // as much as about kCutTiles tiles.
+        const int64_t even = line.total / line.shares;
+        const int64_t longest = run[p.num_seqs];
+        const int64_t most = even < longest ? longest : even + longest;
+        line.whole = most <= even + kCutTiles;
+    }
+    const int64_t u_begin = line.begin(blockIdx.x);
+    const int64_t u_end = line.begin(blockIdx.x + 1);
 
     if (warp == 0) {
         // ------------------------------- TMA producer -------------------------------
@@ -345,13 +379,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             TreeSegment s = {};
             s.n = -1;
             if (u < u_end) {
-                int lo = 0, hi = p.num_seqs;      // largest b with pref[b] <= u
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (pref[mid] <= u) lo = mid; else hi = mid;
-                }
+                const int lo = line.sequence(u);
                 const TreeSeq q = tree_seq(p, lo, false);
-                const int tiles = tree_tiles(q, p.window);
+                const int tiles = run[lo];
                 const int row_tiles = (q.T + a.nodes - 1) / a.nodes;
                 const int64_t rel = u - pref[lo];
                 const int item = static_cast<int>(rel / tiles);
@@ -366,10 +396,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 s.n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
                 s.j0 = tree_first_key(q, p.window) / kKeys + j;
                 s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
-                if (j > 0 && u - j >= tree_share_begin(total, shares, blockIdx.x - 1)) {
+                if (j > 0 && u - j >= line.begin(blockIdx.x - 1)) {
                     // the share before holds the run's first piece: this one has it joined
                     TreeCut cut = {2, s.n_nodes * a.group, s.head, s.row0 + s.node0};
-                    while (tree_share_begin(total, shares, blockIdx.x - 1 + cut.pieces) < u - j + tiles) ++cut.pieces;
+                    while (line.begin(blockIdx.x - 1 + cut.pieces) < u - j + tiles) ++cut.pieces;
                     if (lane == 0) a.cuts[blockIdx.x] = cut;
                     joined = true;
                 }
@@ -602,12 +632,18 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const __nv_bfloat16 *>(p.q) +
                     (static_cast<int64_t>(w.row0 + node) * p.num_q_heads + head) * HD);
+                // up to 128 channels stay in registers between the two passes over them
+                constexpr int HELD = HD < 256 ? HD / 8 : 8;
+                uint4 held[HELD];
                 float most = 0.f;
-                if (mine) {
-#pragma unroll 4
-                    for (int c = 0; c < HD / 8; ++c) {
+#pragma unroll
+                for (int c0 = 0; c0 < HD / 8; c0 += HELD) {
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) held[c] = mine ? src[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) {
                         float f[8];
-                        unpack_bf16x8(__ldg(src + c), f);
+                        unpack_bf16x8(held[c], f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
                     }
@@ -618,14 +654,14 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const float s = ex == 255 ? NAN : ex > 0 ? __uint_as_float(static_cast<uint32_t>(min(max(127 + 7 + 127 - ex, 1), 254)) << 23) : 1.f;
                 scale = p.scale_log2 * p.k_scale / s;
                 if (busy) {
-#pragma unroll 2
+#pragma unroll
                     for (int c = 0; c < HD / 16; ++c) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
                             float f[8];
-                            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                            if (mine) raw = __ldg(src + 2 * c + v);
+                            uint4 raw = held[(2 * c + v) % HELD];
+                            if constexpr (HELD < HD / 8) raw = mine ? src[2 * c + v] : make_uint4(0u, 0u, 0u, 0u);
                             unpack_bf16x8(raw, f);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
@@ -804,9 +840,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                                 make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     } else if (mine) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<uint4 *>(part + c * 32)[e] =
-                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 32; e += 8)   // whole sectors
+                            st_global_32B(part + c * 32 + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5],
+                                          o[e + 6], o[e + 7]);
                     }
                     __syncwarp();
                 }
@@ -1001,7 +1037,6 @@ cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t s
     a.heads = p.num_q_heads / a.group;
     a.nodes = tree_nodes(a.group, p.max_tree_len);
     a.slot_rows = a.nodes * a.group;
-    a.min_tiles = 1;
     const size_t slots = 2 * kMaxCtas;
     a.part_o = static_cast<float *>(p.workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots * a.slot_rows * head_dim);
