@@ -147,7 +147,6 @@ cudaError_t launch_bounds(const BoundsParams &p, bool fp8, cudaStream_t stream) 
 
 // ---- scores ---------------------------------------------------------------------------------
 
-constexpr int kChunk = 32;   // pages per warp of the score pass
 
 struct SelectParams {
     int32_t *page_tables, *page_lens;
@@ -155,11 +154,11 @@ struct SelectParams {
     const uint8_t *bounds;
     const int32_t *block_tables, *seq_lens;
     float *score;       // [B][nkv][max_blocks]
-    float *span;        // [B][nkv][chunks]: largest S of a chunk's pages
+    float *span;        // [B][nkv][groups]: largest S of a group's pages
     int32_t *band;      // [B][nkv][max_blocks]
     double *exact;      // [B][nkv][max_blocks]
     int64_t num_blocks;
-    int num_seqs, nq, nkv, max_blocks, chunks, max_pages, sink, recent;
+    int num_seqs, nq, nkv, max_blocks, group, groups, max_pages, sink, recent;   // group: pages of one S
     int *status;
 };
 
@@ -208,88 +207,150 @@ __device__ __forceinline__ void unpack16(const uint4 &raw, float (&f)[FP8 ? 16 :
     }
 }
 
-// One warp per (sequence, kv head, 32 pages); nothing is shared, so no warp waits for another.
-// A page's bounds (min row, then max row) are UNITS units of 16 bytes, so a warp reads
-// 32 / UNITS pages with one load instruction (at head_dim 256 in bf16 a page takes two).
-// What does not wait for something else is issued first: the page ids (one per lane, one
-// load) and the query heads, then kLoads groups of bounds at a time.  The pass reads
-// 2 head_dim elements a page and multiplies each once, so streaming them is its bound.
+// The pass reads 2 head_dim elements a page and multiplies each once: streaming them is its
+// bound, so every SM holds 24 warps with up to 4 KB of bounds on their way each, and what comes
+// before the stream is paid once: the (sequence, kv head, group of pages) steps form a line
+// and every warp takes an equal run of it, with the next group's page ids read a group ahead.
+// (A warp per 32 pages paid its two dependent reads and its query heads for every 16 KB:
+// 37 us for 168 MB; bulk copies of single pages into shared memory were slower still, 47 us:
+// 512 bytes are too little for one.)  A page is UNITS units of 16 bytes (min row, then max
+// row): 32 / UNITS pages a load, and the sums of a group's pages are reduced over the lanes at
+// once by halving exchanges (16 shuffles for 16 sums instead of 80).
 template <int HD, bool FP8>
-__global__ void __launch_bounds__(256, 3) score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int PAGE = 2 * HD * (FP8 ? 1 : 2);
-    constexpr int UNITS = PAGE / 16;
-    constexpr int LANES = UNITS < 32 ? UNITS : 32;
-    constexpr int PARTS = UNITS / LANES;          // loads per page
-    constexpr int PER = 32 / LANES;               // pages per load
+struct ScoreCfg {
+    static constexpr int PAGE = 2 * HD * (FP8 ? 1 : 2);
+    static constexpr int UNITS = PAGE / 16;
+    static constexpr int LANES = UNITS < 32 ? UNITS : 32;
+    static constexpr int PARTS = UNITS / LANES;          // units a lane takes of a page
+    static constexpr int PER = 32 / LANES;               // pages of a load
+    static constexpr int LOADS = (FP8 ? 4 : 8) / PARTS;  // page loads of a group
+    static constexpr int GROUP = LOADS * PER;            // pages of a group
+};
+
+constexpr int kLeastGroup = 4;     // of any ScoreCfg
+constexpr int kScoreThreads = 256;
+constexpr int kScoreSeqs = 1024;   // sequences per launch (their prefix is in shared memory)
+
+template <int HD, bool FP8>
+__global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_constant__ SelectParams p) {
+    using C = ScoreCfg<HD, FP8>;
+    static_assert(C::GROUP >= kLeastGroup && C::GROUP <= 32, "group");
+    constexpr int UNITS = C::UNITS, LANES = C::LANES, PARTS = C::PARTS, PER = C::PER, LOADS = C::LOADS;
     constexpr int E = FP8 ? 16 : 8;               // elements of a unit
-    constexpr int kLoads = (FP8 ? 4 : 8) / PARTS; // page groups in flight
+    __shared__ int64_t pref[kScoreSeqs + 1];      // groups before sequence b
+    __shared__ int pages[kScoreSeqs];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = item / p.chunks;          // b * nkv + kh
-    const int chunk = static_cast<int>(item - row * p.chunks);
-    if (row >= static_cast<int64_t>(p.num_seqs) * p.nkv) return;
-    const int b = static_cast<int>(row / p.nkv), kh = static_cast<int>(row - static_cast<int64_t>(b) * p.nkv);
-    const int L = select_len(p, b, chunk == 0 && kh == 0 && lane == 0);
-    const int np = (L + kBlockSize - 1) / kBlockSize;
-    const int first = chunk * kChunk;
-    const int n = min(kChunk, np - first);
-    if (np <= p.max_pages || n <= 0) return;
-    const int id = lane < n ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + first + lane] : 0;
-    const int unit = lane % LANES, sub = lane / LANES;
-    // this lane's weights: N for the units of the min row (the page's first half), P for the others
-    float w[PARTS][E];
-    const int g = p.nq / p.nkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int b = threadIdx.x; b < p.num_seqs; b += kScoreThreads) {
+        const int np = (select_len(p, b, blockIdx.x == 0) + kBlockSize - 1) / kBlockSize;
+        pages[b] = np;
+        pref[b + 1] = np > p.max_pages ? static_cast<int64_t>((np + C::GROUP - 1) / C::GROUP) * p.nkv : 0;
+    }
+    if (threadIdx.x == 0) pref[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        long long carry = 0;
+        for (int base = 1; base <= p.num_seqs; base += 32) {
+            const int i = base + lane;
+            long long v = i <= p.num_seqs ? pref[i] : 0;
 #pragma unroll
-    for (int v = 0; v < PARTS; ++v) {
-        const int u = v * LANES + unit;
-        const bool low = u < UNITS / 2;
-        const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + (low ? u : u - UNITS / 2) * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[v][e] = 0.f;
-#pragma unroll 4
-        for (int h = 0; h < g; ++h) {
-#pragma unroll
-            for (int e0 = 0; e0 < E; e0 += 8) {
-                float f[8];
-                unpack_bf16x8(*reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(h) * HD + e0), f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)   // a NaN goes to P
-                    w[v][e0 + e] += (f[e] < 0.f) == low ? f[e] : 0.f;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(kAll, v, o);
+                if (lane >= o) v += u;
             }
+            if (i <= p.num_seqs) pref[i] = v + carry;
+            carry += __shfl_sync(kAll, v, 31);
         }
     }
-    const bool known = id >= 0 && id < p.num_blocks;
-    if (!known) atomicOr(p.status, kStatusBounds);
-    const unsigned unknown = __ballot_sync(kAll, !known);
-    const int page = known ? id : 0;
-    float most = 0.f;
-    for (int at = 0; at < n; at += kLoads * PER) {
-        uint4 raw[kLoads][PARTS];
+    __syncthreads();
+    const int64_t total = pref[p.num_seqs];
+    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kScoreThreads / 32);
+    // neighbouring runs go to different SMs
+    const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+    int64_t u = total * me / n_warps;
+    const int64_t end = total * (me + 1) / n_warps;
+    if (u >= end) return;
+    int b = 0;
+    for (int hi = p.num_seqs; hi - b > 1;) {      // the largest b with pref[b] <= u
+        const int mid = (b + hi) >> 1;
+        if (pref[mid] <= u) b = mid; else hi = mid;
+    }
+    int groups = static_cast<int>((pref[b + 1] - pref[b]) / p.nkv);
+    int kh = static_cast<int>((u - pref[b]) / groups);
+    int grp = static_cast<int>(u - pref[b] - static_cast<int64_t>(kh) * groups);
+    const int unit = lane % LANES, sub = lane / LANES;
+    const int g = p.nq / p.nkv;
+    auto page_id = [&](int b, int grp) -> int {
+        const int i = grp * C::GROUP + lane;
+        return lane < C::GROUP && i < pages[b] ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + i] : 0;
+    };
+    int id = page_id(b, grp);
+    float w[PARTS][E];   // this lane's weights: N for the units of the min row (a page's first half), else P
+    for (bool fresh = true; u < end; ++u) {
+        // this group's bounds first: nothing here waits for the query
+        const bool known = id >= 0 && id < p.num_blocks;
+        if (!known) atomicOr(p.status, kStatusBounds);
+        const unsigned unknown = __ballot_sync(kAll, !known);
+        const int page = known ? id : 0;
+        const int first = grp * C::GROUP, n = min(C::GROUP, pages[b] - first);
+        uint4 raw[LOADS][PARTS];
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const int i = at + k * PER + sub;
-            const int64_t pg = __shfl_sync(kAll, page, i & 31);
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (pg * p.nkv + kh) * PAGE) + unit;
+        for (int k = 0; k < LOADS; ++k) {
+            const int i = k * PER + sub;
+            const int64_t pg = __shfl_sync(kAll, page, i);
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (pg * p.nkv + kh) * C::PAGE) + unit;
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) raw[k][v] = i < n ? __ldg(src + v * LANES) : make_uint4(0u, 0u, 0u, 0u);
         }
+        const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
+        // where the next group is, and its ids
+        int b1 = b, kh1 = kh, grp1 = grp + 1;
+        if (grp1 == groups) {
+            grp1 = 0;
+            if (++kh1 == p.nkv) {
+                kh1 = 0;
+                do ++b1; while (b1 + 1 < p.num_seqs && pref[b1 + 1] == pref[b1]);
+            }
+        }
+        const int id1 = u + 1 < end ? page_id(b1, grp1) : 0;
+        if (fresh) {
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            // four chains of E / 4 products a unit; the sum of magnitudes needs no better than
-            // its own roundings
+            for (int v = 0; v < PARTS; ++v) {
+                const int at = v * LANES + unit;
+                const bool low = at < UNITS / 2;
+                const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD +
+                                         (low ? at : at - UNITS / 2) * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) w[v][e] = 0.f;
+#pragma unroll 4
+                for (int h = 0; h < g; ++h) {
+#pragma unroll
+                    for (int e0 = 0; e0 < E; e0 += 8) {
+                        float f[8];
+                        unpack_bf16x8(*reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(h) * HD + e0), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)   // a NaN goes to P
+                            w[v][e0 + e] += (f[e] < 0.f) == low ? f[e] : 0.f;
+                    }
+                }
+            }
+        }
+        float x[2 * LOADS];   // the pages' sums, then their sums of magnitudes
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
             float s = 0.f, a = 0.f;
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) {
-                float f[E], c[4] = {0.f, 0.f, 0.f, 0.f};
+                float f[E], c[4] = {0.f, 0.f, 0.f, 0.f}, t[2] = {0.f, 0.f};   // chains of E / 4 products
                 unpack16<FP8>(raw[k][v], f);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const float x = w[v][e] * f[e];
-                    c[e & 3] += x;
-                    a += fabsf(x);
+                    const float y = w[v][e] * f[e];
+                    c[e & 3] += y;
+                    t[e & 1] += fabsf(y);
                 }
                 s += (c[0] + c[1]) + (c[2] + c[3]);
+                a += t[0] + t[1];
             }
             if (a != a) {   // a zero weight met an infinity, or there is a NaN: the exact rule
                 s = a = 0.f;
@@ -299,25 +360,47 @@ __global__ void __launch_bounds__(256, 3) score_kernel(const __grid_constant__ S
                     unpack16<FP8>(raw[k][v], f);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const float x = weighed(w[v][e], f[e]);
-                        s += x;
-                        a += fabsf(x);
+                        const float y = weighed(w[v][e], f[e]);
+                        s += y;
+                        a += fabsf(y);
                     }
                 }
             }
-#pragma unroll
-            for (int o = LANES / 2; o; o >>= 1) {
-                s += __shfl_xor_sync(kAll, s, o);
-                a += __shfl_xor_sync(kAll, a, o);
-            }
-            const int i = at + k * PER + sub;
-            most = max_nan(most, a);
-            if (unit == 0 && i < n) p.score[row * p.max_blocks + first + i] = unknown >> i & 1 ? -INFINITY : s;
+            x[k] = s;
+            x[LOADS + k] = a;
         }
-    }
+        __syncwarp();
+        int which = 0;   // the sum this lane ends up with
+        int m = LANES / 2;
 #pragma unroll
-    for (int o = 16; o >= LANES; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
-    if (lane == 0) p.span[row * p.chunks + chunk] = most;
+        for (int half = LOADS; half >= 1; half >>= 1, m >>= 1) {
+            const bool up = lane & m;
+            which += up ? half : 0;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if (i < half) {
+                    const float give = up ? x[i] : x[i + half];
+                    x[i] = (up ? x[i + half] : x[i]) + __shfl_xor_sync(kAll, give, m);
+                }
+        }
+#pragma unroll
+        for (int o = LANES / (4 * LOADS); o >= 1; o >>= 1) x[0] += __shfl_xor_sync(kAll, x[0], o);
+        const bool mag = which >= LOADS;
+        const int i = (which & (LOADS - 1)) * PER + sub;
+        const bool lost = unknown >> i & 1;
+        if (!mag && unit % (LANES / (2 * LOADS)) == 0 && i < n)
+            p.score[row * p.max_blocks + first + i] = lost ? -INFINITY : x[0];
+        float most = mag && !lost ? x[0] : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
+        if (lane == 0) p.span[row * p.groups + grp] = most;
+        fresh = kh1 != kh || b1 != b;
+        if (b1 != b) groups = static_cast<int>((pref[min(b1, p.num_seqs - 1) + 1] - pref[min(b1, p.num_seqs - 1)]) / p.nkv);
+        b = b1;
+        kh = kh1;
+        grp = grp1;
+        id = id1;
+    }
 }
 
 // ---- selection ------------------------------------------------------------------------------
@@ -327,6 +410,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     if (isnan(x)) return 0xffffffffu;
     const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float score_of(uint32_t k) {
+    return k == 0xffffffffu ? NAN : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 __device__ __forceinline__ uint64_t key_of(double x) {
@@ -391,8 +478,11 @@ __device__ __forceinline__ int block_scan(int x, int *warps) {
 // One CTA per (kv head, sequence).  Thread t owns the K consecutive pages from t K on, so that
 // one scan over the threads gives every chosen page its place; their scores stay in
 // registers (K > 0, up to NT K pages) or are read again from the workspace (K = 0).  The
-// border score is found by counting, two bits a step and below the bits that all
-// candidates share: one barrier a step, no histogram and no atomics.
+// border score comes from a histogram of 2 NT bins spread evenly over the scores' range
+// (scores crowd in few binades, so bins of their bits would not part them) and the order of
+// the few scores in the border's bin.  Where that bin holds more than 32, or scores are
+// not finite, it is found by counting instead, two bits a step below the bits that all
+// candidates share.
 template <int HD, bool FP8, int NT, int K>
 __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
@@ -400,9 +490,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
     constexpr int kSmallBand = 32;
     __shared__ int sums_sh[2 * 3 * 32];
     __shared__ int warps[32];
-    __shared__ uint32_t ends[2][32];
+    __shared__ uint32_t ends[3][32];
     __shared__ double P[HD], N[HD];
     __shared__ uint64_t small_key[kSmallBand];
+    __shared__ int small_page[kSmallBand];
+    __shared__ int hist[2 * NT];
+    __shared__ uint32_t bin_key[32];
+    __shared__ int bin_at, bin_above, bin_n;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = select_len(p, b, false);
@@ -423,19 +517,20 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
     const int per = K > 0 ? K : (np + NT - 1) / NT;
     const int mine = tid * per;
     uint32_t key[K > 0 ? K : 1];                // 0 for pages that are not candidates
-    int id[K > 0 ? K : 1];
     if constexpr (K > 0) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            id[i] = mine + i < np ? bt[mine + i] : 0;
-            key[i] = mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
-        }
+        for (int i = 0; i < K; ++i) key[i] = mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
     }
-    float s = 0.f;                              // S of the bound E
-    for (int i = lane; i < (np + kChunk - 1) / kChunk; i += 32) s = max_nan(s, p.span[row * p.chunks + i]);
+    hist[2 * tid] = hist[2 * tid + 1] = 0;
+    if (tid == 0) bin_n = 0;
+    float span = 0.f;                           // S of the bound E
+    for (int i = tid; i < (np + p.group - 1) / p.group; i += NT) span = max_nan(span, p.span[row * p.groups + i]);
     auto key_at = [&](int i) -> uint32_t {      // of page mine + i
         if constexpr (K > 0) return key[i];
         else return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
+    };
+    auto score_key = [&](int i) -> uint32_t {   // the same from memory: for loops that are not unrolled
+        return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
     };
     BlockSums<NT> sums{sums_sh, 0};
     // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
@@ -455,25 +550,63 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         }
         least = __reduce_min_sync(kAll, least);
         top = __reduce_max_sync(kAll, top);
-        if (lane == 0) ends[0][warp] = least, ends[1][warp] = top;
+        const uint32_t wide = __reduce_max_sync(kAll, key_of(span));   // a NaN is the largest
+        if (lane == 0) ends[0][warp] = least, ends[1][warp] = top, ends[2][warp] = wide;
         __syncthreads();
         least = __reduce_min_sync(kAll, lane < W ? ends[0][lane] : 0xffffffffu);
         top = __reduce_max_sync(kAll, lane < W ? ends[1][lane] : 0u);
-        const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
-        const uint32_t t = nth_largest<uint32_t>(
-            bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
-                if constexpr (K > 0) {
+        // bins over [low, low + range], monotone in the score as each rounding is
+        const float low = score_of(least), scale = (2 * NT - 1) / (score_of(top) - low);
+        auto bin_of = [&](uint32_t k) { return min(2 * NT - 1, static_cast<int>((score_of(k) - low) * scale)); };
+        uint32_t t = 0;
+        bool found = isfinite(scale) && scale > 0.f && top < 0xff800000u && least > 0x007fffffu;
+        if (found) {
 #pragma unroll
-                    for (int i = 0; i < K; ++i) c += key[i] >= x;
-                } else {
-                    for (int i = 0; i < per; ++i) c += key_at(i) >= x;
+            for (int i = 0; i < per; ++i) {
+                const uint32_t k = key_at(i);
+                if (k) atomicAdd(&hist[bin_of(k)], 1);
+            }
+            __syncthreads();
+            const int hi_bin = 2 * (NT - 1 - tid) + 1;    // from the top: two bins a thread
+            const int c1 = hist[hi_bin], c0 = hist[hi_bin - 1];
+            const int before = block_scan<NT>(c1 + c0, warps);
+            if (before < f && f <= before + c1 + c0) {
+                const bool first = f <= before + c1;
+                bin_at = first ? hi_bin : hi_bin - 1;
+                bin_above = first ? before : before + c1;
+            }
+            __syncthreads();
+            const int bin = bin_at;
+            if (hist[bin] > 32) {
+                found = false;
+            } else {
+#pragma unroll
+                for (int i = 0; i < per; ++i) {
+                    const uint32_t k = key_at(i);
+                    if (k && bin_of(k) == bin) bin_key[atomicAdd(&bin_n, 1)] = k;
                 }
+                __syncthreads();
+                const int m = bin_n;
+                const uint32_t k = lane < m ? bin_key[lane] : 0u;
+                int place = 0;
+                for (int i = 0; i < m; ++i) {
+                    const uint32_t o = __shfl_sync(kAll, k, i);
+                    place += o > k || (o == k && i < lane);
+                }
+                const unsigned who = __ballot_sync(kAll, lane < m && place == f - bin_above - 1);
+                t = __shfl_sync(kAll, k, __ffs(who) - 1);
+            }
+        }
+        if (!found) {
+            const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
+            t = nth_largest<uint32_t>(bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
+#pragma unroll 1
+                for (int i = 0; i < per; ++i) c += score_key(i) >= x;
             });
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s = max_nan(s, __shfl_xor_sync(kAll, s, o));
-        const float T = t == 0xffffffffu ? NAN
-                                         : __uint_as_float(t & 0x80000000u ? t & 0x7fffffffu : ~t);
-        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 24) * 0x1p-24f * s;
+        }
+        span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
+        const float T = score_of(t);
+        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 24) * 0x1p-24f * span;
         if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
             above = key_of(T + E2);
             below = key_of(T - E2);
@@ -495,10 +628,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         if (!all) {
             band_at = block_scan<NT>(in, warps);
             int to = band_at;
-#pragma unroll
-            for (int i = 0; i < per; ++i) {
-                const uint32_t k = key_at(i);
-                if (k >= below && k <= above) band[to++] = mine + i;
+#pragma unroll 1
+            for (int i = 0; i < per && in > 0; ++i) {
+                const uint32_t k = score_key(i);
+                if (k >= below && k <= above) {
+                    if (n_band <= kSmallBand) small_page[to++] = mine + i;
+                    else band[to++] = mine + i;
+                }
             }
             const int g = p.nq / p.nkv;
             for (int d = tid; d < HD; d += NT) {
@@ -515,7 +651,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
             }
             __syncthreads();
             for (int i = warp; i < n_band; i += W) {
-                const int id = bt[band[i]];
+                const int id = bt[n_band <= kSmallBand ? small_page[i] : band[i]];
                 double e = -INFINITY;
                 if (id >= 0 && id < p.num_blocks) {
                     e = 0.0;
@@ -557,23 +693,36 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         }
     }
     auto exact_key = [&](int i) -> uint64_t { return n_band <= kSmallBand ? small_key[i] : key_of(exact[i]); };
-    // Which of a thread's pages win, in order; a tie at the edge goes to the lower pages.
+    if (K > 0 && all) {
+        // the usual case: the sinks, the newest pages, and what is not a sure loser
+        uint32_t win = 0;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const int page = mine + i;
+            const bool held = page < np && (page < lo || page >= hi);
+            if (held || (f > 0 && key_at(i) >= below)) win |= 1u << i;
+        }
+        int to = block_scan<NT>(__popc(win), warps);
+        for (; win; win &= win - 1) out[to++] = bt[mine + __ffs(win) - 1];
+        return;
+    }
+    // a tie at the edge goes to the lower pages
     int tie_at = 0;
     if (!all) {
         int n = 0, at = band_at;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < per; ++i) {
-            const uint32_t k = key_at(i);
+            const uint32_t k = score_key(i);
             if (k >= below && k <= above) n += exact_key(at++) == edge;
         }
         tie_at = block_scan<NT>(n, warps);
     }
     auto walk = [&](auto emit) {
         int at = band_at, tie = tie_at;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < per; ++i) {
             const int page = mine + i;
-            const uint32_t k = key_at(i);
+            const uint32_t k = score_key(i);
             bool win = page < np && (page < lo || page >= hi);
             if (!win && f > 0 && k > above) win = true;
             if (!win && f > 0 && k >= below && k <= above) {
@@ -583,13 +732,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
                     win = e > edge || (e == edge && tie++ < ties);
                 }
             }
-            if (win) emit(i);
+            if (win) emit(page);
         }
     };
     int n = 0;
     walk([&](int) { ++n; });
     int to = block_scan<NT>(n, warps);
-    walk([&](int i) { out[to++] = K > 0 ? id[i] : bt[mine + i]; });
+    walk([&](int page) { out[to++] = bt[page]; });
 }
 
 // Launches a kernel as a programmatic dependent of the work before it in the stream.
@@ -608,11 +757,19 @@ cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams
 }
 
 template <int HD, bool FP8>
-cudaError_t launch_select(const SelectParams &p, cudaStream_t stream) {
+cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
+    using C = ScoreCfg<HD, FP8>;
+    p.group = C::GROUP;
+    p.groups = (p.max_blocks + C::GROUP - 1) / C::GROUP;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
     if (p.max_blocks > p.max_pages) {
-        const cudaError_t e = launch_after(
-            score_kernel<HD, FP8>,
-            dim3(static_cast<unsigned>((static_cast<int64_t>(p.num_seqs) * p.nkv * p.chunks + 7) / 8)), 256, p, stream);
+        // three CTAs an SM, or a warp for every group there can be
+        const int64_t most = (static_cast<int64_t>(p.num_seqs) * p.nkv * p.groups + 7) / 8;
+        const unsigned grid = static_cast<unsigned>(most < 3 * sms ? most : 3 * sms);
+        e = launch_after(score_kernel<HD, FP8>, dim3(grid), kScoreThreads, p, stream);
         if (e != cudaSuccess) return e;
     }
     // as many threads as a table's pages need at 8 a thread; past 8192 pages (131072 tokens) the
@@ -632,10 +789,10 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t select_layout(int num_seqs, int nkv, int max_blocks, size_t off[4]) {
     const size_t rows = static_cast<size_t>(num_seqs > 0 ? num_seqs : 0) * (nkv > 0 ? nkv : 0);
     const size_t n = rows * (max_blocks > 0 ? max_blocks : 0);
-    const size_t chunks = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kChunk - 1) / kChunk;
+    const size_t groups = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kLeastGroup - 1) / kLeastGroup;
     off[0] = 0;
     off[1] = off[0] + round256(n * 4);
-    off[2] = off[1] + round256(rows * chunks * 4);
+    off[2] = off[1] + round256(rows * groups * 4);
     off[3] = off[2] + round256(n * 4);
     return off[3] + round256(n * 8);
 }
@@ -731,8 +888,6 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     if (num_seqs > 65535 || num_kv_heads > 65535)
         return api_fail(PA_ERR_UNSUPPORTED, "num_seqs %d, num_kv_heads %d: at most 65535", num_seqs,
                         num_kv_heads);
-    if (static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_blocks_per_seq + kChunk - 1) / kChunk) / 8 >= INT32_MAX)
-        return api_fail(PA_ERR_UNSUPPORTED, "too many pages for one launch");
     if (num_seqs == 0) return PA_OK;
     if (!page_tables || !page_lens || !q || !bounds || !block_tables || !seq_lens)
         return api_fail(PA_ERR_INVALID, "null pointer argument");
@@ -761,7 +916,6 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     p.nq = num_q_heads;
     p.nkv = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
-    p.chunks = (max_blocks_per_seq + kChunk - 1) / kChunk;
     p.max_pages = max_pages;
     p.sink = sink_pages;
     p.recent = recent_pages;
@@ -769,12 +923,22 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     if (rc) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    cudaError_t e;
-    switch (head_dim) {
-        case 64: e = fp8 ? launch_select<64, true>(p, s) : launch_select<64, false>(p, s); break;
-        case 128: e = fp8 ? launch_select<128, true>(p, s) : launch_select<128, false>(p, s); break;
-        default: e = fp8 ? launch_select<256, true>(p, s) : launch_select<256, false>(p, s); break;
+    // the score pass holds kScoreSeqs sequences' lengths: more go in several launches
+    for (int at = 0; at < num_seqs; at += kScoreSeqs) {
+        SelectParams a = p;
+        a.num_seqs = num_seqs - at < kScoreSeqs ? num_seqs - at : kScoreSeqs;
+        a.page_tables += static_cast<int64_t>(at) * num_kv_heads * max_pages;
+        a.page_lens += at;
+        a.q += static_cast<int64_t>(at) * num_q_heads * head_dim;
+        a.block_tables += static_cast<int64_t>(at) * max_blocks_per_seq;
+        a.seq_lens += at;
+        cudaError_t e;
+        switch (head_dim) {
+            case 64: e = fp8 ? launch_select<64, true>(a, s) : launch_select<64, false>(a, s); break;
+            case 128: e = fp8 ? launch_select<128, true>(a, s) : launch_select<128, false>(a, s); break;
+            default: e = fp8 ? launch_select<256, true>(a, s) : launch_select<256, false>(a, s); break;
+        }
+        if (e != cudaSuccess) return api_cuda_fail(e, "page selection launch");
     }
-    if (e != cudaSuccess) return api_cuda_fail(e, "page selection launch");
     return PA_OK;
 }
