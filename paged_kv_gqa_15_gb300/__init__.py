@@ -8,6 +8,7 @@ missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -96,13 +97,14 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # ctypes takes a plain address for a void *: no object per argument and call
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def pool_strides(cache: torch.Tensor, layout: str = "HND"):
@@ -387,10 +389,14 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
     pools = [t for kv in zip(key_caches, value_caches) for t in kv]
     nb, nkv, bs, hd = _pool_geometry(pools[0], layout)
     sb, sh, st = pool_strides(pools[0], layout)
-    first = (pools[0].shape, pools[0].stride(), pools[0].dtype)
-    assert all([(t.shape, t.stride(), t.dtype) == first for t in pools]), "pools differ in geometry"
+    # a model has two pools a layer, so the checks go over whole lists
+    n = len(pools)
+    for values in ([t.shape for t in pools], list(map(torch.Tensor.stride, pools)),
+                   [t.dtype for t in pools]):
+        assert values.count(values[0]) == n, "pools differ in geometry"
     assert accepted.dtype == torch.int32 and accepted.is_contiguous()
-    _check(load().pa_tree_commit(_pointer_array(pools), len(pools), _ptr(block_tables),
+    addresses = array.array("Q", list(map(torch.Tensor.data_ptr, pools)))
+    _check(load().pa_tree_commit(addresses.buffer_info()[0], n, _ptr(block_tables),
                                  _ptr(seq_lens), _ptr(qo_indptr), _ptr(accepted),
                                  _ptr(accept_lens), _ptr(new_seq_lens), block_tables.shape[0],
                                  int(max_tree_len), accepted.shape[1], nkv, hd, bs,

@@ -10,10 +10,10 @@
 // than one head, and the pass is bound by reading the bounds (2 head_dim elements a page).
 //
 // Selection is by exact scores.  A score computed in fp32 is off by at most
-//     E = (group + 24) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
-// (P and N are sums of `group` terms; a product is rounded, added in a chain of four, joined
-// by three more sums in the lane and five across lanes; S itself may be 32 roundings off and
-// T +- 2E is rounded: fewer than group + 24 roundings act on any term).  With T the f-th
+//     E = (group + 14) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
+// (P and N are sums of `group` terms of one sign: group - 1 roundings; a product is rounded
+// once, added in a chain of four, joined by three more sums in the lane and five across
+// lanes; T +- 2E is rounded: fewer than group + 14 act on any term).  With T the f-th
 // largest computed score, a page above T + 2E is among the f best and one below T - 2E is
 // not; the band between is scored again in fp64 and ranked by (score, page).
 #include "../../include/pa.h"
@@ -239,6 +239,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
     constexpr int E = FP8 ? 16 : 8;               // elements of a unit
     __shared__ int64_t pref[kScoreSeqs + 1];      // groups before sequence b
     __shared__ int pages[kScoreSeqs];
+    __shared__ int64_t even;                      // groups of a warp's run
+    __shared__ int more;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b = threadIdx.x; b < p.num_seqs; b += kScoreThreads) {
@@ -261,23 +263,27 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
             if (i <= p.num_seqs) pref[i] = v + carry;
             carry += __shfl_sync(kAll, v, 31);
         }
+        if (lane == 0) {
+            const int n_warps = static_cast<int>(gridDim.x) * (kScoreThreads / 32);
+            even = carry / n_warps;
+            more = static_cast<int>(carry - even * n_warps);
+        }
     }
     __syncthreads();
-    const int64_t total = pref[p.num_seqs];
-    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kScoreThreads / 32);
-    // neighbouring runs go to different SMs
-    const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-    int64_t u = total * me / n_warps;
-    const int64_t end = total * (me + 1) / n_warps;
+    // neighbouring runs go to different SMs; the first `more` runs are one group longer
+    const int me = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    int64_t u = even * me + min(me, more);
+    const int64_t end = u + even + (me < more ? 1 : 0);
     if (u >= end) return;
     int b = 0;
     for (int hi = p.num_seqs; hi - b > 1;) {      // the largest b with pref[b] <= u
         const int mid = (b + hi) >> 1;
         if (pref[mid] <= u) b = mid; else hi = mid;
     }
-    int groups = static_cast<int>((pref[b + 1] - pref[b]) / p.nkv);
-    int kh = static_cast<int>((u - pref[b]) / groups);
-    int grp = static_cast<int>(u - pref[b] - static_cast<int64_t>(kh) * groups);
+    int groups = (pages[b] + C::GROUP - 1) / C::GROUP;
+    const int64_t in = u - pref[b];               // below nkv groups
+    int kh = in <= INT32_MAX ? static_cast<int>(in) / groups : static_cast<int>(in / groups);
+    int grp = static_cast<int>(in - static_cast<int64_t>(kh) * groups);
     const int unit = lane % LANES, sub = lane / LANES;
     const int g = p.nq / p.nkv;
     auto page_id = [&](int b, int grp) -> int {
@@ -326,13 +332,20 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
                 for (int h = 0; h < g; ++h) {
 #pragma unroll
                     for (int e0 = 0; e0 < E; e0 += 8) {
+                        // max(q, 0), or max(-q, 0) for N; a NaN stays one
+                        uint4 raw8 = *reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(h) * HD + e0);
+                        const uint32_t turn = low ? 0x80008000u : 0u;
+                        raw8.x = max2<false>(raw8.x ^ turn, 0u), raw8.y = max2<false>(raw8.y ^ turn, 0u);
+                        raw8.z = max2<false>(raw8.z ^ turn, 0u), raw8.w = max2<false>(raw8.w ^ turn, 0u);
                         float f[8];
-                        unpack_bf16x8(*reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(h) * HD + e0), f);
+                        unpack_bf16x8(raw8, f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)   // a NaN goes to P
-                            w[v][e0 + e] += (f[e] < 0.f) == low ? f[e] : 0.f;
+                        for (int e = 0; e < 8; ++e) w[v][e0 + e] += f[e];
                     }
                 }
+                if (low)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) w[v][e] = -w[v][e];
             }
         }
         float x[2 * LOADS];   // the pages' sums, then their sums of magnitudes
@@ -341,15 +354,18 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
             float s = 0.f, a = 0.f;
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) {
-                float f[E], c[4] = {0.f, 0.f, 0.f, 0.f}, t[2] = {0.f, 0.f};   // chains of E / 4 products
+                float f[E], t[2] = {0.f, 0.f};
+                float2 c[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // chains of E / 4 products
                 unpack16<FP8>(raw[k][v], f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = w[v][e] * f[e];
-                    c[e & 3] += y;
-                    t[e & 1] += fabsf(y);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 y = __fmul2_rn(make_float2(w[v][e], w[v][e + 1]), make_float2(f[e], f[e + 1]));
+                    c[e / 2 & 1] = __fadd2_rn(c[e / 2 & 1], y);
+                    t[0] += fabsf(y.x);
+                    t[1] += fabsf(y.y);
                 }
-                s += (c[0] + c[1]) + (c[2] + c[3]);
+                const float2 c2 = __fadd2_rn(c[0], c[1]);
+                s += c2.x + c2.y;
                 a += t[0] + t[1];
             }
             if (a != a) {   // a zero weight met an infinity, or there is a NaN: the exact rule
@@ -395,7 +411,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
         for (int o = 16; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
         if (lane == 0) p.span[row * p.groups + grp] = most;
         fresh = kh1 != kh || b1 != b;
-        if (b1 != b) groups = static_cast<int>((pref[min(b1, p.num_seqs - 1) + 1] - pref[min(b1, p.num_seqs - 1)]) / p.nkv);
+        if (b1 != b) groups = (pages[min(b1, p.num_seqs - 1)] + C::GROUP - 1) / C::GROUP;
         b = b1;
         kh = kh1;
         grp = grp1;
@@ -606,7 +622,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         }
         span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
         const float T = score_of(t);
-        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 24) * 0x1p-24f * span;
+        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 14) * 0x1p-24f * span;
         if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
             above = key_of(T + E2);
             below = key_of(T - E2);
