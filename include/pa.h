@@ -408,7 +408,7 @@ size_t pa_select_pages_workspace_size(int num_seqs, int num_kv_heads, int max_bl
  *                pages' ids in the order of their tokens, then -1
  *   page_lens    [num_seqs] int32, written: the number of tokens those pages hold
  * max_pages > 0, sink_pages >= 0, recent_pages >= 1 (a newest page's bounds may lag its
- * rows), sink_pages + recent_pages <= max_pages.  A page id outside the pool scores
+ * rows), sink_pages + recent_pages <= max_pages, max_blocks_per_seq <= 524288.  A page id outside the pool scores
  * lowest and sets PA_ERR_DEVICE_BOUNDS.
  */
 int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const void *q, const void *bounds,

@@ -155,8 +155,7 @@ struct SelectParams {
     const int32_t *block_tables, *seq_lens;
     float *score;       // [B][nkv][max_blocks]
     float *span;        // [B][nkv][groups]: largest S of a group's pages
-    int32_t *band;      // [B][nkv][max_blocks]
-    double *exact;      // [B][nkv][max_blocks]
+    double *exact;      // [B][nkv][max_blocks], of the pages that are scored again
     int64_t num_blocks;
     int num_seqs, nq, nkv, max_blocks, group, groups, max_pages, sink, recent;   // group: pages of one S
     int *status;
@@ -475,9 +474,9 @@ __device__ __forceinline__ Key nth_largest(Key t, int shift, int f, Sums &sums, 
     return t;
 }
 
-// Exclusive prefix of x over the CTA's NT threads.
+// Exclusive prefix of x over the CTA's NT threads, and the total.
 template <int NT>
-__device__ __forceinline__ int block_scan(int x, int *warps) {
+__device__ __forceinline__ int block_scan(int x, int *warps, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int v = x;
 #pragma unroll
@@ -488,31 +487,44 @@ __device__ __forceinline__ int block_scan(int x, int *warps) {
     __syncthreads();
     if (lane == 31) warps[warp] = v;
     __syncthreads();
-    return __reduce_add_sync(kAll, lane < warp ? warps[lane] : 0) + v - x;
+    const int w = lane < NT / 32 ? warps[lane] : 0;
+    total = __reduce_add_sync(kAll, w);
+    return __reduce_add_sync(kAll, lane < warp ? w : 0) + v - x;
 }
 
-// One CTA per (kv head, sequence).  Thread t owns the K consecutive pages from t K on, so that
-// one scan over the threads gives every chosen page its place; their scores stay in
-// registers (K > 0, up to NT K pages) or are read again from the workspace (K = 0).  The
-// border score comes from a histogram of 2 NT bins spread evenly over the scores' range
-// (scores crowd in few binades, so bins of their bits would not part them) and the order of
-// the few scores in the border's bin.  Where that bin holds more than 32, or scores are
-// not finite, it is found by counting instead, two bits a step below the bits that all
-// candidates share.
-template <int HD, bool FP8, int NT, int K>
-__global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_constant__ SelectParams p) {
+constexpr int kBins = 2048;
+constexpr int kFew = 32;                       // candidates that one warp puts in order
+constexpr int kHeldPages = 40960;              // pages whose scores fit shared memory
+constexpr int kMostPages = 1 << 19;            // pages whose outcome bits do
+
+// Bytes of dynamic shared memory: scores (HELD), then three words per 32 pages.
+size_t select_smem(int max_blocks, bool held) {
+    return (held ? static_cast<size_t>(max_blocks) * 4 : 0) + static_cast<size_t>((max_blocks + 31) / 32) * 12;
+}
+
+// One CTA per (kv head, sequence); all passes go over the pages in the same order, thread t
+// taking pages t, t + NT, ...  The border score comes from a histogram of even bins over the
+// scores' range (scores crowd in few binades, so bins of their bits would not part them)
+// and the order of the few scores in the border's bin.  Where that bin holds more than 32, or
+// scores are not finite, it is found by counting instead, two bits a step below the bits that
+// all candidates share.  A page's outcome is a bit of its warp's word; one scan over the words'
+// counts gives every chosen page its place, in page order.  A row is one pass of dependent
+// steps, bound by their latency (a dozen barriers) and not by its 32 KB of scores: short loops
+// rather than unrolled code, whose instruction fetches showed.
+template <int HD, bool FP8, int NT, bool HELD>
+__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
     constexpr int W = NT / 32;
-    constexpr int kSmallBand = 32;
+    extern __shared__ uint32_t dyn[];
     __shared__ int sums_sh[2 * 3 * 32];
     __shared__ int warps[32];
     __shared__ uint32_t ends[3][32];
     __shared__ double P[HD], N[HD];
-    __shared__ uint64_t small_key[kSmallBand];
-    __shared__ int small_page[kSmallBand];
-    __shared__ int hist[2 * NT];
-    __shared__ uint32_t bin_key[32];
-    __shared__ int bin_at, bin_above, bin_n;
+    __shared__ int hist[kBins];
+    __shared__ uint32_t bin_key[kFew];
+    __shared__ uint64_t few_key[kFew];
+    __shared__ int few_page[kFew];
+    __shared__ int bin_at, bin_above, bin_n, few_n;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = select_len(p, b, false);
@@ -530,23 +542,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
     // f pages of [lo, hi) join the sinks and the newest ones
     const int lo = p.sink, hi = np - p.recent, f = p.max_pages - p.sink - p.recent;
     const float *score = p.score + row * p.max_blocks;
-    const int per = K > 0 ? K : (np + NT - 1) / NT;
-    const int mine = tid * per;
-    uint32_t key[K > 0 ? K : 1];                // 0 for pages that are not candidates
-    if constexpr (K > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) key[i] = mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
-    }
-    hist[2 * tid] = hist[2 * tid + 1] = 0;
-    if (tid == 0) bin_n = 0;
-    float span = 0.f;                           // S of the bound E
-    for (int i = tid; i < (np + p.group - 1) / p.group; i += NT) span = max_nan(span, p.span[row * p.groups + i]);
-    auto key_at = [&](int i) -> uint32_t {      // of page mine + i
-        if constexpr (K > 0) return key[i];
-        else return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
-    };
-    auto score_key = [&](int i) -> uint32_t {   // the same from memory: for loops that are not unrolled
-        return mine + i >= lo && mine + i < hi ? key_of(score[mine + i]) : 0u;
+    uint32_t *keys = dyn;                              // 0 for pages that are not candidates
+    uint32_t *words = dyn + (HELD ? p.max_blocks : 0); // outcome bits of 32 pages
+    const int n_words = (np + 31) / 32;
+    uint32_t *tie_words = words + (p.max_blocks + 31) / 32;
+    int *places = reinterpret_cast<int *>(tie_words + (p.max_blocks + 31) / 32);
+    auto key_at = [&](int i) -> uint32_t {
+        if constexpr (HELD) return keys[i];
+        else return i >= lo && i < hi ? key_of(score[i]) : 0u;
     };
     BlockSums<NT> sums{sums_sh, 0};
     // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
@@ -554,16 +557,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
     bool all = true;                            // the whole band wins
     uint64_t edge = 0;                          // else the weakest exact score that wins ...
     int ties = 0;                               // ... and how many equal to it do
-    int band_at = 0, n_band = 0;                // band members before this thread's, and in all
-    int32_t *band = p.band + row * p.max_blocks;
     double *exact = p.exact + row * p.max_blocks;
     if (f > 0) {
         uint32_t least = 0xffffffffu, top = 0u;
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const uint32_t k = key_at(i);
+        float span = 0.f;                       // S of the bound E
+        for (int i = tid; i < (np + p.group - 1) / p.group; i += NT) span = max_nan(span, p.span[row * p.groups + i]);
+#pragma unroll 8
+        for (int i = tid; i < np; i += NT) {   // loads that wait for nothing: many at once
+            const uint32_t k = i >= lo && i < hi ? key_of(score[i]) : 0u;
+            if constexpr (HELD) keys[i] = k;
             if (k) least = min(least, k), top = max(top, k);
         }
+        for (int i = tid; i < kBins; i += NT) hist[i] = 0;
+        if (tid == 0) bin_n = few_n = 0;
         least = __reduce_min_sync(kAll, least);
         top = __reduce_max_sync(kAll, top);
         const uint32_t wide = __reduce_max_sync(kAll, key_of(span));   // a NaN is the largest
@@ -571,33 +577,38 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         __syncthreads();
         least = __reduce_min_sync(kAll, lane < W ? ends[0][lane] : 0xffffffffu);
         top = __reduce_max_sync(kAll, lane < W ? ends[1][lane] : 0u);
+        span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
         // bins over [low, low + range], monotone in the score as each rounding is
-        const float low = score_of(least), scale = (2 * NT - 1) / (score_of(top) - low);
-        auto bin_of = [&](uint32_t k) { return min(2 * NT - 1, static_cast<int>((score_of(k) - low) * scale)); };
+        const float low = score_of(least), scale = (kBins - 1) / (score_of(top) - low);
+        auto bin_of = [&](uint32_t k) { return min(kBins - 1, static_cast<int>((score_of(k) - low) * scale)); };
         uint32_t t = 0;
         bool found = isfinite(scale) && scale > 0.f && top < 0xff800000u && least > 0x007fffffu;
         if (found) {
-#pragma unroll
-            for (int i = 0; i < per; ++i) {
+#pragma unroll 4
+            for (int i = tid; i < np; i += NT) {
                 const uint32_t k = key_at(i);
                 if (k) atomicAdd(&hist[bin_of(k)], 1);
             }
             __syncthreads();
-            const int hi_bin = 2 * (NT - 1 - tid) + 1;    // from the top: two bins a thread
-            const int c1 = hist[hi_bin], c0 = hist[hi_bin - 1];
-            const int before = block_scan<NT>(c1 + c0, warps);
-            if (before < f && f <= before + c1 + c0) {
-                const bool first = f <= before + c1;
-                bin_at = first ? hi_bin : hi_bin - 1;
-                bin_above = first ? before : before + c1;
+            constexpr int EACH = kBins / NT;
+            const int first_bin = kBins - 1 - tid * EACH;   // from the top, EACH bins a thread
+            int c = 0, total;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) c += hist[first_bin - i];
+            int before = block_scan<NT>(c, warps, total);
+            if (before < f && f <= before + c) {
+                int at = first_bin;
+                while (before + hist[at] < f) before += hist[at--];
+                bin_at = at;
+                bin_above = before;
             }
             __syncthreads();
             const int bin = bin_at;
-            if (hist[bin] > 32) {
+            if (hist[bin] > kFew) {
                 found = false;
             } else {
-#pragma unroll
-                for (int i = 0; i < per; ++i) {
+#pragma unroll 4
+                for (int i = tid; i < np; i += NT) {
                     const uint32_t k = key_at(i);
                     if (k && bin_of(k) == bin) bin_key[atomicAdd(&bin_n, 1)] = k;
                 }
@@ -616,11 +627,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
         if (!found) {
             const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
             t = nth_largest<uint32_t>(bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
-#pragma unroll 1
-                for (int i = 0; i < per; ++i) c += score_key(i) >= x;
+                for (int i = tid; i < np; i += NT) c += key_at(i) >= x;
             });
         }
-        span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
         const float T = score_of(t);
         const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 14) * 0x1p-24f * span;
         if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
@@ -630,28 +639,20 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
             below = 1u;
         }
         int c[3] = {0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
+#pragma unroll 4
+        for (int i = tid; i < np; i += NT) {
             const uint32_t k = key_at(i);
             c[0] += k > above;
-            c[1] += k >= below && k <= above;
+            if (k >= below && k <= above) {
+                ++c[1];
+                const int at = atomicAdd(&few_n, 1);
+                if (at < kFew) few_page[at] = i;
+            }
         }
-        const int in = c[1];
         sums(c);
-        const int take = f - c[0];               // winners that come from the band
-        n_band = c[1];
+        const int take = f - c[0], n_band = c[1];   // winners that come from the band, and its size
         all = take == n_band;
         if (!all) {
-            band_at = block_scan<NT>(in, warps);
-            int to = band_at;
-#pragma unroll 1
-            for (int i = 0; i < per && in > 0; ++i) {
-                const uint32_t k = score_key(i);
-                if (k >= below && k <= above) {
-                    if (n_band <= kSmallBand) small_page[to++] = mine + i;
-                    else band[to++] = mine + i;
-                }
-            }
             const int g = p.nq / p.nkv;
             for (int d = tid; d < HD; d += NT) {
                 const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
@@ -666,103 +667,129 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
                 N[d] = y;
             }
             __syncthreads();
-            for (int i = warp; i < n_band; i += W) {
-                const int id = bt[n_band <= kSmallBand ? small_page[i] : band[i]];
-                double e = -INFINITY;
-                if (id >= 0 && id < p.num_blocks) {
-                    e = 0.0;
-                    const uint8_t *r = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
+            // page i's score in fp64, by one warp
+            auto exact_score = [&](int i) -> double {
+                const int id = bt[i];
+                if (id < 0 || id >= p.num_blocks) return -INFINITY;
+                const uint8_t *r = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
+                double e = 0.0;
 #pragma unroll
-                    for (int d = 0; d < HD; d += 32)
-                        e += weighed<double>(P[d + lane], bound_value<FP8>(r + ROW, d + lane)) +
-                             weighed<double>(N[d + lane], bound_value<FP8>(r, d + lane));
+                for (int d = 0; d < HD; d += 32)
+                    e += weighed<double>(P[d + lane], bound_value<FP8>(r + ROW, d + lane)) +
+                         weighed<double>(N[d + lane], bound_value<FP8>(r, d + lane));
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(kAll, e, o);
+                for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(kAll, e, o);
+                return e;
+            };
+            if (n_band <= kFew) {
+                for (int i = warp; i < n_band; i += W) {
+                    const double e = exact_score(few_page[i]);
+                    if (lane == 0) {
+                        few_key[i] = key_of(e);
+                        exact[few_page[i]] = e;
+                    }
                 }
-                if (lane == 0) {
-                    if (n_band <= kSmallBand) small_key[i] = key_of(e);
-                    else exact[i] = e;
-                }
-            }
-            __syncthreads();
-            if (n_band <= kSmallBand) {
-                // the take-th of the band in the order (score, lower page first): a member's
-                // place is the number of those before it
-                const uint64_t k = lane < n_band ? small_key[lane] : 0ull;
+                __syncthreads();
+                // the take-th of the band: a member's place is the number of those before it
+                const uint64_t k = lane < n_band ? few_key[lane] : 0ull;
                 int place = 0;
                 for (int i = 0; i < n_band; ++i) {
-                    const uint64_t o = small_key[i];
+                    const uint64_t o = few_key[i];
                     place += o > k || (o == k && i < lane);
                 }
                 const int who = __ffs(__ballot_sync(kAll, lane < n_band && place == take - 1)) - 1;
-                edge = small_key[who];
+                edge = few_key[who];
                 ties = take - __popc(__ballot_sync(kAll, lane < n_band && k > edge));
             } else {
-                edge = nth_largest<uint64_t>(0ull, 64, take, sums, [&](uint64_t x, int &n) {
-                    for (int i = tid; i < n_band; i += NT) n += key_of(exact[i]) >= x;
-                });
+                for (int base = warp * 32; base < np; base += NT) {
+                    const uint32_t mine = base + lane < np ? key_at(base + lane) : 0u;
+                    for (unsigned m = __ballot_sync(kAll, mine >= below && mine <= above); m; m &= m - 1) {
+                        const int i = base + __ffs(m) - 1;
+                        const double e = exact_score(i);
+                        if (lane == 0) exact[i] = e;
+                    }
+                }
+                __syncthreads();
+                auto count = [&](uint64_t x, int &n, bool strict) {
+                    for (int i = tid; i < np; i += NT) {
+                        const uint32_t k = key_at(i);
+                        if (k < below || k > above) continue;
+                        const uint64_t e = key_of(exact[i]);
+                        n += strict ? e > x : e >= x;
+                    }
+                };
+                edge = nth_largest<uint64_t>(0ull, 64, take, sums, [&](uint64_t x, int &n) { count(x, n, false); });
                 int n[3] = {0, 0, 0};
-                for (int i = tid; i < n_band; i += NT) n[0] += key_of(exact[i]) > edge;
+                count(edge, n[0], true);
                 sums(n);
                 ties = take - n[0];
             }
         }
     }
-    auto exact_key = [&](int i) -> uint64_t { return n_band <= kSmallBand ? small_key[i] : key_of(exact[i]); };
-    if (K > 0 && all) {
-        // the usual case: the sinks, the newest pages, and what is not a sure loser
-        uint32_t win = 0;
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const int page = mine + i;
-            const bool held = page < np && (page < lo || page >= hi);
-            if (held || (f > 0 && key_at(i) >= below)) win |= 1u << i;
-        }
-        int to = block_scan<NT>(__popc(win), warps);
-        for (; win; win &= win - 1) out[to++] = bt[mine + __ffs(win) - 1];
-        return;
-    }
-    // a tie at the edge goes to the lower pages
-    int tie_at = 0;
-    if (!all) {
-        int n = 0, at = band_at;
-#pragma unroll 1
-        for (int i = 0; i < per; ++i) {
-            const uint32_t k = score_key(i);
-            if (k >= below && k <= above) n += exact_key(at++) == edge;
-        }
-        tie_at = block_scan<NT>(n, warps);
-    }
-    auto walk = [&](auto emit) {
-        int at = band_at, tie = tie_at;
-#pragma unroll 1
-        for (int i = 0; i < per; ++i) {
-            const int page = mine + i;
-            const uint32_t k = score_key(i);
-            bool win = page < np && (page < lo || page >= hi);
-            if (!win && f > 0 && k > above) win = true;
-            if (!win && f > 0 && k >= below && k <= above) {
-                win = all;
-                if (!all) {
-                    const uint64_t e = exact_key(at++);
-                    win = e > edge || (e == edge && tie++ < ties);
-                }
+    // the outcome of every page
+    for (int base = warp * 32; base < np; base += NT) {
+        const int i = base + lane;
+        bool win = i < np && (i < lo || i >= hi), tie = false;
+        if (i < np && !win && f > 0) {
+            const uint32_t k = key_at(i);
+            win = k > above;
+            if (!win && k >= below) {   // in the band
+                const uint64_t e = all ? 1ull : key_of(exact[i]);
+                win = all || e > edge;
+                tie = !all && e == edge;
             }
-            if (win) emit(page);
         }
-    };
+        const unsigned w = __ballot_sync(kAll, win), t = __ballot_sync(kAll, tie);
+        if (lane == 0) {
+            words[base / 32] = w;
+            if (!all) tie_words[base / 32] = t;
+        }
+    }
+    __syncthreads();
+    // every thread takes `each` consecutive words
+    const int each = (n_words + NT - 1) / NT, w0 = min(tid * each, n_words), w1 = min(w0 + each, n_words);
+    int total;
+    if (!all) {   // of the pages that tie at the edge, the lowest `ties` win
+        int n = 0;
+        for (int i = w0; i < w1; ++i) n += __popc(tie_words[i]);
+        int left = ties - block_scan<NT>(n, warps, total);
+        for (int i = w0; i < w1 && left > 0; ++i)
+            for (uint32_t t = tie_words[i]; t && left > 0; t &= t - 1, --left) words[i] |= t & -t;
+    }
     int n = 0;
-    walk([&](int) { ++n; });
-    int to = block_scan<NT>(n, warps);
-    walk([&](int page) { out[to++] = bt[page]; });
+    for (int i = w0; i < w1; ++i) n += __popc(words[i]);
+    int at = block_scan<NT>(n, warps, total);
+    for (int i = w0; i < w1; ++i) {
+        places[i] = at;
+        at += __popc(words[i]);
+    }
+    __syncthreads();
+    // The winners' numbers first (over the scores, which have done their work), so that each
+    // thread then waits for one block-table read and not for one per word of its warp.
+    int *won = reinterpret_cast<int *>(keys);
+    for (int base = warp * 32; base < np; base += NT) {
+        const uint32_t w = words[base / 32];
+        if (w >> lane & 1) {
+            const int to = places[base / 32] + __popc(w & ((1u << lane) - 1));
+            if constexpr (HELD) won[to] = base + lane;
+            else out[to] = bt[base + lane];
+        }
+    }
+    if constexpr (HELD) {
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < kept; i += NT) out[i] = bt[won[i]];
+    }
 }
 
 // Launches a kernel as a programmatic dependent of the work before it in the stream.
 template <typename Kernel>
-cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams &p, cudaStream_t stream) {
+cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams &p, cudaStream_t stream,
+                         size_t smem = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -788,29 +815,32 @@ cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
         e = launch_after(score_kernel<HD, FP8>, dim3(grid), kScoreThreads, p, stream);
         if (e != cudaSuccess) return e;
     }
-    // as many threads as a table's pages need at 8 a thread; past 8192 pages (131072 tokens) the
-    // scores no longer fit the registers
     const dim3 grid(p.nkv, p.num_seqs);
-    if (p.max_blocks <= 2048) return launch_after(select_kernel<HD, FP8, 256, 8>, grid, 256, p, stream);
-    if (p.max_blocks <= 4096) return launch_after(select_kernel<HD, FP8, 512, 8>, grid, 512, p, stream);
-    if (p.max_blocks <= 8192) return launch_after(select_kernel<HD, FP8, 1024, 8>, grid, 1024, p, stream);
-    return launch_after(select_kernel<HD, FP8, 1024, 0>, grid, 1024, p, stream);
+    const bool held = p.max_blocks <= kHeldPages;
+    const size_t smem = select_smem(p.max_blocks, held);
+    auto select = [&](auto kern, int threads) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        return e != cudaSuccess ? e : launch_after(kern, grid, threads, p, stream, smem);
+    };
+    // short tables: fewer warps to wait for at each barrier
+    if (p.max_blocks <= 1024) return select(select_kernel<HD, FP8, 256, true>, 256);
+    return held ? select(select_kernel<HD, FP8, 512, true>, 512) : select(select_kernel<HD, FP8, 512, false>, 512);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Offsets of the workspace's parts (scores, spans, band, exact scores) and its size.
-size_t select_layout(int num_seqs, int nkv, int max_blocks, size_t off[4]) {
+// Offsets of the workspace's parts (scores, spans, exact scores) and its size.
+size_t select_layout(int num_seqs, int nkv, int max_blocks, size_t off[3]) {
     const size_t rows = static_cast<size_t>(num_seqs > 0 ? num_seqs : 0) * (nkv > 0 ? nkv : 0);
     const size_t n = rows * (max_blocks > 0 ? max_blocks : 0);
     const size_t groups = (static_cast<size_t>(max_blocks > 0 ? max_blocks : 0) + kLeastGroup - 1) / kLeastGroup;
     off[0] = 0;
     off[1] = off[0] + round256(n * 4);
     off[2] = off[1] + round256(rows * groups * 4);
-    off[3] = off[2] + round256(n * 4);
-    return off[3] + round256(n * 8);
+    return off[2] + round256(n * 8);
 }
 
 }  // namespace
@@ -873,7 +903,7 @@ extern "C" int pa_page_bounds(void *bounds, const void *k_cache, const int32_t *
 
 extern "C" size_t pa_select_pages_workspace_size(int num_seqs, int num_kv_heads,
                                                  int max_blocks_per_seq) {
-    size_t off[4];
+    size_t off[3];
     return pa::select_layout(num_seqs, num_kv_heads, max_blocks_per_seq, off);
 }
 
@@ -895,6 +925,8 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     if (num_blocks <= 0) return api_fail(PA_ERR_INVALID, "num_blocks %lld", (long long)num_blocks);
     if (max_blocks_per_seq <= 0 || max_blocks_per_seq > INT32_MAX / kBlockSize)
         return api_fail(PA_ERR_INVALID, "max_blocks_per_seq %d", max_blocks_per_seq);
+    if (max_blocks_per_seq > kMostPages)
+        return api_fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq %d > %d", max_blocks_per_seq, kMostPages);
     if (max_pages <= 0 || max_pages > INT32_MAX / kBlockSize)
         return api_fail(PA_ERR_INVALID, "max_pages %d", max_pages);
     if (sink_pages < 0 || recent_pages < 1 || sink_pages > max_pages ||
@@ -909,7 +941,7 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
         return api_fail(PA_ERR_INVALID, "null pointer argument");
     if (!aligned(q, 16) || !aligned(bounds, 16))
         return api_fail(PA_ERR_INVALID, "q and bounds must be 16-byte aligned");
-    size_t off[4];
+    size_t off[3];
     const size_t need = select_layout(num_seqs, num_kv_heads, max_blocks_per_seq, off);
     if (workspace_bytes < need)
         return api_fail(PA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -925,8 +957,7 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     p.seq_lens = seq_lens;
     p.score = reinterpret_cast<float *>(ws + off[0]);
     p.span = reinterpret_cast<float *>(ws + off[1]);
-    p.band = reinterpret_cast<int32_t *>(ws + off[2]);
-    p.exact = reinterpret_cast<double *>(ws + off[3]);
+    p.exact = reinterpret_cast<double *>(ws + off[2]);
     p.num_blocks = num_blocks;
     p.num_seqs = num_seqs;
     p.nq = num_q_heads;

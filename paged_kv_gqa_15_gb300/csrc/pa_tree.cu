@@ -31,11 +31,17 @@
 //    and rows see different nodes.  So in those tiles the softmax warps also clean V: rows
 //    past the sequence are zeroed, and non-finite elements of partly seen rows are zeroed and
 //    noted, to be added in the epilogue to the rows that do see them.
-//  * 8-bit caches (FP8): K and V tiles go to the 8-bit tensor cores as they are.  q is split
-//    into two E4M3 rows, q s = hi + lo with s a power of two that puts the row's largest |q s|
-//    in [128, 256), and P into hi + lo of 256 p, each pair good to 2^-8 of its value; two
-//    MMAs with the same B operand add up S (and O), at twice the bf16 rate each.  A row's
-//    maximum may then lag by a factor 1.75 at most, so 256 p stays within E4M3's 448.
+//  * 8-bit caches (FP8): K and V tiles go to the 8-bit tensor cores as they are, and MMAs with
+//    the same B operand add up the terms of the other.  q is split into two E4M3 rows, q s =
+//    hi + lo with s a power of two that puts the row's largest |q s| in [128, 256): the pair
+//    holds q to 2^-8 of its value.  P is split into three E5M2 terms: an f16 value's upper byte
+//    is an E5M2 value, so each term is a mask and a subtraction and four of them one byte
+//    permutation.  Three terms hold at least 9 bits (2^-8 of P, mostly better) over f16's range.
+//    P as E4M3 pairs needs four conversions per pair of weights (the ALU pipe is what bounds
+//    this softmax), and reaches from 448 to 2^-9 only, so that every growth of a row's maximum by
+//    a factor 1.75 rescaled O and weights far under one large maximum lost their bits: 154 us for
+//    32 sequences of 1k-8k and 64-node trees.  Two more warps turning V into f16 left too little
+//    shared memory for tiles on their way: 261 us.
 //  * Every mbarrier wait is bounded.
 #include <cuda.h>
 
@@ -179,10 +185,17 @@ __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, 
 struct TreeShares {
     const int64_t *pref;   // [n + 1] tiles before sequence b
     const int *run;        // [n] tiles of each of sequence b's runs
-    int64_t total;
-    int n, shares;
+    int64_t total, even;   // total = even * shares + more
+    int n, shares, more;
     bool whole;
 
+    // x / d and x % d, in 32 bits where they do (64-bit division is a hundred instructions)
+    static __device__ __forceinline__ int quotient(int64_t x, int d) {
+        return x <= INT32_MAX ? static_cast<int>(x) / d : static_cast<int>(x / d);
+    }
+    static __device__ __forceinline__ int remainder(int64_t x, int d) {
+        return x <= INT32_MAX ? static_cast<int>(x) % d : static_cast<int>(x % d);
+    }
     // the largest b with pref[b] <= u
     __device__ __forceinline__ int sequence(int64_t u) const {
         int lo = 0, hi = n;
@@ -194,10 +207,10 @@ struct TreeShares {
     }
     __device__ __forceinline__ int64_t begin(int c) const {
         if (c >= shares) return total;
-        const int64_t u = total * c / shares;
+        const int64_t u = even * c + min(c, more);
         if (!whole || u <= 0) return u;
         const int b = sequence(u);
-        const int r = static_cast<int>((u - pref[b]) % run[b]);
+        const int r = remainder(u - pref[b], run[b]);
         return 2 * r >= run[b] ? u - r + run[b] : u - r;
     }
 };
@@ -268,17 +281,20 @@ __device__ __forceinline__ bool drop_non_finite(uint4 &v) {
     return any;
 }
 
-// Two P values (at most 448) as E4M3 pairs: x = hi + lo to 2^-8 of x, by way of f16.
-__device__ __forceinline__ void split_e4m3x2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    unsigned short h, l;
-    uint32_t v, b;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(y), "f"(x));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(v));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(b));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(v));
-    hi = h;
-    lo = l;
+// Four P values (0 to 2^15) as E5M2 codes of three terms that add up to them: by way of f16,
+// whose upper byte is the value cut to E5M2; what is cut off goes to the next term, exactly.
+__device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float x3, uint32_t (&t)[3]) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x1), "f"(x0));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x3), "f"(x2));
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        t[i] = __byte_perm(a, b, 0x7531);   // the upper bytes
+        if (i == 2) break;
+        const uint32_t ta = a & 0xff00ff00u, tb = b & 0xff00ff00u;
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(ta));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(tb));
+    }
 }
 
 template <int HD, bool FP8>
@@ -352,16 +368,17 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    TreeShares line{pref, run, pref[p.num_seqs], p.num_seqs, static_cast<int>(gridDim.x), false};
+    TreeShares line{pref, run, pref[p.num_seqs], 0, p.num_seqs, static_cast<int>(gridDim.x), 0, false};
     if (line.total < line.shares) line.shares = max(1, static_cast<int>(line.total));
+    line.even = line.total <= INT32_MAX ? static_cast<int>(line.total) / line.shares : line.total / line.shares;
+    line.more = static_cast<int>(line.total - line.even * line.shares);
     {
         // Shares of whole runs hold at most one run when there are no more runs than shares, else
         // an even share and a run; cutting costs a partial tile's round trip and the join,
         // as much as about kCutTiles tiles.
-        const int64_t even = line.total / line.shares;
         const int64_t longest = run[p.num_seqs];
-        const int64_t most = even < longest ? longest : even + longest;
-        line.whole = most <= even + kCutTiles;
+        const int64_t most = line.even < longest ? longest : line.even + longest;
+        line.whole = most <= line.even + kCutTiles;
     }
     const int64_t u_begin = line.begin(blockIdx.x);
     const int64_t u_end = line.begin(blockIdx.x + 1);
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         uint32_t n_k = 0, n_v = 0, n_q = 0;   // copies issued (for the drain on an abort)
         int stop = 0;
         int64_t u = u_begin;
-        bool joined = false;                  // this share joins a cut run
+        int64_t run_begin = -1, run_end = -1; // of a run that began in a share before
         // Publishes the next segment of the share (or the end) and returns it.
         auto next_segment = [&]() -> TreeSegment {
             const int slot = n_seg & 3;
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const int tiles = run[lo];
                 const int row_tiles = (q.T + a.nodes - 1) / a.nodes;
                 const int64_t rel = u - pref[lo];
-                const int item = static_cast<int>(rel / tiles);
+                const int item = TreeShares::quotient(rel, tiles);
                 const int j = static_cast<int>(rel - static_cast<int64_t>(item) * tiles);
                 s.b = lo;
                 s.head = item / row_tiles;
@@ -396,12 +413,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 s.n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
                 s.j0 = tree_first_key(q, p.window) / kKeys + j;
                 s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
-                if (j > 0 && u - j >= line.begin(blockIdx.x - 1)) {
-                    // the share before holds the run's first piece: this one has it joined
-                    TreeCut cut = {2, s.n_nodes * a.group, s.head, s.row0 + s.node0};
-                    while (line.begin(blockIdx.x - 1 + cut.pieces) < u - j + tiles) ++cut.pieces;
-                    if (lane == 0) a.cuts[blockIdx.x] = cut;
-                    joined = true;
+                if (j > 0) {   // only in the share's first segment
+                    run_begin = u - j;
+                    run_end = run_begin + tiles;
                 }
                 if (p.window > 0) {   // pages before the first key a row does see are not looked up
                     int least = 1 << 30;
@@ -434,7 +448,20 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         };
         const uint64_t policy = l2_policy_evict_first();
         TreeSegment w = next_segment();
-        if (!joined && lane == 0) a.cuts[blockIdx.x] = TreeCut{};
+        const TreeCut run_cut = {2, w.n_nodes * a.group, w.head, w.row0 + w.node0};
+        bool noted = false;
+        // Where the share before holds the run's first piece, this one has it joined; written
+        // behind the first loads, since nothing here waits for it.
+        auto note_cut = [&]() {
+            if (noted) return;
+            noted = true;
+            TreeCut cut = {};
+            if (run_begin >= 0 && run_begin >= line.begin(blockIdx.x - 1)) {
+                cut = run_cut;
+                while (line.begin(blockIdx.x - 1 + cut.pieces) < run_end) ++cut.pieces;
+            }
+            if (lane == 0) a.cuts[blockIdx.x] = cut;
+        };
         while (!stop && w.n >= 0) {
             const int kvh = w.head / a.kv_rep;
             if (!FP8) {
@@ -484,6 +511,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             load(0, g, page);
             const TreeSegment next = stop ? w : next_segment();
             for (int j = 0; j < w.n && !stop; ++j) {
+                if (j == 1) note_cut();
                 int page_next = 0;
                 if (j + 1 < w.n) {
                     page_next = page_fix(raw, g + j + 1);
@@ -496,6 +524,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             g += w.n;
             w = next;
         }
+        note_cut();
         // never leave the CTA with copies still landing in its shared memory
         if (lane == 0 && (stop || *abort_flag)) {
             auto settle = [&](uint64_t *full, int ns, uint32_t n) {
@@ -514,7 +543,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         if (lane == 0) {
             constexpr uint32_t idesc_s = FP8 ? idesc_f32(kRows, kKeys, 0, 0, false, false)
                                              : idesc_bf16_f32(kRows, kKeys, false, false);
-            constexpr uint32_t idesc_o = FP8 ? idesc_f32(kRows, HD, 0, 0, false, true)
+            // P: three terms of E5M2 (format 1)
+            constexpr uint32_t idesc_o = FP8 ? idesc_f32(kRows, HD, 1, 0, false, true)
                                              : idesc_bf16_f32(kRows, HD, false, true);
             constexpr int KB = 32;                         // bytes of K per MMA
             constexpr int PER_CHUNK = C::ROWB / KB;        // MMAs per chunk of a row
@@ -537,7 +567,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const uint64_t vd = v_desc + ((s * C::KV_BYTES) >> 4);
                 const uint32_t pt = tmem + (t & 1) * kKeys;
 #pragma unroll
-                for (int part = 0; part < (FP8 ? 2 : 1); ++part)
+                for (int part = 0; part < (FP8 ? 3 : 1); ++part)
 #pragma unroll
                     for (int kk = 0; kk < kKeys / PV_ROWS; ++kk) {
                         const uint64_t d = vd + ((kk * PV_ROWS * C::ROWB) >> 4);
@@ -598,10 +628,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         const int row = quad * 32 + lane;          // row of the tile
         const int tid = threadIdx.x - 64;          // 0 .. 127 over the softmax warps
         const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-        // A row's maximum moves only when it grows by more than `lag` (log2 units): O is then
-        // rescaled rarely.  bf16 holds any P; E4M3 holds 256 p <= 448 only.
-        constexpr float lag = FP8 ? 0.8f : 8.f;
-        constexpr float lift = FP8 ? 8.f : 0.f;    // P is 2^(x - m + lift)
+        // A row's maximum moves only when it grows by more than 2^8: O is then rescaled rarely,
+        // and bf16 holds any P.  FP8: 2^(8 + 7) is within f16 and E5M2, whose smallest step is 2^-16.
+        constexpr float lag = 8.f;
+        constexpr float lift = FP8 ? 7.f : 0.f;    // P is 2^(x - m + lift)
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t k = 0;; ++k) {
@@ -780,34 +810,37 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                     }
                     // P = 2^(s scale - m + lift); the sum takes the unrounded values
                     const float sub = m == -INFINITY ? 0.f : m - lift;
-                    uint32_t pk[32];
+                    constexpr int P_WORDS = FP8 ? 48 : 32;
+                    uint32_t pk[P_WORDS];
                     float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                      make_float2(0.f, 0.f)};
                     const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-sub, -sub);
 #pragma unroll
-                    for (int c = 0; c < kKeys / 2; ++c) {
-                        const float2 x = __ffma2_rn(
-                            make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2);
-                        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum[c & 3] = __fadd2_rn(sum[c & 3], e);
+                    for (int c = 0; c < kKeys / 2; c += 2) {
+                        float2 e[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * (c + i)]),
+                                                                    __uint_as_float(sr[2 * (c + i) + 1])), sc2, nm2);
+                            e[i] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            sum[(c + i) & 3] = __fadd2_rn(sum[(c + i) & 3], e[i]);
+                        }
                         if constexpr (FP8) {
-                            uint32_t hi, lo;
-                            split_e4m3x2(e.x, e.y, hi, lo);
-                            if (c & 1) {
-                                pk[c / 2] |= hi << 16;
-                                pk[16 + c / 2] |= lo << 16;
-                            } else {
-                                pk[c / 2] = hi;
-                                pk[16 + c / 2] = lo;
-                            }
+                            uint32_t t3[3];
+                            split_e5m2x4(e[0].x, e[0].y, e[1].x, e[1].y, t3);
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) pk[i * 16 + c / 2] = t3[i];
                         } else {
-                            pk[c] = pack_bf16x2(e.x, e.y);
+                            pk[c] = pack_bf16x2(e[0].x, e[0].y);
+                            pk[c + 1] = pack_bf16x2(e[1].x, e[1].y);
                         }
                     }
                     const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
                     const float2 st = __fadd2_rn(s01, s23);
                     l += st.x + st.y;
-                    tmem_store_32(tmem + t_lane + s_col, pk);
+                    tmem_store_32(tmem + t_lane + s_col, *reinterpret_cast<uint32_t (*)[32]>(&pk[0]));
+                    if constexpr (FP8)
+                        tmem_store_16(tmem + t_lane + s_col + 32, *reinterpret_cast<uint32_t (*)[16]>(&pk[32]));
                     tmem_store_wait();
                 }
                 tc_fence_before_sync();

@@ -135,6 +135,7 @@ def test_bounds_refusals(lib, kw, code):
     (dict(bs=32), pa.PA_ERR_UNSUPPORTED),
     (dict(nb=0), pa.PA_ERR_INVALID),
     (dict(mb=0), pa.PA_ERR_INVALID),
+    (dict(mb=524289), pa.PA_ERR_UNSUPPORTED),
     (dict(most=0), pa.PA_ERR_INVALID),
     (dict(most=1 << 28), pa.PA_ERR_INVALID),
     (dict(sink=-1), pa.PA_ERR_INVALID),

@@ -154,6 +154,19 @@ def test_selection_is_exact(i, fp8):
     assert pa.device_status() == 0
 
 
+def test_selection_in_a_table_wider_than_its_sequences():
+    """Tables of 50000 entries, whose scores no longer fit shared memory."""
+    c = make([3000, 700], 8, 2, 64, 47)
+    fill_bounds(c)
+    want = ref64.select(c["q"], c["bounds"], c["table"].cpu(), c["lens"].cpu(), 20, 1, 2)
+    wide = torch.full((2, 50000), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = wide
+    pages, lens = select(c, 20, 1, 2)
+    assert torch.equal(pages.cpu(), want[0]) and torch.equal(lens.cpu(), want[1])
+    assert pa.device_status() == 0
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_equal_scores_go_to_the_lower_page(fp8):
     c = make([1600, 800], 8, 2, 128, 50, fp8)
