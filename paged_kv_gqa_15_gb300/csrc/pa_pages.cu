@@ -496,10 +496,17 @@ constexpr int kBins = 2048;
 constexpr int kFew = 32;                       // candidates that one warp puts in order
 constexpr int kHeldPages = 40960;              // pages whose scores fit shared memory
 constexpr int kMostPages = 1 << 19;            // pages whose outcome bits do
+constexpr int kBatch = 8;                      // pages a thread takes at once
+
+// Scores held for n pages: whole batches of the CTA's threads, so that no pass checks its ends.
+__host__ __device__ inline int select_held(int n, int threads) {
+    return (n + threads * kBatch - 1) / (threads * kBatch) * (threads * kBatch);
+}
 
 // Bytes of dynamic shared memory: scores (HELD), then three words per 32 pages.
-size_t select_smem(int max_blocks, bool held) {
-    return (held ? static_cast<size_t>(max_blocks) * 4 : 0) + static_cast<size_t>((max_blocks + 31) / 32) * 12;
+size_t select_smem(int max_blocks, int threads, bool held) {
+    return (held ? static_cast<size_t>(select_held(max_blocks, threads)) * 4 : 0) +
+           static_cast<size_t>((max_blocks + 31) / 32) * 12;
 }
 
 // One CTA per (kv head, sequence); all passes go over the pages in the same order, thread t
@@ -508,9 +515,10 @@ size_t select_smem(int max_blocks, bool held) {
 // and the order of the few scores in the border's bin.  Where that bin holds more than 32, or
 // scores are not finite, it is found by counting instead, two bits a step below the bits that
 // all candidates share.  A page's outcome is a bit of its warp's word; one scan over the words'
-// counts gives every chosen page its place, in page order.  A row is one pass of dependent
-// steps, bound by their latency (a dozen barriers) and not by its 32 KB of scores: short loops
-// rather than unrolled code, whose instruction fetches showed.
+// counts gives every chosen page its place, in page order.  A row is one chain of dependent
+// steps, bound by their latency (a dozen barriers) and not by its 32 KB of scores: passes take
+// eight scores a thread at once, all read before any is used (one after another they cost
+// 11800 of a row's 31600 cycles in the first pass alone).
 template <int HD, bool FP8, int NT, bool HELD>
 __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
@@ -543,13 +551,24 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     const int lo = p.sink, hi = np - p.recent, f = p.max_pages - p.sink - p.recent;
     const float *score = p.score + row * p.max_blocks;
     uint32_t *keys = dyn;                              // 0 for pages that are not candidates
-    uint32_t *words = dyn + (HELD ? p.max_blocks : 0); // outcome bits of 32 pages
+    const int held = select_held(np, NT);
+    uint32_t *words = dyn + (HELD ? select_held(p.max_blocks, NT) : 0); // outcome bits of 32 pages
     const int n_words = (np + 31) / 32;
     uint32_t *tie_words = words + (p.max_blocks + 31) / 32;
     int *places = reinterpret_cast<int *>(tie_words + (p.max_blocks + 31) / 32);
     auto key_at = [&](int i) -> uint32_t {
-        if constexpr (HELD) return keys[i];
+        if constexpr (HELD) return f > 0 ? keys[i] : 0u;
         else return i >= lo && i < hi ? key_of(score[i]) : 0u;
+    };
+    // calls f(page, key) for this thread's pages, a batch of keys read before any call
+    auto each_key = [&](auto f) {
+        for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
+            uint32_t k[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) k[u] = key_at(i0 + u * NT);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) f(i0 + u * NT, k[u]);
+        }
     };
     BlockSums<NT> sums{sums_sh, 0};
     // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
@@ -561,12 +580,29 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     if (f > 0) {
         uint32_t least = 0xffffffffu, top = 0u;
         float span = 0.f;                       // S of the bound E
-        for (int i = tid; i < (np + p.group - 1) / p.group; i += NT) span = max_nan(span, p.span[row * p.groups + i]);
-#pragma unroll 8
-        for (int i = tid; i < np; i += NT) {   // loads that wait for nothing: many at once
-            const uint32_t k = i >= lo && i < hi ? key_of(score[i]) : 0u;
-            if constexpr (HELD) keys[i] = k;
-            if (k) least = min(least, k), top = max(top, k);
+        for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
+            float x[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * NT;
+                x[u] = i >= lo && i < hi ? score[i] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * NT;
+                const uint32_t k = i >= lo && i < hi ? key_of(x[u]) : 0u;
+                if constexpr (HELD) keys[i] = k;
+                least = min(least, k ? k : 0xffffffffu);
+                top = max(top, k);
+            }
+        }
+        const float *spans = p.span + row * p.groups;
+        const int n_spans = (np + p.group - 1) / p.group;
+        for (int i0 = tid; i0 < n_spans; i0 += NT * 4) {
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = i0 + u * NT < n_spans ? spans[i0 + u * NT] : 0.f;
+            span = max_nan(span, max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])));
         }
         for (int i = tid; i < kBins; i += NT) hist[i] = 0;
         if (tid == 0) bin_n = few_n = 0;
@@ -584,11 +620,9 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         uint32_t t = 0;
         bool found = isfinite(scale) && scale > 0.f && top < 0xff800000u && least > 0x007fffffu;
         if (found) {
-#pragma unroll 4
-            for (int i = tid; i < np; i += NT) {
-                const uint32_t k = key_at(i);
+            each_key([&](int, uint32_t k) {
                 if (k) atomicAdd(&hist[bin_of(k)], 1);
-            }
+            });
             __syncthreads();
             constexpr int EACH = kBins / NT;
             const int first_bin = kBins - 1 - tid * EACH;   // from the top, EACH bins a thread
@@ -607,11 +641,9 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
             if (hist[bin] > kFew) {
                 found = false;
             } else {
-#pragma unroll 4
-                for (int i = tid; i < np; i += NT) {
-                    const uint32_t k = key_at(i);
+                each_key([&](int, uint32_t k) {
                     if (k && bin_of(k) == bin) bin_key[atomicAdd(&bin_n, 1)] = k;
-                }
+                });
                 __syncthreads();
                 const int m = bin_n;
                 const uint32_t k = lane < m ? bin_key[lane] : 0u;
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         if (!found) {
             const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
             t = nth_largest<uint32_t>(bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
-                for (int i = tid; i < np; i += NT) c += key_at(i) >= x;
+                each_key([&](int, uint32_t k) { c += k >= x; });
             });
         }
         const float T = score_of(t);
@@ -639,16 +671,14 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
             below = 1u;
         }
         int c[3] = {0, 0, 0};
-#pragma unroll 4
-        for (int i = tid; i < np; i += NT) {
-            const uint32_t k = key_at(i);
+        each_key([&](int i, uint32_t k) {
             c[0] += k > above;
             if (k >= below && k <= above) {
                 ++c[1];
                 const int at = atomicAdd(&few_n, 1);
                 if (at < kFew) few_page[at] = i;
             }
-        }
+        });
         sums(c);
         const int take = f - c[0], n_band = c[1];   // winners that come from the band, and its size
         all = take == n_band;
@@ -726,23 +756,29 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
             }
         }
     }
-    // the outcome of every page
-    for (int base = warp * 32; base < np; base += NT) {
-        const int i = base + lane;
-        bool win = i < np && (i < lo || i >= hi), tie = false;
-        if (i < np && !win && f > 0) {
-            const uint32_t k = key_at(i);
-            win = k > above;
-            if (!win && k >= below) {   // in the band
-                const uint64_t e = all ? 1ull : key_of(exact[i]);
-                win = all || e > edge;
-                tie = !all && e == edge;
+    // the outcome of every page: thread t's pages of a batch are bit t % 32 of their words
+    for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) k[u] = key_at(i0 + u * NT);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * NT;
+            if (i - lane >= np) break;   // the same for the warp
+            bool win = i < np && (i < lo || i >= hi), tie = false;
+            if (i < np && !win && f > 0) {
+                win = k[u] > above;
+                if (!win && k[u] >= below) {   // in the band
+                    const uint64_t e = all ? 1ull : key_of(exact[i]);
+                    win = all || e > edge;
+                    tie = !all && e == edge;
+                }
             }
-        }
-        const unsigned w = __ballot_sync(kAll, win), t = __ballot_sync(kAll, tie);
-        if (lane == 0) {
-            words[base / 32] = w;
-            if (!all) tie_words[base / 32] = t;
+            const unsigned w = __ballot_sync(kAll, win), t = __ballot_sync(kAll, tie);
+            if (lane == 0) {
+                words[i / 32] = w;
+                if (!all) tie_words[i / 32] = t;
+            }
         }
     }
     __syncthreads();
@@ -817,8 +853,8 @@ cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
     }
     const dim3 grid(p.nkv, p.num_seqs);
     const bool held = p.max_blocks <= kHeldPages;
-    const size_t smem = select_smem(p.max_blocks, held);
     auto select = [&](auto kern, int threads) {
+        const size_t smem = select_smem(p.max_blocks, threads, held);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
         return e != cudaSuccess ? e : launch_after(kern, grid, threads, p, stream, smem);
