@@ -66,8 +66,14 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h2) {
     return c;
 }
 
-// One warp per (sequence, page, kv head).  A row is CPR chunks of 16 bytes; the warp reads
-// 32 / CPR rows per load instruction, every load in flight before the first comparison.
+// A unit is one (sequence, page, kv head), its heads next to each other; a warp takes kUnits of
+// them in a row.  Lane u looks unit u up (lengths and page id: two dependent reads, once per
+// warp), and the rows of the next unit are on their way while one is compared.  A row is CPR
+// chunks of 16 bytes; a load instruction reads 32 / CPR rows.  Bound by streaming K: a warp per
+// unit reached 88 % of the measured copy rate on 618 MB of keys, its 4 KB waiting for the
+// look-up every time.
+constexpr int kUnits = 4;
+
 template <int HD, bool FP8>
 __global__ void __launch_bounds__(256) bounds_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
@@ -75,74 +81,109 @@ __global__ void __launch_bounds__(256) bounds_kernel(const __grid_constant__ Bou
     constexpr int RPL = 32 / CPR;                 // rows per load
     constexpr int LOADS = kBlockSize / RPL;
     constexpr int W = FP8 ? 8 : 4;                // 16-bit pairs a lane holds
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kUnits + lane;
     const int64_t per_seq = static_cast<int64_t>(p.pages) * p.num_kv_heads;
     const int64_t b = unit / per_seq;
-    if (b >= p.num_seqs) return;
-    const int rest = static_cast<int>(unit - b * per_seq);
-    const int kh = rest % p.num_kv_heads;
-    int L = max(p.seq_lens[b], 0);
-    const int first = p.first_tokens ? min(max(p.first_tokens[b], 0), L) : 0;
-    const int cap = p.max_blocks * kBlockSize;
-    bool bad = L > cap;
-    L = min(L, cap);
-    const int page = first / kBlockSize + rest / p.num_kv_heads;
-    // the last unit of a sequence sees whether its pages go on past the launch's
-    bad = bad || (L + kBlockSize - 1) / kBlockSize - first / kBlockSize > p.pages;
-    if (bad && rest == 0 && lane == 0) atomicOr(p.status, kStatusBounds);
-    const int rows = min(kBlockSize, L - page * kBlockSize);
-    if (rows <= 0 || first >= L) return;
-    const int id = p.block_tables[b * p.max_blocks + page];
-    if (id < 0 || id >= p.num_blocks) {
-        if (lane == 0) atomicOr(p.status, kStatusBounds);
-        return;
+    int my_rows = 0, my_id = 0, my_head = 0;
+    if (lane < kUnits && b < p.num_seqs) {
+        const int rest = static_cast<int>(unit - b * per_seq);
+        my_head = rest % p.num_kv_heads;
+        int L = max(p.seq_lens[b], 0);
+        const int first = p.first_tokens ? min(max(p.first_tokens[b], 0), L) : 0;
+        const int cap = p.max_blocks * kBlockSize;
+        bool bad = L > cap;
+        L = min(L, cap);
+        const int page = first / kBlockSize + rest / p.num_kv_heads;
+        // a sequence's first unit sees whether its pages go on past the launch's
+        bad = bad || (L + kBlockSize - 1) / kBlockSize - first / kBlockSize > p.pages;
+        if (bad && rest == 0) atomicOr(p.status, kStatusBounds);
+        my_rows = first < L ? max(0, min(kBlockSize, L - page * kBlockSize)) : 0;
+        if (my_rows > 0) {
+            my_id = p.block_tables[b * p.max_blocks + page];
+            if (my_id < 0 || my_id >= p.num_blocks) {
+                atomicOr(p.status, kStatusBounds);
+                my_rows = 0;
+            }
+        }
     }
+    __syncwarp();
     const int c = lane % CPR, r0 = lane / CPR;
-    const uint8_t *src = p.k_cache + id * p.b_block + kh * p.b_head + c * 16;
-    uint4 raw[LOADS];
+    auto load = [&](int u, uint4 (&raw)[LOADS]) {
+        const int rows = __shfl_sync(kAll, my_rows, u), id = __shfl_sync(kAll, my_id, u);
+        const int kh = __shfl_sync(kAll, my_head, u);
+        const uint8_t *src = p.k_cache + id * p.b_block + kh * p.b_head + c * 16;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {   // rows past the sequence repeat its last one
-        const int r = min(i * RPL + r0, rows - 1);
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + r * p.b_token));
-    }
-    uint32_t lo[W], hi[W];
+        for (int i = 0; i < LOADS; ++i)   // rows past the sequence repeat its last one
+            raw[i] = rows > 0 ? *reinterpret_cast<const uint4 *>(src + min(i * RPL + r0, rows - 1) * p.b_token)
+                              : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 raw[2][LOADS];
+    load(0, raw[0]);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int u = 0; u < kUnits; ++u) {
+        if (u + 1 < kUnits) load(u + 1, raw[(u + 1) & 1]);
+        uint32_t lo[W], hi[W];
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const uint32_t x = FP8 ? e4m3x2_to_f16x2(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu) : w[e % 4];
-            lo[e] = i ? min2<FP8>(lo[e], x) : x;
-            hi[e] = i ? max2<FP8>(hi[e], x) : x;
+        for (int i = 0; i < LOADS; ++i) {
+            const uint4 &v = raw[u & 1][i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const uint32_t x = FP8 ? e4m3x2_to_f16x2(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu) : w[e % 4];
+                lo[e] = i ? min2<FP8>(lo[e], x) : x;
+                hi[e] = i ? max2<FP8>(hi[e], x) : x;
+            }
         }
-    }
 #pragma unroll
-    for (int off = CPR; off < 32; off <<= 1)
+        for (int off = CPR; off < 32; off <<= 1)
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            lo[e] = min2<FP8>(lo[e], __shfl_xor_sync(kAll, lo[e], off));
-            hi[e] = max2<FP8>(hi[e], __shfl_xor_sync(kAll, hi[e], off));
+            for (int e = 0; e < W; ++e) {
+                lo[e] = min2<FP8>(lo[e], __shfl_xor_sync(kAll, lo[e], off));
+                hi[e] = max2<FP8>(hi[e], __shfl_xor_sync(kAll, hi[e], off));
+            }
+        const int rows = __shfl_sync(kAll, my_rows, u), id = __shfl_sync(kAll, my_id, u);
+        const int kh = __shfl_sync(kAll, my_head, u);
+        if (rows > 0 && lane < CPR) {
+            uint8_t *dst = p.bounds + (static_cast<int64_t>(id) * p.num_kv_heads + kh) * 2 * ROW + c * 16;
+            uint32_t a[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[e] = FP8 ? f16x2_to_e4m3x2(lo[(2 * e) % W]) | f16x2_to_e4m3x2(lo[(2 * e + 1) % W]) << 16 : lo[e];
+                z[e] = FP8 ? f16x2_to_e4m3x2(hi[(2 * e) % W]) | f16x2_to_e4m3x2(hi[(2 * e + 1) % W]) << 16 : hi[e];
+            }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4 *>(dst + ROW) = make_uint4(z[0], z[1], z[2], z[3]);
         }
-    if (lane >= CPR) return;
-    uint8_t *dst = p.bounds + (static_cast<int64_t>(id) * p.num_kv_heads + kh) * 2 * ROW + c * 16;
-    uint32_t a[4], z[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        a[e] = FP8 ? f16x2_to_e4m3x2(lo[(2 * e) % W]) | f16x2_to_e4m3x2(lo[(2 * e + 1) % W]) << 16 : lo[e];
-        z[e] = FP8 ? f16x2_to_e4m3x2(hi[(2 * e) % W]) | f16x2_to_e4m3x2(hi[(2 * e + 1) % W]) << 16 : hi[e];
+        __syncwarp();
     }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(a[0], a[1], a[2], a[3]);
-    *reinterpret_cast<uint4 *>(dst + ROW) = make_uint4(z[0], z[1], z[2], z[3]);
+}
+
+// Launches a kernel as a programmatic dependent of the work before it in the stream: its CTAs may
+// start while that finishes, and wait for it before they read anything.
+template <typename Kernel, typename Params>
+cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const Params &p, cudaStream_t stream,
+                         size_t smem = 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int HD>
 cudaError_t launch_bounds(const BoundsParams &p, bool fp8, cudaStream_t stream) {
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.pages * p.num_kv_heads;
-    const unsigned grid = static_cast<unsigned>((units + 7) / 8);
-    if (fp8) bounds_kernel<HD, true><<<grid, 256, 0, stream>>>(p);
-    else bounds_kernel<HD, false><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    const dim3 grid(static_cast<unsigned>((units + 8 * kUnits - 1) / (8 * kUnits)));
+    return fp8 ? launch_after(bounds_kernel<HD, true>, grid, 256, p, stream)
+               : launch_after(bounds_kernel<HD, false>, grid, 256, p, stream);
 }
 
 // ---- scores ---------------------------------------------------------------------------------
@@ -816,23 +857,6 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
 #pragma unroll 4
         for (int i = tid; i < kept; i += NT) out[i] = bt[won[i]];
     }
-}
-
-// Launches a kernel as a programmatic dependent of the work before it in the stream.
-template <typename Kernel>
-cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const SelectParams &p, cudaStream_t stream,
-                         size_t smem = 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int HD, bool FP8>

@@ -81,6 +81,9 @@ struct TreeCfg {
     static constexpr uint32_t KV_BYTES = CH * KV_CHUNK;
     // Ring stages: as many tiles as two CTAs' (one at head_dim 256) shared memory holds
     static constexpr int STAGES = HD == 256 ? (FP8 ? 4 : 2) : (HD == 128 ? (FP8 ? 4 : 2) : (FP8 ? 8 : 4));
+    // With two stages, K stage t % 2 is free once S_t is done, which s_full[t % 2] says: one commit
+    // less per tile (the next phase of s_full needs a K tile that the producer has not sent).
+    static constexpr bool K_BY_S = STAGES == 2;
     static constexpr uint32_t OFF_K = Q_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + STAGES * KV_BYTES;
     static constexpr uint32_t OFF_PREF = OFF_V + STAGES * KV_BYTES;    // int64 [kMaxSeqs + 1]
@@ -482,7 +485,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const uint32_t ph = ((t / C::STAGES) & 1) ^ 1u;
                 uint64_t *full = kv ? &v_full[s] : &k_full[s];
                 if (lane == 0) {
-                    if (!mbar_wait(kv ? &v_empty[s] : &k_empty[s], ph, p.status, abort_flag)) stop = 1;
+                    uint64_t *empty = kv ? &v_empty[s] : (C::K_BY_S ? &s_full[s] : &k_empty[s]);
+                    if (!mbar_wait(empty, ph, p.status, abort_flag)) stop = 1;
                     else mbar_arrive_expect_tx(full, C::KV_BYTES);
                 }
                 stop = __shfl_sync(kAll, stop, 0);
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                             else mma_bf16_ss(tmem + (t & 1) * kKeys, qd, d, idesc_s, acc);
                         }
                     tc_commit(&s_full[t & 1]);
-                    tc_commit(&k_empty[s]);
+                    if (!C::K_BY_S) tc_commit(&k_empty[s]);
                     if (j == n - 1) tc_commit(q_empty);
                     if (j > 0) issue_pv(t - 1, j == 1, k);
                 }
