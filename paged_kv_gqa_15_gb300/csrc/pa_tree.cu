@@ -59,7 +59,7 @@ constexpr int kKeys = 64;           // keys of a tile
 constexpr int kPages = kKeys / kBlockSize;
 constexpr int kTreeThreads = 192;
 constexpr int kMaxCtas = 304;       // two per SM of 152
-constexpr int kMaxSeqs = 1024;      // sequences per launch (their prefix is in shared memory)
+constexpr int kMaxSeqs = 960;       // sequences per launch (their prefix is in shared memory)
 
 constexpr int kCutTiles = 12;
 
@@ -98,11 +98,12 @@ struct TreeCfg {
     static_assert(CTAS_PER_SM * (SMEM + 2048) <= 228 * 1024, "shared memory");
 };
 
-// A run of tiles that was cut, as the share of its second piece notes it (pieces = 0: none).
+// A run of tiles that was cut, as the CTA of its second piece notes it (pieces = 0: none).
 struct TreeCut {
     int pieces;        // shares it lies in, from the one before on
     int rows, head;    // rows of its row tile, kernel head group
     int node0;         // first row of q and out
+    int stride;        // CTAs from one of its shares to the next
 };
 
 struct TreeLaunch {
@@ -150,23 +151,53 @@ __device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
     return s.T > 0 ? (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys : 0;
 }
 
+// Row tiles that go together are worked on by as many CTAs at once (see TreeShares); with fewer
+// rows than that in some sequences, some of those CTAs are idle there: no more than a quarter of
+// the work may be.  bf16 only: over 8-bit caches wide trees are bound by their products and not by
+// reading (32 sequences of 1k-8k, 64-node trees: 174 us side by side, 167 one after another;
+// bf16 140 against 155, and 549 against 675 for 8 of 32k-131k).
+constexpr int kMostTogether = 8;
+
 // pref[b] = tiles of the line before sequence b, run[b] the tiles of its runs, run[n] those of
-// the longest; all threads of the CTA call it.
+// the longest, run[n + 1] the row tiles that go together; all threads of the CTA call it.
+template <bool FP8>
 __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, int *run, bool flag) {
     const TreeParams &p = a.p;
-    for (int b = threadIdx.x; b < p.num_seqs; b += kTreeThreads) {
-        const TreeSeq s = tree_seq(p, b, flag);
-        run[b] = tree_tiles(s, p.window);
-        pref[b + 1] = static_cast<int64_t>(run[b]) * ((s.T + a.nodes - 1) / a.nodes) * a.heads;
+    const int n = p.num_seqs;
+    if (threadIdx.x == 0) {
+        pref[0] = 0;
+        run[n] = run[n + 1] = 0;
     }
-    if (threadIdx.x == 0) pref[0] = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < n; b += kTreeThreads) {
+        const TreeSeq s = tree_seq(p, b, flag);
+        const int tiles = tree_tiles(s, p.window), row_tiles = (s.T + a.nodes - 1) / a.nodes;
+        run[b] = tiles;
+        pref[b + 1] = static_cast<int64_t>(tiles) * row_tiles * a.heads;
+        atomicMax(&run[n], tiles);
+        atomicMax(&run[n + 1], row_tiles);
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int longest = 0;
-        for (int b = lane; b < p.num_seqs; b += 32) longest = max(longest, run[b]);
-        longest = __reduce_max_sync(kAll, longest);
-        if (lane == 0) run[p.num_seqs] = longest;
+        const int together = run[n + 1];
+        long long apart = 0, once = 0;   // tiles with row tiles one after another, and side by side
+        for (int b = lane; b < n; b += 32) {
+            apart += pref[b + 1];
+            once += static_cast<long long>(run[b]) * a.heads;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            apart += __shfl_xor_sync(kAll, apart, o);
+            once += __shfl_xor_sync(kAll, once, o);
+        }
+        const bool pair = !FP8 && together > 1 && together <= kMostTogether && once * together * 3 <= apart * 4;
+        __syncwarp();
+        if (pair)
+            for (int b = lane; b < n; b += 32) pref[b + 1] = static_cast<int64_t>(run[b]) * a.heads;
+        else if (lane == 0)
+            run[n + 1] = 1;
+        __syncwarp();
         long long carry = 0;
         for (int base = 1; base <= p.num_seqs; base += 32) {
             const int i = base + lane;
@@ -184,7 +215,10 @@ __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, 
 }
 
 // How the line of tiles is cut into shares: evenly, or at the run boundaries nearest to the
-// even cuts, which needs no joining.
+// even cuts, which needs no joining.  Where trees take several row tiles, that many CTAs take
+// one share together, a row tile each, and so read the same keys at about the same time: the
+// second comes from L2.  (One after another in the line, the row tiles of 8 sequences of 32k-131k
+// tokens with 64-node trees read every key from HBM twice: 675 us.)
 struct TreeShares {
     const int64_t *pref;   // [n + 1] tiles before sequence b
     const int *run;        // [n] tiles of each of sequence b's runs
@@ -366,12 +400,14 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     }
     // launched as a programmatic dependent: nothing before this point reads global memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    tree_prefix(a, pref, run, blockIdx.x == 0);
+    tree_prefix<FP8>(a, pref, run, blockIdx.x == 0);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    TreeShares line{pref, run, pref[p.num_seqs], 0, p.num_seqs, static_cast<int>(gridDim.x), 0, false};
+    const int together = run[p.num_seqs + 1];
+    const int share = static_cast<int>(blockIdx.x) / together, member = static_cast<int>(blockIdx.x) % together;
+    TreeShares line{pref, run, pref[p.num_seqs], 0, p.num_seqs, static_cast<int>(gridDim.x) / together, 0, false};
     if (line.total < line.shares) line.shares = max(1, static_cast<int>(line.total));
     line.even = line.total <= INT32_MAX ? static_cast<int>(line.total) / line.shares : line.total / line.shares;
     line.more = static_cast<int>(line.total - line.even * line.shares);
@@ -383,8 +419,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         const int64_t most = line.even < longest ? longest : line.even + longest;
         line.whole = most <= line.even + kCutTiles;
     }
-    const int64_t u_begin = line.begin(blockIdx.x);
-    const int64_t u_end = line.begin(blockIdx.x + 1);
+    const int64_t u_begin = line.begin(share);
+    const int64_t u_end = line.begin(share + 1);
 
     if (warp == 0) {
         // ------------------------------- TMA producer -------------------------------
@@ -398,22 +434,28 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             const int slot = n_seg & 3;
             TreeSegment s = {};
             s.n = -1;
-            if (u < u_end) {
+            while (u < u_end) {
                 const int lo = line.sequence(u);
                 const TreeSeq q = tree_seq(p, lo, false);
                 const int tiles = run[lo];
-                const int row_tiles = (q.T + a.nodes - 1) / a.nodes;
+                const int row_tiles = together > 1 ? 1 : (q.T + a.nodes - 1) / a.nodes;
                 const int64_t rel = u - pref[lo];
                 const int item = TreeShares::quotient(rel, tiles);
                 const int j = static_cast<int>(rel - static_cast<int64_t>(item) * tiles);
+                const int n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
+                const int node0 = (together > 1 ? member : item % row_tiles) * a.nodes;
+                if (node0 >= q.T) {   // the sequence has no such row tile
+                    u += n;
+                    continue;
+                }
                 s.b = lo;
                 s.head = item / row_tiles;
-                s.node0 = item % row_tiles * a.nodes;
+                s.node0 = node0;
                 s.n_nodes = min(a.nodes, q.T - s.node0);
                 s.row0 = q.row0;
                 s.T = q.T;
                 s.L = q.L;
-                s.n = static_cast<int>(min(static_cast<int64_t>(tiles - j), u_end - u));
+                s.n = n;
                 s.j0 = tree_first_key(q, p.window) / kKeys + j;
                 s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
                 if (j > 0) {   // only in the share's first segment
@@ -428,7 +470,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                     for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(kAll, least, o));
                     s.page_lo = max(0, min(q.L - q.T, q.L - q.T + least - p.window)) / kBlockSize;
                 }
-                u += s.n;
+                u += n;
+                break;
             }
             if (lane == 0) {
                 if (!mbar_wait(&seg_empty[slot], ((n_seg >> 2) & 1) ^ 1u, p.status, abort_flag)) {
@@ -451,7 +494,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         };
         const uint64_t policy = l2_policy_evict_first();
         TreeSegment w = next_segment();
-        const TreeCut run_cut = {2, w.n_nodes * a.group, w.head, w.row0 + w.node0};
+        const TreeCut run_cut = {2, w.n_nodes * a.group, w.head, w.row0 + w.node0, together};
         bool noted = false;
         // Where the share before holds the run's first piece, this one has it joined; written
         // behind the first loads, since nothing here waits for it.
@@ -459,9 +502,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             if (noted) return;
             noted = true;
             TreeCut cut = {};
-            if (run_begin >= 0 && run_begin >= line.begin(blockIdx.x - 1)) {
+            if (run_begin >= 0 && run_begin >= line.begin(share - 1)) {
                 cut = run_cut;
-                while (line.begin(blockIdx.x - 1 + cut.pieces) < run_end) ++cut.pieces;
+                while (line.begin(share - 1 + cut.pieces) < run_end) ++cut.pieces;
             }
             if (lane == 0) a.cuts[blockIdx.x] = cut;
         };
@@ -932,22 +975,22 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
 
 // Joins the partial rows of every (sequence, kernel head group, row tile) that was cut: one
 // warp per row, the shares' partials in a fixed order, so the result does not depend on
-// timing.  Grid: x = share, y = eight rows; the share that holds a cut run's second piece
-// joins it.  The maxima and sums of up to 32 pieces are read at once, one per lane, and the
+// timing.  Grid: x = CTA, y = eight rows; the CTA that had a cut run's second piece stands for
+// it.  The maxima and sums of up to 32 pieces are read at once, one per lane, and the
 // partial rows four at a time: a row costs a few memory round trips, not one per piece.
 template <int HD>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a) {
     constexpr int D = HD / 32;
     const TreeParams &p = a.p;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int share = static_cast<int>(blockIdx.x) + 1;
-    const TreeCut cut = a.cuts[share];
+    const int cta = static_cast<int>(blockIdx.x) + 1;
+    const TreeCut cut = a.cuts[cta];
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (cut.pieces == 0 || row >= cut.rows) return;
     // piece 0 is the last run of the share before, the others are the first runs of theirs
     auto slot_of = [&](int i) -> int64_t {
-        return static_cast<int64_t>(i == 0 ? 2 * (share - 1) + 1 : 2 * (share - 1 + i)) * a.slot_rows + row;
+        return (2 * static_cast<int64_t>(cta + (i - 1) * cut.stride) + (i == 0 ? 1 : 0)) * a.slot_rows + row;
     };
     float m = -INFINITY, l = 0.f, acc[D];
 #pragma unroll

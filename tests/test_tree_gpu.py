@@ -221,6 +221,16 @@ def test_bad_trees_and_pages_are_flagged_and_nothing_else_is_touched():
     assert torch.equal(got[:12], good[:12])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_row_tiles_side_by_side_and_one_after_another(fp8):
+    """Trees of several row tiles, all alike and of very different sizes, over keys that many CTAs
+    share; a sequence without the other sequences' second row tile among them."""
+    for nodes in ([64, 64, 64], [64, 40, 33], [64, 5, 60], [64, 3, 2], [200, 190, 5], [100, 1, 0]):
+        c = gpu(make([3000, 1700, 900], nodes, 8, 2, 128, seed=sum(nodes), fp8=fp8))
+        check(c, call(c), what=str(nodes))
+    assert pa.device_status() == 0
+
+
 def test_empty_trees_and_sequences():
     c = gpu(make([40, 30, 50], [3, 0, 2], 4, 2, 128, seed=16))
     check(c, call(c))
