@@ -16,6 +16,8 @@
 // lanes; T +- 2E is rounded: fewer than group + 14 act on any term).  With T the f-th
 // largest computed score, a page above T + 2E is among the f best and one below T - 2E is
 // not; the band between is scored again in fp64 and ranked by (score, page).
+#include <atomic>
+
 #include "../../include/pa.h"
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -535,6 +537,7 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int &total) {
 
 constexpr int kBins = 2048;
 constexpr int kFew = 32;                       // candidates that one warp puts in order
+constexpr int kShortPages = 1024;              // tables for fewer threads
 constexpr int kHeldPages = 40960;              // pages whose scores fit shared memory
 constexpr int kMostPages = 1 << 19;            // pages whose outcome bits do
 constexpr int kBatch = 8;                      // pages a thread takes at once
@@ -864,28 +867,42 @@ cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
     using C = ScoreCfg<HD, FP8>;
     p.group = C::GROUP;
     p.groups = (p.max_blocks + C::GROUP - 1) / C::GROUP;
-    int dev = 0, sms = 0;
+    static std::atomic<int> configured{-1};   // last device whose attributes are set
+    static std::atomic<int> sm_count{0};
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    auto allow = [&](auto kern, int pages, int threads, bool held) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(select_smem(pages, threads, held)));
+    };
+    if (configured.load() != dev) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        allow(select_kernel<HD, FP8, 256, true>, kShortPages, 256, true);
+        allow(select_kernel<HD, FP8, 512, true>, kHeldPages, 512, true);
+        allow(select_kernel<HD, FP8, 512, false>, kMostPages, 512, false);
+        if (e != cudaSuccess) return e;
+        sm_count = n;
+        configured = dev;
+    }
     if (p.max_blocks > p.max_pages) {
         // three CTAs an SM, or a warp for every group there can be
         const int64_t most = (static_cast<int64_t>(p.num_seqs) * p.nkv * p.groups + 7) / 8;
-        const unsigned grid = static_cast<unsigned>(most < 3 * sms ? most : 3 * sms);
+        const int64_t room = 3 * sm_count.load();
+        const unsigned grid = static_cast<unsigned>(most < room ? most : room);
         e = launch_after(score_kernel<HD, FP8>, dim3(grid), kScoreThreads, p, stream);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(p.nkv, p.num_seqs);
-    const bool held = p.max_blocks <= kHeldPages;
-    auto select = [&](auto kern, int threads) {
-        const size_t smem = select_smem(p.max_blocks, threads, held);
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        return e != cudaSuccess ? e : launch_after(kern, grid, threads, p, stream, smem);
+    auto select = [&](auto kern, int threads, bool held) {
+        return launch_after(kern, grid, threads, p, stream, select_smem(p.max_blocks, threads, held));
     };
     // short tables: fewer warps to wait for at each barrier
-    if (p.max_blocks <= 1024) return select(select_kernel<HD, FP8, 256, true>, 256);
-    return held ? select(select_kernel<HD, FP8, 512, true>, 512) : select(select_kernel<HD, FP8, 512, false>, 512);
+    if (p.max_blocks <= kShortPages) return select(select_kernel<HD, FP8, 256, true>, 256, true);
+    if (p.max_blocks <= kHeldPages) return select(select_kernel<HD, FP8, 512, true>, 512, true);
+    return select(select_kernel<HD, FP8, 512, false>, 512, false);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -11,7 +11,7 @@
 // 4 bytes against 286 flops a byte of the GPU).  The design follows from that:
 //  * Rows are packed for the MMA's M = 128: row r of a tile is node r / g, query head r % g of
 //    one kv head, loaded by one TMA box (64 columns, g heads, 128 / g nodes).  A tree with
-//    more rows takes several row tiles, whose second read of the keys comes from L2.
+//    more rows takes several row tiles, worked on side by side where that pays (TreeShares).
 //  * The work is a line of key tiles: for every (sequence, kv head, row tile) its 64-key
 //    tiles, one after another.  CTA c of n takes an equal share of that line, whatever the
 //    lengths: no list is sorted, no counter claimed, and no CTA has more than one tile more
@@ -37,12 +37,13 @@
 //    holds q to 2^-8 of its value.  P is split into three E5M2 terms: an f16 value's upper byte
 //    is an E5M2 value, so each term is a mask and a subtraction and four of them one byte
 //    permutation.  Three terms hold at least 9 bits (2^-8 of P, mostly better) over f16's range.
-//    P as E4M3 pairs needs four conversions per pair of weights (the ALU pipe is what bounds
-//    this softmax), and reaches from 448 to 2^-9 only, so that every growth of a row's maximum by
-//    a factor 1.75 rescaled O and weights far under one large maximum lost their bits: 154 us for
-//    32 sequences of 1k-8k and 64-node trees.  Two more warps turning V into f16 left too little
-//    shared memory for tiles on their way: 261 us.
+//    P as E4M3 pairs has one product less and was 8 % faster where the products bound the call (154
+//    us against 167 for 32 sequences of 1k-8k, 64-node trees), but E4M3 reaches from 448 to 2^-9
+//    only: weights far under one large maximum lost their bits, and they can be most of the sum.
+//    Two more warps turning V into f16 left too little shared memory for tiles on their way: 261 us.
 //  * Every mbarrier wait is bounded.
+#include <atomic>
+
 #include <cuda.h>
 
 #include "../../include/pa.h"
@@ -61,6 +62,9 @@ constexpr int kTreeThreads = 192;
 constexpr int kMaxCtas = 304;       // two per SM of 152
 constexpr int kMaxSeqs = 960;       // sequences per launch (their prefix is in shared memory)
 
+// A cut run costs a partial tile's way out and back and a second kernel's work: about as much as
+// this many tiles (32 sequences of 500 tokens, 8 tiles a run, 128 rows: 39.6 us cut evenly, 26.0 in
+// whole runs; at 4000 tokens the two are level).
 constexpr int kCutTiles = 12;
 
 constexpr uint32_t pow2_columns(uint32_t x) {
@@ -263,7 +267,7 @@ struct TreeSegment {
 
 struct TreeQueue {
     TreeSegment seg[4];
-    uint32_t bad_nodes[16];        // partly seen rows with non-finite values (see clean_values)
+    uint32_t bad_nodes[16];        // partly seen rows with non-finite values (see the cleaning of V)
     uint32_t bad_pages[16];        // ring by tile: pages whose ids are out of range
 };
 static_assert(48 * 8 + sizeof(TreeQueue) <= 1024, "queue fits behind the barriers");
@@ -413,8 +417,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     line.more = static_cast<int>(line.total - line.even * line.shares);
     {
         // Shares of whole runs hold at most one run when there are no more runs than shares, else
-        // an even share and a run; cutting costs a partial tile's round trip and the join,
-        // as much as about kCutTiles tiles.
+        // an even share and a run.
         const int64_t longest = run[p.num_seqs];
         const int64_t most = line.even < longest ? longest : line.even + longest;
         line.whole = most <= line.even + kCutTiles;
@@ -1074,15 +1077,22 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
         if (!encode(&a.tm_k, p.k_cache, 4, dims, str, box) || !encode(&a.tm_v, p.v_cache, 4, dims, str, box))
             return cudaErrorInvalidValue;
     }
-    int dev = 0, sms = 0;
+    auto kern = tree_kernel<HD, FP8>;
+    static std::atomic<int> configured{-1};   // last device whose attributes are set
+    static std::atomic<int> sm_count{0};
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    auto kern = tree_kernel<HD, FP8>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e != cudaSuccess) return e;
+    if (configured.load() != dev) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        sm_count = n;
+        configured = dev;
+    }
+    const int sms = sm_count.load();
     // no more CTAs than the longest possible line has tiles
     const int row_tiles = (p.max_tree_len + a.nodes - 1) / a.nodes;
     const int64_t line = static_cast<int64_t>(p.num_seqs) * a.heads * row_tiles *

@@ -177,6 +177,28 @@ def test_large_scores():
     ref64.assert_attention(got, out, bound, extra=0.084)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_far_under_one_large_maximum(fp8):
+    """One key ten units above 4999 equal ones, which hold a fifth of the sum between them.  The
+    scores are exact in every type (one channel, small whole numbers), so an 8-bit cache keeps
+    the bounds of a bf16 one."""
+    hd, n = 128, 5000
+    c = make([n], [2], 4, 2, hd, seed=40, fp8=fp8)
+    dt = c["k"].dtype
+    c["scale"], c["kv_scale"] = 1.0, 1.0
+    c["k"] = torch.zeros(c["k"].shape).to(dt)
+    c["k"][c["table"][0, 7], :, 3, 0] = torch.tensor(10.0).to(dt)
+    gen = torch.Generator().manual_seed(3)
+    c["v"] = (torch.randn(c["v"].shape, generator=gen) + 1.0).to(dt)
+    c["q"] = torch.zeros(c["q"].shape, dtype=torch.bfloat16)
+    c["q"][..., 0] = 1.0
+    c = gpu(c)
+    got = call(c)
+    out, bound = ref64.tree(c["q"], c["k"], c["v"], c["table"].cpu(), c["lens"].cpu(), c["indptr"].cpu(),
+                            c["mask"].cpu(), 1.0)
+    ref64.assert_attention(got, out, bound)
+
+
 def test_padded_pools():
     """Strides other than the dense ones: heads and pages with room between them."""
     c = gpu(make([300, 90], [9, 4], 8, 2, 128, seed=14))
