@@ -348,12 +348,14 @@ int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_
  * For sequence b and i < accept_lens[b], token C_b + i of each pool becomes what token
  * C_b + accepted[b][i] was, bit for bit, and new_seq_lens[b] = C_b + accept_lens[b].
  *   pools         HOST array of num_pools device pointers, all with the same strides,
- *                 kv_dtype and block tables (e.g. [k_0, v_0, k_1, v_1, ...])
+ *                 kv_dtype and block tables (e.g. [k_0, v_0, k_1, v_1, ...]); a pool that
+ *                 layers share is listed once
  *   accepted      [num_seqs][max_accept] int32 node indices, each greater than the one
  *                 before it (a path from the root down); entries past accept_lens[b]
  *                 are not read
  *   accept_lens   [num_seqs] int32
- *   new_seq_lens  [num_seqs] int32, written; must not be seq_lens itself
+ *   new_seq_lens  [num_seqs] int32, written; shares no memory with seq_lens, accept_lens
+ *                 or qo_indptr
  * A path is cut before its first entry that is out of range or not ascending, and
  * before max_accept entries; a sequence whose T_b is negative or exceeds max_tree_len
  * or seq_lens[b] keeps its length and rows; both set PA_ERR_DEVICE_BOUNDS.  A page id
@@ -408,8 +410,9 @@ size_t pa_select_pages_workspace_size(int num_seqs, int num_kv_heads, int max_bl
  *                pages' ids in the order of their tokens, then -1
  *   page_lens    [num_seqs] int32, written: the number of tokens those pages hold
  * max_pages > 0, sink_pages >= 0, recent_pages >= 1 (a newest page's bounds may lag its
- * rows), sink_pages + recent_pages <= max_pages, max_blocks_per_seq <= 524288.  A page id outside the pool scores
- * lowest and sets PA_ERR_DEVICE_BOUNDS.
+ * rows), sink_pages + recent_pages <= max_pages, max_blocks_per_seq <= 524288.  A page id
+ * outside the pool scores lowest and sets PA_ERR_DEVICE_BOUNDS.  page_tables and page_lens
+ * share no memory with block_tables and seq_lens.
  */
 int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const void *q, const void *bounds,
                     const int32_t *block_tables, const int32_t *seq_lens, int num_seqs,

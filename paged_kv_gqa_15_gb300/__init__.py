@@ -385,7 +385,9 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
                    accept_lens, new_seq_lens, max_tree_len, layout="HND", stream=None):
     """Moves the K/V rows of each sequence's accepted nodes (accepted int32 [B, n], ascending,
     accept_lens[b] of them) behind its context in every layer's pools, and writes the
-    sequences' new lengths into new_seq_lens (not seq_lens itself)."""
+    sequences' new lengths into new_seq_lens (not seq_lens itself).  Layers that share a cache
+    list it once."""
+    assert len(key_caches) == len(value_caches) > 0
     pools = [t for kv in zip(key_caches, value_caches) for t in kv]
     nb, nkv, bs, hd = _pool_geometry(pools[0], layout)
     sb, sh, st = pool_strides(pools[0], layout)

@@ -143,6 +143,11 @@ cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t s
 // The argument checks of the entry points, shared by those in other translation units.
 int api_check_heads(int head_dim, int num_q_heads, int num_kv_heads);
 int api_check_kv_dtype(int kv_dtype, float k_scale, float v_scale);
+// Whether n int32 values at a share memory with m at b.
+inline bool api_overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * static_cast<uintptr_t>(m) && y < x + 4 * static_cast<uintptr_t>(n);
+}
 int api_check_pool(int head_dim, int block_size, int64_t num_blocks, int num_kv_heads, int64_t sb,
                    int64_t sh, int64_t st, int kv_dtype);
 

@@ -10,12 +10,14 @@
 // than one head, and the pass is bound by reading the bounds (2 head_dim elements a page).
 //
 // Selection is by exact scores.  A score computed in fp32 is off by at most
-//     E = (group + 14) 2^-24 S,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
+//     E = (group + 24) 2^-24 S + 2^-140,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
 // (P and N are sums of `group` terms of one sign: group - 1 roundings; a product is rounded
-// once, added in a chain of four, joined by three more sums in the lane and five across
-// lanes; T +- 2E is rounded: fewer than group + 14 act on any term).  With T the f-th
-// largest computed score, a page above T + 2E is among the f best and one below T - 2E is
-// not; the band between is scored again in fp64 and ranked by (score, page).
+// once at most, added in a chain of up to 16, joined over at most 32 lanes in five sums; S
+// itself and T +- 2E are rounded: fewer than group + 24 act on any term.  Products below the
+// normal numbers lose up to 2^-150 each).  S is taken once for a group of pages, from the
+// largest magnitude of every channel.  With T the f-th largest computed score, a page above
+// T + 2E is among the f best and one below T - 2E is not; the band between is scored again in
+// fp64 and ranked by (score, page).
 #include <atomic>
 
 #include "../../include/pa.h"
@@ -220,6 +222,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The largest of three magnitudes, or NaN if one is.
+__device__ __forceinline__ float most_of(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // A channel whose query weight is zero adds nothing, an infinite bound included.
 template <typename T>
 __device__ __forceinline__ T weighed(T w, T x) {
@@ -339,16 +348,17 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
         const bool known = id >= 0 && id < p.num_blocks;
         if (!known) atomicOr(p.status, kStatusBounds);
         const unsigned unknown = __ballot_sync(kAll, !known);
-        const int page = known ? id : 0;
         const int first = grp * C::GROUP, n = min(C::GROUP, pages[b] - first);
+        // lane i knows where page i's bounds are, in units of 16 bytes (the host sees to it that 32
+        // bits hold them); lanes past the group's pages take its first
+        const uint32_t place = (static_cast<uint32_t>(__shfl_sync(kAll, known ? id : 0, lane < n ? lane : 0)) * p.nkv + kh) * UNITS;
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds) + unit;
         uint4 raw[LOADS][PARTS];
 #pragma unroll
         for (int k = 0; k < LOADS; ++k) {
-            const int i = k * PER + sub;
-            const int64_t pg = __shfl_sync(kAll, page, i);
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (pg * p.nkv + kh) * C::PAGE) + unit;
+            const uint32_t at = __shfl_sync(kAll, place, k * PER + sub);
 #pragma unroll
-            for (int v = 0; v < PARTS; ++v) raw[k][v] = i < n ? __ldg(src + v * LANES) : make_uint4(0u, 0u, 0u, 0u);
+            for (int v = 0; v < PARTS; ++v) raw[k][v] = __ldg(src + (at + v * LANES));
         }
         const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
         // where the next group is, and its ids
@@ -390,67 +400,79 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
                     for (int e = 0; e < E; ++e) w[v][e] = -w[v][e];
             }
         }
-        float x[2 * LOADS];   // the pages' sums, then their sums of magnitudes
+        float x[LOADS];         // the pages' sums
+        float far[PARTS][E];    // the largest magnitudes of the group's elements
+        bool odd = false;
 #pragma unroll
-        for (int k = 0; k < LOADS; ++k) {
-            float s = 0.f, a = 0.f;
+        for (int k = 0; k < LOADS; k += 2) {
+            float s[2] = {0.f, 0.f};
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) {
-                float f[E], t[2] = {0.f, 0.f};
-                float2 c[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // chains of E / 4 products
-                unpack16<FP8>(raw[k][v], f);
+                float f[2][E];
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 y = __fmul2_rn(make_float2(w[v][e], w[v][e + 1]), make_float2(f[e], f[e + 1]));
-                    c[e / 2 & 1] = __fadd2_rn(c[e / 2 & 1], y);
-                    t[0] += fabsf(y.x);
-                    t[1] += fabsf(y.y);
+                for (int u = 0; u < 2; ++u) {
+                    unpack16<FP8>(raw[k + u][v], f[u]);
+                    float2 c[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // chains of E / 4 products
+#pragma unroll
+                    for (int e = 0; e < E; e += 2)
+                        c[e / 2 & 1] = __ffma2_rn(make_float2(w[v][e], w[v][e + 1]), make_float2(f[u][e], f[u][e + 1]),
+                                                  c[e / 2 & 1]);
+                    const float2 c2 = __fadd2_rn(c[0], c[1]);
+                    s[u] += c2.x + c2.y;
                 }
-                const float2 c2 = __fadd2_rn(c[0], c[1]);
-                s += c2.x + c2.y;
-                a += t[0] + t[1];
+#pragma unroll
+                for (int e = 0; e < E; ++e) far[v][e] = most_of(k ? far[v][e] : 0.f, f[0][e], f[1][e]);
             }
-            if (a != a) {   // a zero weight met an infinity, or there is a NaN: the exact rule
-                s = a = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[k + u] = s[u];
+                odd |= s[u] != s[u];
+            }
+        }
+        // a zero weight met an infinity, or a sum is a NaN: the exact rule, from the bounds read again
+        if (__any_sync(kAll, odd)) {
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k) {
+                const uint32_t at = __shfl_sync(kAll, place, k * PER + sub);
+                x[k] = 0.f;
 #pragma unroll
                 for (int v = 0; v < PARTS; ++v) {
                     float f[E];
-                    unpack16<FP8>(raw[k][v], f);
+                    unpack16<FP8>(__ldg(src + (at + v * LANES)), f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float y = weighed(w[v][e], f[e]);
-                        s += y;
-                        a += fabsf(y);
-                    }
+                    for (int e = 0; e < E; ++e) x[k] += weighed(w[v][e], f[e]);
                 }
             }
-            x[k] = s;
-            x[LOADS + k] = a;
         }
+        float most = 0.f;   // S of a page with the group's largest magnitudes
+#pragma unroll
+        for (int v = 0; v < PARTS; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e) most += weighed(fabsf(w[v][e]), far[v][e]);
         __syncwarp();
         int which = 0;   // the sum this lane ends up with
         int m = LANES / 2;
 #pragma unroll
-        for (int half = LOADS; half >= 1; half >>= 1, m >>= 1) {
+        for (int half = LOADS / 2; half >= 1; half >>= 1, m >>= 1) {
             const bool up = lane & m;
             which += up ? half : 0;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i)
+            for (int i = 0; i < LOADS / 2; ++i)
                 if (i < half) {
                     const float give = up ? x[i] : x[i + half];
                     x[i] = (up ? x[i + half] : x[i]) + __shfl_xor_sync(kAll, give, m);
                 }
         }
 #pragma unroll
-        for (int o = LANES / (4 * LOADS); o >= 1; o >>= 1) x[0] += __shfl_xor_sync(kAll, x[0], o);
-        const bool mag = which >= LOADS;
-        const int i = (which & (LOADS - 1)) * PER + sub;
-        const bool lost = unknown >> i & 1;
-        if (!mag && unit % (LANES / (2 * LOADS)) == 0 && i < n)
-            p.score[row * p.max_blocks + first + i] = lost ? -INFINITY : x[0];
-        float most = mag && !lost ? x[0] : 0.f;
+        for (int o = LANES / (2 * LOADS); o >= 1; o >>= 1) x[0] += __shfl_xor_sync(kAll, x[0], o);
+        const int i = which * PER + sub;
+        if (unit % (LANES / LOADS) == 0 && i < n)
+            p.score[row * p.max_blocks + first + i] = unknown >> i & 1 ? -INFINITY : x[0];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(kAll, most, o));
+        for (int o = 16; o; o >>= 1) {
+            const float y = __shfl_xor_sync(kAll, most, o);
+            most = o < LANES ? most + y : max_nan(most, y);
+        }
         if (lane == 0) p.span[row * p.groups + grp] = most;
         fresh = kh1 != kh || b1 != b;
         if (b1 != b) groups = (pages[min(b1, p.num_seqs - 1)] + C::GROUP - 1) / C::GROUP;
@@ -536,7 +558,7 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int &total) {
 }
 
 constexpr int kBins = 2048;
-constexpr int kFew = 32;                       // candidates that one warp puts in order
+constexpr int kFew = 32;                       // pages at the border that one warp puts in order
 constexpr int kShortPages = 1024;              // tables for fewer threads
 constexpr int kHeldPages = 40960;              // pages whose scores fit shared memory
 constexpr int kMostPages = 1 << 19;            // pages whose outcome bits do
@@ -554,15 +576,16 @@ size_t select_smem(int max_blocks, int threads, bool held) {
 }
 
 // One CTA per (kv head, sequence); all passes go over the pages in the same order, thread t
-// taking pages t, t + NT, ...  The border score comes from a histogram of even bins over the
-// scores' range (scores crowd in few binades, so bins of their bits would not part them)
-// and the order of the few scores in the border's bin.  Where that bin holds more than 32, or
-// scores are not finite, it is found by counting instead, two bits a step below the bits that
-// all candidates share.  A page's outcome is a bit of its warp's word; one scan over the words'
-// counts gives every chosen page its place, in page order.  A row is one chain of dependent
-// steps, bound by their latency (a dozen barriers) and not by its 32 KB of scores: passes take
-// eight scores a thread at once, all read before any is used (one after another they cost
-// 11800 of a row's 31600 cycles in the first pass alone).
+// taking pages t, t + NT, ...  The border score's bin comes from a histogram of even bins over the
+// scores' range (scores crowd in few binades, so bins of their bits would not part them).  One more
+// pass then settles every page whose score is 2E away from that bin; the few others are put in
+// order, by exact scores where 2E does not part them, and join.  Where more than 32 pages are that
+// close to the border, or scores are not finite, the border is found by counting instead, two bits
+// a step below the bits that all candidates share.  A page's outcome is a bit of its warp's word;
+// one scan over the words' counts gives every chosen page its place, in page order.  A row is one
+// chain of dependent steps, bound by their latency and by what its SM can issue, not by its 32 KB of
+// scores: passes take eight scores a thread at once, all read before any is used (one after another
+// they cost 11800 of a row's 31600 cycles in the first pass alone).
 template <int HD, bool FP8, int NT, bool HELD>
 __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);
@@ -573,10 +596,10 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     __shared__ uint32_t ends[3][32];
     __shared__ double P[HD], N[HD];
     __shared__ int hist[kBins];
-    __shared__ uint32_t bin_key[kFew];
+    __shared__ float few_x[kFew];
     __shared__ uint64_t few_key[kFew];
     __shared__ int few_page[kFew];
-    __shared__ int bin_at, bin_above, bin_n, few_n;
+    __shared__ int bin_at, bin_above, near_n, few_n;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = select_len(p, b, false);
@@ -591,53 +614,72 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         for (int i = tid; i < np; i += NT) out[i] = bt[i];
         return;
     }
-    // f pages of [lo, hi) join the sinks and the newest ones
+    // f of the candidates [lo, hi) join the sinks and the newest pages
     const int lo = p.sink, hi = np - p.recent, f = p.max_pages - p.sink - p.recent;
     const float *score = p.score + row * p.max_blocks;
-    uint32_t *keys = dyn;                              // 0 for pages that are not candidates
+    float *held_x = reinterpret_cast<float *>(dyn);
     const int held = select_held(np, NT);
     uint32_t *words = dyn + (HELD ? select_held(p.max_blocks, NT) : 0); // outcome bits of 32 pages
     const int n_words = (np + 31) / 32;
     uint32_t *tie_words = words + (p.max_blocks + 31) / 32;
-    int *places = reinterpret_cast<int *>(tie_words + (p.max_blocks + 31) / 32);
-    auto key_at = [&](int i) -> uint32_t {
-        if constexpr (HELD) return f > 0 ? keys[i] : 0u;
-        else return i >= lo && i < hi ? key_of(score[i]) : 0u;
-    };
-    // calls f(page, key) for this thread's pages, a batch of keys read before any call
-    auto each_key = [&](auto f) {
-        for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
-            uint32_t k[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) k[u] = key_at(i0 + u * NT);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) f(i0 + u * NT, k[u]);
-        }
-    };
-    BlockSums<NT> sums{sums_sh, 0};
-    // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
-    uint32_t above = 0xffffffffu, below = 0xffffffffu;
-    bool all = true;                            // the whole band wins
-    uint64_t edge = 0;                          // else the weakest exact score that wins ...
-    int ties = 0;                               // ... and how many equal to it do
-    double *exact = p.exact + row * p.max_blocks;
-    if (f > 0) {
-        uint32_t least = 0xffffffffu, top = 0u;
-        float span = 0.f;                       // S of the bound E
+    auto candidate = [&](int i) { return static_cast<unsigned>(i - lo) < static_cast<unsigned>(hi - lo); };
+    // a candidate's score, and -infinity for other pages
+    auto read_x = [&](int i) { return candidate(i) ? score[i] : -INFINITY; };
+    // calls f(page, score) for this thread's pages, a batch of scores read before any call
+    auto each_x = [&](auto f) {
         for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
             float x[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int i = i0 + u * NT;
-                x[u] = i >= lo && i < hi ? score[i] : 0.f;
+            for (int u = 0; u < kBatch; ++u) x[u] = HELD ? held_x[i0 + u * NT] : read_x(i0 + u * NT);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) f(i0 + u * NT, x[u]);
+        }
+    };
+    // page i's score in fp64, by one warp, from P and N
+    auto exact_weights = [&]() {
+        const int g = p.nq / p.nkv;
+        for (int d = tid; d < HD; d += NT) {
+            const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
+            double x = 0.0, y = 0.0;
+#pragma unroll 8
+            for (int h = 0; h < g; ++h) {
+                const float v = __bfloat162float(q[h * HD]);
+                if (v < 0.f) y += v;
+                else x += v;
             }
+            P[d] = x;
+            N[d] = y;
+        }
+        __syncthreads();
+    };
+    auto exact_score = [&](int i) -> double {
+        const int id = bt[i];
+        if (id < 0 || id >= p.num_blocks) return -INFINITY;
+        const uint8_t *r = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
+        double e = 0.0;
+#pragma unroll
+        for (int d = 0; d < HD; d += 32)
+            e += weighed<double>(P[d + lane], bound_value<FP8>(r + ROW, d + lane)) +
+                 weighed<double>(N[d + lane], bound_value<FP8>(r, d + lane));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(kAll, e, o);
+        return e;
+    };
+    BlockSums<NT> sums{sums_sh, 0};
+    float least = INFINITY, top = -INFINITY, span = 0.f;   // ends of the scores; S of the bound E
+    bool odd = f == 0;                                     // a score is not finite, or none is asked for
+    if (f > 0) {
+        for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
+            float x[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) x[u] = read_x(i0 + u * NT);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int i = i0 + u * NT;
-                const uint32_t k = i >= lo && i < hi ? key_of(x[u]) : 0u;
-                if constexpr (HELD) keys[i] = k;
-                least = min(least, k ? k : 0xffffffffu);
-                top = max(top, k);
+                if constexpr (HELD) held_x[i] = x[u];
+                least = fminf(least, candidate(i) ? x[u] : INFINITY);
+                top = fmaxf(top, x[u]);
+                odd |= candidate(i) && !(fabsf(x[u]) < INFINITY);
             }
         }
         const float *spans = p.span + row * p.groups;
@@ -648,136 +690,130 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
             for (int u = 0; u < 4; ++u) x[u] = i0 + u * NT < n_spans ? spans[i0 + u * NT] : 0.f;
             span = max_nan(span, max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])));
         }
-        for (int i = tid; i < kBins; i += NT) hist[i] = 0;
-        if (tid == 0) bin_n = few_n = 0;
-        least = __reduce_min_sync(kAll, least);
-        top = __reduce_max_sync(kAll, top);
-        const uint32_t wide = __reduce_max_sync(kAll, key_of(span));   // a NaN is the largest
-        if (lane == 0) ends[0][warp] = least, ends[1][warp] = top, ends[2][warp] = wide;
+    }
+    for (int i = tid; i < kBins; i += NT) hist[i] = 0;
+    if (tid == 0) near_n = few_n = 0;
+    const uint32_t k_least = __reduce_min_sync(kAll, key_of(least)), k_top = __reduce_max_sync(kAll, key_of(top));
+    const uint32_t k_span = __reduce_max_sync(kAll, key_of(span));   // a NaN is the largest
+    if (lane == 0) ends[0][warp] = k_least, ends[1][warp] = k_top, ends[2][warp] = k_span;
+    odd = __syncthreads_or(odd);
+    least = score_of(__reduce_min_sync(kAll, lane < W ? ends[0][lane] : 0xffffffffu));
+    top = score_of(__reduce_max_sync(kAll, lane < W ? ends[1][lane] : 0u));
+    span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
+    const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 24) * 0x1p-24f * span + 0x1p-138f;
+    const float scale = (kBins - 1) / (top - least);
+    // a score's place among the bins, rounded by less than 2^-12; 2E there, with both roundings
+    auto place_of = [&](float x) { return (x - least) * scale; };
+    const float margin = E2 * scale + 0x1p-10f;
+    bool settled = !odd && scale > 0.f && margin < 8.f;   // not for an infinite or NaN scale either
+    if (settled) {
+        each_x([&](int, float x) {
+            if (x != -INFINITY) atomicAdd(&hist[static_cast<int>(place_of(x))], 1);
+        });
         __syncthreads();
-        least = __reduce_min_sync(kAll, lane < W ? ends[0][lane] : 0xffffffffu);
-        top = __reduce_max_sync(kAll, lane < W ? ends[1][lane] : 0u);
-        span = score_of(__reduce_max_sync(kAll, lane < W ? ends[2][lane] : 0u));
-        // bins over [low, low + range], monotone in the score as each rounding is
-        const float low = score_of(least), scale = (kBins - 1) / (score_of(top) - low);
-        auto bin_of = [&](uint32_t k) { return min(kBins - 1, static_cast<int>((score_of(k) - low) * scale)); };
-        uint32_t t = 0;
-        bool found = isfinite(scale) && scale > 0.f && top < 0xff800000u && least > 0x007fffffu;
-        if (found) {
-            each_key([&](int, uint32_t k) {
-                if (k) atomicAdd(&hist[bin_of(k)], 1);
-            });
-            __syncthreads();
-            constexpr int EACH = kBins / NT;
-            const int first_bin = kBins - 1 - tid * EACH;   // from the top, EACH bins a thread
-            int c = 0, total;
+        constexpr int EACH = kBins / NT;
+        const int first_bin = kBins - 1 - tid * EACH;   // from the top, EACH bins a thread
+        int c = 0, total;
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) c += hist[first_bin - i];
-            int before = block_scan<NT>(c, warps, total);
-            if (before < f && f <= before + c) {
-                int at = first_bin;
-                while (before + hist[at] < f) before += hist[at--];
-                bin_at = at;
-                bin_above = before;
-            }
-            __syncthreads();
-            const int bin = bin_at;
-            if (hist[bin] > kFew) {
-                found = false;
-            } else {
-                each_key([&](int, uint32_t k) {
-                    if (k && bin_of(k) == bin) bin_key[atomicAdd(&bin_n, 1)] = k;
-                });
-                __syncthreads();
-                const int m = bin_n;
-                const uint32_t k = lane < m ? bin_key[lane] : 0u;
-                int place = 0;
-                for (int i = 0; i < m; ++i) {
-                    const uint32_t o = __shfl_sync(kAll, k, i);
-                    place += o > k || (o == k && i < lane);
-                }
-                const unsigned who = __ballot_sync(kAll, lane < m && place == f - bin_above - 1);
-                t = __shfl_sync(kAll, k, __ffs(who) - 1);
-            }
+        for (int i = 0; i < EACH; ++i) c += hist[first_bin - i];
+        int before = block_scan<NT>(c, warps, total);
+        if (before < f && f <= before + c) {
+            int at = first_bin;
+            while (before + hist[at] < f) before += hist[at--];
+            bin_at = at;
+            bin_above = before;
         }
-        if (!found) {
-            const int bits = (32 - __clz(least ^ top) + 1) & ~1;   // below the shared ones, even
-            t = nth_largest<uint32_t>(bits == 32 ? 0u : top >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
-                each_key([&](int, uint32_t k) { c += k >= x; });
-            });
-        }
-        const float T = score_of(t);
-        const float E2 = 2.f * static_cast<float>(p.nq / p.nkv + 14) * 0x1p-24f * span;
-        if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
-            above = key_of(T + E2);
-            below = key_of(T - E2);
-        } else {
-            below = 1u;
-        }
-        int c[3] = {0, 0, 0};
-        each_key([&](int i, uint32_t k) {
-            c[0] += k > above;
-            if (k >= below && k <= above) {
-                ++c[1];
-                const int at = atomicAdd(&few_n, 1);
-                if (at < kFew) few_page[at] = i;
+        __syncthreads();
+        const int bin = bin_at;
+        const float from = bin - margin, past = bin + 1 + margin;
+        each_x([&](int i, float x) {
+            const float y = place_of(x);
+            const unsigned w = __ballot_sync(kAll, y >= past || (i < np && !candidate(i)));
+            if (lane == 0 && i < np) words[i / 32] = w;
+            if (y >= from && y < past) {
+                const int at = atomicAdd(&near_n, 1);
+                if (at < kFew) few_x[at] = x, few_page[at] = i;
             }
         });
-        sums(c);
-        const int take = f - c[0], n_band = c[1];   // winners that come from the band, and its size
-        all = take == n_band;
-        if (!all) {
-            const int g = p.nq / p.nkv;
-            for (int d = tid; d < HD; d += NT) {
-                const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(b) * p.nq + kh * g) * HD + d;
-                double x = 0.0, y = 0.0;
-#pragma unroll 8
-                for (int h = 0; h < g; ++h) {
-                    const float v = __bfloat162float(q[h * HD]);
-                    if (v < 0.f) y += v;
-                    else x += v;
-                }
-                P[d] = x;
-                N[d] = y;
+        __syncthreads();
+        const int m = near_n;
+        settled = m <= kFew;
+        if (settled) {   // every warp puts the m pages at the border in order
+            const bool here = lane < m;
+            const float x = here ? few_x[lane] : 0.f;
+            const int page = here ? few_page[lane] : 0;
+            // winners among them: pages of higher bins are counted in bin_above
+            const int need = f - bin_above + __popc(__ballot_sync(kAll, here && static_cast<int>(place_of(x)) > bin));
+            int rank = 0;
+            for (int i = 0; i < m; ++i) {
+                const float o = __shfl_sync(kAll, x, i);
+                rank += o > x || (o == x && i < lane);
             }
-            __syncthreads();
-            // page i's score in fp64, by one warp
-            auto exact_score = [&](int i) -> double {
-                const int id = bt[i];
-                if (id < 0 || id >= p.num_blocks) return -INFINITY;
-                const uint8_t *r = p.bounds + (static_cast<int64_t>(id) * p.nkv + kh) * 2 * ROW;
-                double e = 0.0;
-#pragma unroll
-                for (int d = 0; d < HD; d += 32)
-                    e += weighed<double>(P[d + lane], bound_value<FP8>(r + ROW, d + lane)) +
-                         weighed<double>(N[d + lane], bound_value<FP8>(r, d + lane));
-#pragma unroll
-                for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(kAll, e, o);
-                return e;
-            };
-            if (n_band <= kFew) {
-                for (int i = warp; i < n_band; i += W) {
-                    const double e = exact_score(few_page[i]);
-                    if (lane == 0) {
-                        few_key[i] = key_of(e);
-                        exact[few_page[i]] = e;
-                    }
-                }
-                __syncthreads();
-                // the take-th of the band: a member's place is the number of those before it
-                const uint64_t k = lane < n_band ? few_key[lane] : 0ull;
-                int place = 0;
-                for (int i = 0; i < n_band; ++i) {
-                    const uint64_t o = few_key[i];
-                    place += o > k || (o == k && i < lane);
-                }
-                const int who = __ffs(__ballot_sync(kAll, lane < n_band && place == take - 1)) - 1;
-                edge = few_key[who];
-                ties = take - __popc(__ballot_sync(kAll, lane < n_band && k > edge));
+            const float T = __shfl_sync(kAll, x, __ffs(__ballot_sync(kAll, here && rank == need - 1)) - 1);
+            bool win = here && x > T + E2;
+            const bool band = here && !win && x >= T - E2;
+            const unsigned in_band = __ballot_sync(kAll, band);
+            const int take = need - __popc(__ballot_sync(kAll, win));
+            if (take == __popc(in_band)) {
+                win |= band;
             } else {
+                exact_weights();
+                for (int i = warp; i < m; i += W)
+                    if (in_band >> i & 1) {
+                        const double e = exact_score(few_page[i]);
+                        if (lane == 0) few_key[i] = key_of(e);
+                    }
+                __syncthreads();
+                const uint64_t k = band ? few_key[lane] : 0ull;
+                int place = 0;   // of the band's pages, by (score, page)
+                for (unsigned r = in_band; r; r &= r - 1) {
+                    const int i = __ffs(r) - 1;
+                    const uint64_t o = few_key[i];
+                    place += o > k || (o == k && few_page[i] < page);
+                }
+                win |= band && place < take;
+            }
+            if (warp == 0 && win) atomicOr(&words[page / 32], 1u << (page & 31));
+            __syncthreads();
+        }
+    }
+    if (!settled) {
+        auto key_at = [&](int i, float x) -> uint32_t { return f > 0 && candidate(i) ? key_of(x) : 0u; };
+        // calls f(page, key) for this thread's pages; 0 for pages that are not candidates
+        auto each_key = [&](auto f) { each_x([&](int i, float x) { f(i, key_at(i, x)); }); };
+        // Keys of the sure winners (> above) and of the sure losers (< below); the band between.
+        uint32_t above = 0xffffffffu, below = 0xffffffffu;
+        bool all = true;                            // the whole band wins
+        uint64_t edge = 0;                          // else the weakest exact score that wins ...
+        int ties = 0;                               // ... and how many equal to it do
+        double *exact = p.exact + row * p.max_blocks;
+        if (f > 0) {
+            const uint32_t best = key_of(top);
+            const int bits = odd ? 32 : (32 - __clz(key_of(least) ^ best) + 1) & ~1;   // below the shared ones, even
+            const uint32_t t = nth_largest<uint32_t>(bits == 32 ? 0u : best >> bits << bits, bits, f, sums, [&](uint32_t x, int &c) {
+                each_key([&](int, uint32_t k) { c += k >= x; });
+            });
+            const float T = score_of(t);
+            if (isfinite(E2) && !isnan(T)) {   // else nothing is sure and all are in the band
+                above = key_of(T + E2);
+                below = key_of(T - E2);
+            } else {
+                below = 1u;
+            }
+            int c[3] = {0, 0, 0};
+            each_key([&](int, uint32_t k) {
+                c[0] += k > above;
+                c[1] += k >= below && k <= above;
+            });
+            sums(c);
+            const int take = f - c[0];   // winners that come from the band
+            all = take == c[1];
+            if (!all) {
+                exact_weights();
                 for (int base = warp * 32; base < np; base += NT) {
-                    const uint32_t mine = base + lane < np ? key_at(base + lane) : 0u;
-                    for (unsigned m = __ballot_sync(kAll, mine >= below && mine <= above); m; m &= m - 1) {
+                    const int mine = base + lane;
+                    const uint32_t k = mine < np ? key_at(mine, HELD ? held_x[mine] : read_x(mine)) : 0u;
+                    for (unsigned m = __ballot_sync(kAll, k >= below && k <= above); m; m &= m - 1) {
                         const int i = base + __ffs(m) - 1;
                         const double e = exact_score(i);
                         if (lane == 0) exact[i] = e;
@@ -785,12 +821,11 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
                 }
                 __syncthreads();
                 auto count = [&](uint64_t x, int &n, bool strict) {
-                    for (int i = tid; i < np; i += NT) {
-                        const uint32_t k = key_at(i);
-                        if (k < below || k > above) continue;
+                    each_key([&](int i, uint32_t k) {
+                        if (k < below || k > above) return;
                         const uint64_t e = key_of(exact[i]);
                         n += strict ? e > x : e >= x;
-                    }
+                    });
                 };
                 edge = nth_largest<uint64_t>(0ull, 64, take, sums, [&](uint64_t x, int &n) { count(x, n, false); });
                 int n[3] = {0, 0, 0};
@@ -799,66 +834,54 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
                 ties = take - n[0];
             }
         }
-    }
-    // the outcome of every page: thread t's pages of a batch are bit t % 32 of their words
-    for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
-        uint32_t k[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) k[u] = key_at(i0 + u * NT);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int i = i0 + u * NT;
-            if (i - lane >= np) break;   // the same for the warp
-            bool win = i < np && (i < lo || i >= hi), tie = false;
-            if (i < np && !win && f > 0) {
-                win = k[u] > above;
-                if (!win && k[u] >= below) {   // in the band
-                    const uint64_t e = all ? 1ull : key_of(exact[i]);
-                    win = all || e > edge;
-                    tie = !all && e == edge;
-                }
+        each_key([&](int i, uint32_t k) {
+            bool win = (i < np && !candidate(i)) || k > above, tie = false;
+            if (!win && k && k >= below) {   // in the band
+                const uint64_t e = all ? 1ull : key_of(exact[i]);
+                win = all || e > edge;
+                tie = !all && e == edge;
             }
             const unsigned w = __ballot_sync(kAll, win), t = __ballot_sync(kAll, tie);
-            if (lane == 0) {
+            if (lane == 0 && i < np) {
                 words[i / 32] = w;
-                if (!all) tie_words[i / 32] = t;
+                tie_words[i / 32] = t;
             }
+        });
+        __syncthreads();
+        if (!all) {   // of the pages that tie at the edge, the lowest `ties` win
+            const int each = (n_words + NT - 1) / NT, w0 = min(tid * each, n_words), w1 = min(w0 + each, n_words);
+            int n = 0, total;
+            for (int i = w0; i < w1; ++i) n += __popc(tie_words[i]);
+            int left = ties - block_scan<NT>(n, warps, total);
+            for (int i = w0; i < w1 && left > 0; ++i)
+                for (uint32_t t = tie_words[i]; t && left > 0; t &= t - 1, --left) words[i] |= t & -t;
         }
     }
-    __syncthreads();
     // every thread takes `each` consecutive words
     const int each = (n_words + NT - 1) / NT, w0 = min(tid * each, n_words), w1 = min(w0 + each, n_words);
-    int total;
-    if (!all) {   // of the pages that tie at the edge, the lowest `ties` win
-        int n = 0;
-        for (int i = w0; i < w1; ++i) n += __popc(tie_words[i]);
-        int left = ties - block_scan<NT>(n, warps, total);
-        for (int i = w0; i < w1 && left > 0; ++i)
-            for (uint32_t t = tie_words[i]; t && left > 0; t &= t - 1, --left) words[i] |= t & -t;
-    }
-    int n = 0;
+    int n = 0, total;
     for (int i = w0; i < w1; ++i) n += __popc(words[i]);
     int at = block_scan<NT>(n, warps, total);
-    for (int i = w0; i < w1; ++i) {
-        places[i] = at;
-        at += __popc(words[i]);
-    }
-    __syncthreads();
-    // The winners' numbers first (over the scores, which have done their work), so that each
-    // thread then waits for one block-table read and not for one per word of its warp.
-    int *won = reinterpret_cast<int *>(keys);
-    for (int base = warp * 32; base < np; base += NT) {
-        const uint32_t w = words[base / 32];
-        if (w >> lane & 1) {
-            const int to = places[base / 32] + __popc(w & ((1u << lane) - 1));
-            if constexpr (HELD) won[to] = base + lane;
-            else out[to] = bt[base + lane];
-        }
-    }
     if constexpr (HELD) {
+        // The winners' numbers first (over the scores, which have done their work), so that each
+        // thread then waits for one block-table read and not for one per winner of its words.
+        int *won = reinterpret_cast<int *>(held_x);
+        for (int i = w0; i < w1; ++i)
+            for (uint32_t w = words[i]; w; w &= w - 1) won[at++] = i * 32 + __ffs(w) - 1;
         __syncthreads();
 #pragma unroll 4
         for (int i = tid; i < kept; i += NT) out[i] = bt[won[i]];
+    } else {
+        int *places = reinterpret_cast<int *>(tie_words + (p.max_blocks + 31) / 32);
+        for (int i = w0; i < w1; ++i) {
+            places[i] = at;
+            at += __popc(words[i]);
+        }
+        __syncthreads();
+        for (int base = warp * 32; base < np; base += NT) {
+            const uint32_t w = words[base / 32];
+            if (w >> lane & 1) out[places[base / 32] + __popc(w & ((1u << lane) - 1))] = bt[base + lane];
+        }
     }
 }
 
@@ -947,9 +970,8 @@ extern "C" int pa_page_bounds(void *bounds, const void *k_cache, const int32_t *
     if (!aligned(bounds, 16) || !aligned(k_cache, 16))
         return api_fail(PA_ERR_INVALID, "bounds and the key pool must be 16-byte aligned");
     // pages that max_new_tokens tokens can touch: one more when they start inside a page
-    int pages = (max_new_tokens + kBlockSize - 1) / kBlockSize;
-    if (first_tokens) pages = (max_new_tokens + 2 * (kBlockSize - 1)) / kBlockSize;
-    if (pages > max_blocks_per_seq) pages = max_blocks_per_seq;
+    const int64_t touched = (static_cast<int64_t>(max_new_tokens) + (first_tokens ? 2 : 1) * (kBlockSize - 1)) / kBlockSize;
+    const int pages = static_cast<int>(touched < max_blocks_per_seq ? touched : max_blocks_per_seq);
     if (static_cast<int64_t>(num_seqs) * pages * num_kv_heads / 8 >= INT32_MAX)
         return api_fail(PA_ERR_UNSUPPORTED, "too many pages for one launch");
     const int elem = kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2;
@@ -1013,6 +1035,8 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
     if (num_seqs > 65535 || num_kv_heads > 65535)
         return api_fail(PA_ERR_UNSUPPORTED, "num_seqs %d, num_kv_heads %d: at most 65535", num_seqs,
                         num_kv_heads);
+    if (num_blocks > (int64_t(1) << 32) / num_kv_heads / head_dim * (kv_dtype == PA_KV_FP8_E4M3 ? 8 : 4))
+        return api_fail(PA_ERR_UNSUPPORTED, "num_blocks %lld: bounds of 2^32 16-byte units at most", (long long)num_blocks);
     if (num_seqs == 0) return PA_OK;
     if (!page_tables || !page_lens || !q || !bounds || !block_tables || !seq_lens)
         return api_fail(PA_ERR_INVALID, "null pointer argument");
@@ -1024,6 +1048,10 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
         return api_fail(PA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (!workspace || !aligned(workspace, 256))
         return api_fail(PA_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+    if (api_overlap(page_lens, num_seqs, seq_lens, num_seqs) ||
+        api_overlap(page_tables, static_cast<int64_t>(num_seqs) * num_kv_heads * max_pages, block_tables,
+                    static_cast<int64_t>(num_seqs) * max_blocks_per_seq))
+        return api_fail(PA_ERR_INVALID, "page_lens and page_tables must not be seq_lens and block_tables");
     char *ws = static_cast<char *>(workspace);
     SelectParams p = {};
     p.page_tables = page_tables;

@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 // its scores are
                 const int ex = static_cast<int>(__float_as_uint(most) >> 23 & 0xff);
                 const float s = ex == 255 ? NAN : ex > 0 ? __uint_as_float(static_cast<uint32_t>(min(max(127 + 7 + 127 - ex, 1), 254)) << 23) : 1.f;
-                scale = p.scale_log2 * p.k_scale / s;
+                scale = fmaxf(p.scale_log2 * p.k_scale / s, 0x1p-126f);   // above zero: -inf times it stays so
                 if (busy) {
 #pragma unroll
                     for (int c = 0; c < HD / 16; ++c) {

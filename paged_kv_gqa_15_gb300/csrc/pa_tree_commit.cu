@@ -124,11 +124,19 @@ extern "C" int pa_tree_commit(void *const *pools, int num_pools, const int32_t *
     if (!block_tables || !seq_lens || !qo_indptr || !accept_lens || !new_seq_lens ||
         (max_accept > 0 && !accepted) || (num_pools > 0 && !pools))
         return api_fail(PA_ERR_INVALID, "null pointer argument");
-    if (new_seq_lens == seq_lens)
-        return api_fail(PA_ERR_INVALID, "new_seq_lens must not be seq_lens");
+    if (api_overlap(new_seq_lens, num_seqs, seq_lens, num_seqs) ||
+        api_overlap(new_seq_lens, num_seqs, accept_lens, num_seqs) ||
+        api_overlap(new_seq_lens, num_seqs, qo_indptr, num_seqs + 1))
+        return api_fail(PA_ERR_INVALID, "new_seq_lens must not be seq_lens, accept_lens or qo_indptr");
     for (int i = 0; i < num_pools; ++i)
         if (!pools[i] || (reinterpret_cast<uintptr_t>(pools[i]) & 15u))
             return api_fail(PA_ERR_INVALID, "pools[%d] is NULL or not 16-byte aligned", i);
+    // a pool moved twice would take its rows from where the first move left others
+    for (int i = 1; i < num_pools; ++i) {
+        bool again = false;
+        for (int j = 0; j < i; ++j) again |= pools[j] == pools[i];
+        if (again) return api_fail(PA_ERR_INVALID, "pools[%d] is listed twice", i);
+    }
     CommitParams p;
     std::memset(&p, 0, sizeof p);
     const int elem = kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2;

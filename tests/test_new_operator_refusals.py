@@ -93,6 +93,10 @@ def test_tree_refuses_a_workspace_one_byte_short(lib):
     (dict(new=None), pa.PA_ERR_INVALID),
     (dict(pools=(ctypes.c_void_p * 2)(0x10000, 0x20008)), pa.PA_ERR_INVALID),
     (dict(pools=(ctypes.c_void_p * 2)(0x10000, 0)), pa.PA_ERR_INVALID),
+    (dict(pools=(ctypes.c_void_p * 2)(0x10000, 0x10000)), pa.PA_ERR_INVALID),         # moved twice
+    (dict(pools=(ctypes.c_void_p * 4)(0x10000, 0x20000, 0x30000, 0x20000), n=4), pa.PA_ERR_INVALID),
+    (dict(new=OFF16, al=OFF16), pa.PA_ERR_INVALID),
+    (dict(new=OFF4), pa.PA_ERR_INVALID),                                               # overlaps seq_lens
     (dict(B=0), pa.PA_OK),
 ])
 def test_commit_refusals(lib, kw, code):
@@ -135,6 +139,7 @@ def test_bounds_refusals(lib, kw, code):
     (dict(bs=32), pa.PA_ERR_UNSUPPORTED),
     (dict(nb=0), pa.PA_ERR_INVALID),
     (dict(mb=0), pa.PA_ERR_INVALID),
+    (dict(nb=1 << 27), pa.PA_ERR_UNSUPPORTED),
     (dict(mb=524289), pa.PA_ERR_UNSUPPORTED),
     (dict(most=0), pa.PA_ERR_INVALID),
     (dict(most=1 << 28), pa.PA_ERR_INVALID),
@@ -149,6 +154,8 @@ def test_bounds_refusals(lib, kw, code):
     (dict(bytes=0), pa.PA_ERR_WORKSPACE),
     (dict(ws=OFF16), pa.PA_ERR_WORKSPACE),
     (dict(ws=None), pa.PA_ERR_WORKSPACE),
+    (dict(pt=ODD), pa.PA_ERR_INVALID),                # over block_tables
+    (dict(pt=ctypes.c_void_p(0x90000)), pa.PA_ERR_INVALID),   # page_lens is seq_lens
     (dict(B=0), pa.PA_OK),
 ])
 def test_select_refusals(lib, kw, code):

@@ -106,6 +106,17 @@ def test_bounds_of_new_tokens_only(fp8):
     assert pa.device_status() == 0
 
 
+def test_bounds_of_as_many_new_tokens_as_there_may_be():
+    c = make([33, 70], 3, 3, 128, 19)
+    first = torch.tensor([16, 30], dtype=torch.int32, device=DEV)
+    want = ref64.bounds(c["bounds"], c["k"], c["table"].cpu(), c["lens"].cpu(), first, "HND")
+    fill_bounds(c, first, new=2 ** 31 - 1)
+    assert same(c["bounds"], want)
+    fill_bounds(c, new=2 ** 31 - 1)
+    assert same(c["bounds"], ref64.bounds(want, c["k"], c["table"].cpu(), c["lens"].cpu(), [0, 0], "HND"))
+    assert pa.device_status() == 0
+
+
 def test_bounds_hand_nan_and_infinities_on():
     c = make([40], 2, 2, 64, 10)
     page = int(c["table"][0, 1])
@@ -194,6 +205,16 @@ def test_pages_that_32_bits_cannot_tell_apart():
     c["bounds"][:, 0, :, 0] = 1024.0
     c["bounds"][:, 0, :, 1] = value.to(torch.bfloat16).to(DEV)[:, None]
     check_select(c, 30, 0, 1)
+
+
+def test_products_below_the_normal_numbers():
+    """Products of about 2^-142, of which fp32 keeps seven bits."""
+    c = make([1600, 1440], 4, 2, 64, 54)
+    c["q"] *= 2.0 ** -70
+    c["k"] *= 2.0 ** -72
+    fill_bounds(c)
+    for most in (10, 30, 60):
+        check_select(c, most, 0, 1)
 
 
 def test_scores_that_are_not_finite():

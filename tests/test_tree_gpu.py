@@ -143,6 +143,17 @@ def test_masks_that_are_not_trees(fp8):
     assert pa.device_status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_that_all_but_vanish(fp8):
+    """q of about 2^-120 and a scale of 2^-40: every weight is the same, and a row without a key
+    in a tile, or in any, stays a number."""
+    c = make([12, 200], [12, 100], 4, 2, 64, seed=31, fp8=fp8, shape="any")
+    c["q"] *= 2.0 ** -120
+    c["scale"] = 2.0 ** -40
+    check(gpu(c), call(gpu(c)))
+    assert pa.device_status() == 0
+
+
 def test_unseen_nodes_and_stale_rows_may_hold_nan():
     c = make([70, 33], [8, 8], 8, 2, 128, seed=11)
     c["mask"][3] = 1 << 3
