@@ -235,6 +235,16 @@ __device__ __forceinline__ T weighed(T w, T x) {
     return w == T(0) ? T(0) : w * x;
 }
 
+// 16 bytes of global memory to shared memory, past L1, without a register in between.
+__device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Element d of a bounds row as a float.
 template <bool FP8>
 __device__ __forceinline__ float bound_value(const uint8_t *row, int d) {
@@ -274,13 +284,14 @@ struct ScoreCfg {
     static constexpr int LANES = UNITS < 32 ? UNITS : 32;
     static constexpr int PARTS = UNITS / LANES;          // units a lane takes of a page
     static constexpr int PER = 32 / LANES;               // pages of a load
-    static constexpr int LOADS = (FP8 ? 4 : 8) / PARTS;  // page loads of a group
+    static constexpr int LOADS = 8 / PARTS;              // page loads of a group: 4 KB
     static constexpr int GROUP = LOADS * PER;            // pages of a group
 };
 
 constexpr int kLeastGroup = 4;     // of any ScoreCfg
 constexpr int kScoreThreads = 256;
-constexpr int kScoreSeqs = 1024;   // sequences per launch (their prefix is in shared memory)
+constexpr size_t kScoreSmem = kScoreThreads * 2 * 8 * 16;   // two groups' bounds per warp
+constexpr int kScoreSeqs = 512;    // sequences per launch (their prefix is in shared memory)
 
 template <int HD, bool FP8>
 __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_constant__ SelectParams p) {
@@ -288,6 +299,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
     static_assert(C::GROUP >= kLeastGroup && C::GROUP <= 32, "group");
     constexpr int UNITS = C::UNITS, LANES = C::LANES, PARTS = C::PARTS, PER = C::PER, LOADS = C::LOADS;
     constexpr int E = FP8 ? 16 : 8;               // elements of a unit
+    extern __shared__ __align__(16) uint32_t dyn[];
     __shared__ int64_t pref[kScoreSeqs + 1];      // groups before sequence b
     __shared__ int pages[kScoreSeqs];
     __shared__ int64_t even;                      // groups of a warp's run
@@ -331,46 +343,60 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
         const int mid = (b + hi) >> 1;
         if (pref[mid] <= u) b = mid; else hi = mid;
     }
-    int groups = (pages[b] + C::GROUP - 1) / C::GROUP;
+    auto groups_of = [&](int b) { return (pages[b] + C::GROUP - 1) / C::GROUP; };
     const int64_t in = u - pref[b];               // below nkv groups
-    int kh = in <= INT32_MAX ? static_cast<int>(in) / groups : static_cast<int>(in / groups);
-    int grp = static_cast<int>(in - static_cast<int64_t>(kh) * groups);
+    int kh = in <= INT32_MAX ? static_cast<int>(in) / groups_of(b) : static_cast<int>(in / groups_of(b));
+    int grp = static_cast<int>(in - static_cast<int64_t>(kh) * groups_of(b));
     const int unit = lane % LANES, sub = lane / LANES;
     const int g = p.nq / p.nkv;
     auto page_id = [&](int b, int grp) -> int {
         const int i = grp * C::GROUP + lane;
         return lane < C::GROUP && i < pages[b] ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + i] : 0;
     };
-    int id = page_id(b, grp);
-    float w[PARTS][E];   // this lane's weights: N for the units of the min row (a page's first half), else P
-    for (bool fresh = true; u < end; ++u) {
-        // this group's bounds first: nothing here waits for the query
+    auto advance = [&](int &b, int &kh, int &grp) {
+        if (++grp < groups_of(b)) return;
+        grp = 0;
+        if (++kh < p.nkv) return;
+        kh = 0;
+        do ++b; while (b + 1 < p.num_seqs && pref[b + 1] == pref[b]);
+    };
+    // Sends a group's bounds to this lane's places of a stage; the pages with ids out of range.
+    uint4 *ring = reinterpret_cast<uint4 *>(dyn) + warp * (2 * 8 * 32) + lane;
+    auto send = [&](int stage, int b, int kh, int grp, int id) -> unsigned {
         const bool known = id >= 0 && id < p.num_blocks;
         if (!known) atomicOr(p.status, kStatusBounds);
-        const unsigned unknown = __ballot_sync(kAll, !known);
-        const int first = grp * C::GROUP, n = min(C::GROUP, pages[b] - first);
+        const int n = min(C::GROUP, pages[b] - grp * C::GROUP);
         // lane i knows where page i's bounds are, in units of 16 bytes (the host sees to it that 32
         // bits hold them); lanes past the group's pages take its first
         const uint32_t place = (static_cast<uint32_t>(__shfl_sync(kAll, known ? id : 0, lane < n ? lane : 0)) * p.nkv + kh) * UNITS;
         const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds) + unit;
-        uint4 raw[LOADS][PARTS];
 #pragma unroll
         for (int k = 0; k < LOADS; ++k) {
             const uint32_t at = __shfl_sync(kAll, place, k * PER + sub);
 #pragma unroll
-            for (int v = 0; v < PARTS; ++v) raw[k][v] = __ldg(src + (at + v * LANES));
+            for (int v = 0; v < PARTS; ++v)
+                cp_async_16(ring + (stage * 8 + k * PARTS + v) * 32, src + (at + v * LANES));
         }
+        return __ballot_sync(kAll, !known);
+    };
+    int stage = 0;
+    unsigned unknown = send(0, b, kh, grp, page_id(b, grp));
+    cp_async_commit();
+    int b1 = b, kh1 = kh, grp1 = grp;             // the next group, and its ids
+    advance(b1, kh1, grp1);
+    int id1 = u + 1 < end ? page_id(b1, grp1) : 0;
+    float w[PARTS][E];   // this lane's weights: N for the units of the min row (a page's first half), else P
+    for (bool fresh = true; u < end; ++u) {
+        unsigned unknown1 = 0;
+        int b2 = b1, kh2 = kh1, grp2 = grp1, id2 = 0;
+        if (u + 1 < end) {
+            unknown1 = send(stage ^ 1, b1, kh1, grp1, id1);
+            advance(b2, kh2, grp2);
+            if (u + 2 < end) id2 = page_id(b2, grp2);
+        }
+        cp_async_commit();
+        const int first = grp * C::GROUP, n = min(C::GROUP, pages[b] - first);
         const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
-        // where the next group is, and its ids
-        int b1 = b, kh1 = kh, grp1 = grp + 1;
-        if (grp1 == groups) {
-            grp1 = 0;
-            if (++kh1 == p.nkv) {
-                kh1 = 0;
-                do ++b1; while (b1 + 1 < p.num_seqs && pref[b1 + 1] == pref[b1]);
-            }
-        }
-        const int id1 = u + 1 < end ? page_id(b1, grp1) : 0;
         if (fresh) {
 #pragma unroll
             for (int v = 0; v < PARTS; ++v) {
@@ -400,6 +426,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
                     for (int e = 0; e < E; ++e) w[v][e] = -w[v][e];
             }
         }
+        cp_async_wait<1>();     // this group's bounds are here; a lane reads what it sent for
+        const uint4 *raw = ring + stage * 8 * 32;
         float x[LOADS];         // the pages' sums
         float far[PARTS][E];    // the largest magnitudes of the group's elements
         bool odd = false;
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
                 float f[2][E];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    unpack16<FP8>(raw[k + u][v], f[u]);
+                    unpack16<FP8>(raw[((k + u) * PARTS + v) * 32], f[u]);
                     float2 c[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};   // chains of E / 4 products
 #pragma unroll
                     for (int e = 0; e < E; e += 2)
@@ -429,19 +457,19 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
                 odd |= s[u] != s[u];
             }
         }
-        // a zero weight met an infinity, or a sum is a NaN: the exact rule, from the bounds read again
-        if (__any_sync(kAll, odd)) {
-#pragma unroll
+        if (odd) {   // a zero weight met an infinity, or a sum is a NaN: the exact rule
+#pragma unroll 1
             for (int k = 0; k < LOADS; ++k) {
-                const uint32_t at = __shfl_sync(kAll, place, k * PER + sub);
-                x[k] = 0.f;
+                float y = 0.f;
 #pragma unroll
                 for (int v = 0; v < PARTS; ++v) {
                     float f[E];
-                    unpack16<FP8>(__ldg(src + (at + v * LANES)), f);
+                    unpack16<FP8>(raw[(k * PARTS + v) * 32], f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[k] += weighed(w[v][e], f[e]);
+                    for (int e = 0; e < E; ++e) y += weighed(w[v][e], f[e]);
                 }
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) x[j] = j == k ? y : x[j];
             }
         }
         float most = 0.f;   // S of a page with the group's largest magnitudes
@@ -475,11 +503,11 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
         }
         if (lane == 0) p.span[row * p.groups + grp] = most;
         fresh = kh1 != kh || b1 != b;
-        if (b1 != b) groups = (pages[min(b1, p.num_seqs - 1)] + C::GROUP - 1) / C::GROUP;
-        b = b1;
-        kh = kh1;
-        grp = grp1;
-        id = id1;
+        b = b1, kh = kh1, grp = grp1;
+        b1 = b2, kh1 = kh2, grp1 = grp2;
+        unknown = unknown1;
+        id1 = id2;
+        stage ^= 1;
     }
 }
 
@@ -623,8 +651,8 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     const int n_words = (np + 31) / 32;
     uint32_t *tie_words = words + (p.max_blocks + 31) / 32;
     auto candidate = [&](int i) { return static_cast<unsigned>(i - lo) < static_cast<unsigned>(hi - lo); };
-    // a candidate's score, and -infinity for other pages
-    auto read_x = [&](int i) { return candidate(i) ? score[i] : -INFINITY; };
+    // a candidate's score, infinity for pages that are chosen anyway, and -infinity past the pages
+    auto read_x = [&](int i) { return candidate(i) ? score[i] : (i < np ? INFINITY : -INFINITY); };
     // calls f(page, score) for this thread's pages, a batch of scores read before any call
     auto each_x = [&](auto f) {
         for (int i0 = tid; i0 < held; i0 += NT * kBatch) {
@@ -678,7 +706,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
                 const int i = i0 + u * NT;
                 if constexpr (HELD) held_x[i] = x[u];
                 least = fminf(least, candidate(i) ? x[u] : INFINITY);
-                top = fmaxf(top, x[u]);
+                top = fmaxf(top, candidate(i) ? x[u] : -INFINITY);
                 odd |= candidate(i) && !(fabsf(x[u]) < INFINITY);
             }
         }
@@ -708,7 +736,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     bool settled = !odd && scale > 0.f && margin < 8.f;   // not for an infinite or NaN scale either
     if (settled) {
         each_x([&](int, float x) {
-            if (x != -INFINITY) atomicAdd(&hist[static_cast<int>(place_of(x))], 1);
+            if (fabsf(x) < INFINITY) atomicAdd(&hist[static_cast<int>(place_of(x))], 1);
         });
         __syncthreads();
         constexpr int EACH = kBins / NT;
@@ -728,7 +756,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         const float from = bin - margin, past = bin + 1 + margin;
         each_x([&](int i, float x) {
             const float y = place_of(x);
-            const unsigned w = __ballot_sync(kAll, y >= past || (i < np && !candidate(i)));
+            const unsigned w = __ballot_sync(kAll, y >= past);
             if (lane == 0 && i < np) words[i / 32] = w;
             if (y >= from && y < past) {
                 const int at = atomicAdd(&near_n, 1);
@@ -903,6 +931,8 @@ cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
     if (configured.load() != dev) {
         int n = 0;
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(score_kernel<HD, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
         allow(select_kernel<HD, FP8, 256, true>, kShortPages, 256, true);
         allow(select_kernel<HD, FP8, 512, true>, kHeldPages, 512, true);
         allow(select_kernel<HD, FP8, 512, false>, kMostPages, 512, false);
@@ -915,7 +945,7 @@ cudaError_t launch_select(SelectParams &p, cudaStream_t stream) {
         const int64_t most = (static_cast<int64_t>(p.num_seqs) * p.nkv * p.groups + 7) / 8;
         const int64_t room = 3 * sm_count.load();
         const unsigned grid = static_cast<unsigned>(most < room ? most : room);
-        e = launch_after(score_kernel<HD, FP8>, dim3(grid), kScoreThreads, p, stream);
+        e = launch_after(score_kernel<HD, FP8>, dim3(grid), kScoreThreads, p, stream, kScoreSmem);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(p.nkv, p.num_seqs);

@@ -42,6 +42,7 @@
 //    only: weights far under one large maximum lost their bits, and they can be most of the sum.
 //    Two more warps turning V into f16 left too little shared memory for tiles on their way: 261 us.
 //  * Every mbarrier wait is bounded.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -1111,7 +1112,11 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::SMEM;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return e;
-    if (grid == 1) return cudaSuccess;   // nothing is cut
+    // Runs of at most kCutTiles are never cut (TreeShares::whole), and one share cuts nothing.
+    int64_t longest = (static_cast<int64_t>(p.max_blocks) * kBlockSize + kKeys - 1) / kKeys;
+    if (p.window > 0)
+        longest = std::min(longest, (static_cast<int64_t>(p.window) + p.max_tree_len + kKeys - 1) / kKeys + 1);
+    if (grid == 1 || longest <= kCutTiles) return cudaSuccess;
     cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), static_cast<unsigned>((a.slot_rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
