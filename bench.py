@@ -66,21 +66,21 @@ PARITY_MAX_ABS, PARITY_MEAN_ABS = 2e-2, 2e-3
 # for the source file hash they were measured on (otherwise reported as null).
 TRAFFIC = {
     # ncu capture of one decode_tc_kernel<4> launch on the Llama-8B decode workload:
-    # dram__bytes_read.sum 568.34 MB + dram__bytes_write.sum 5.08 MB
+    # dram__bytes_read.sum 568.34 MB + dram__bytes_write.sum 5.10 MB
     "decode_partitions:llama8b_decode_b64_h32kv8_d128": {
-        "src": "e53731200feeaa9e", "bytes_per_launch": 573424896},
+        "src": "9e19220740debc0a", "bytes_per_launch": 573436416},
     # ncu capture of one prefill_kernel<128,64,ragged> launch on the 16-request ragged
-    # causal prefill: dram__bytes_read.sum 298.53 MB + dram__bytes_write.sum 108.54 MB
+    # causal prefill: dram__bytes_read.sum 300.23 MB + dram__bytes_write.sum 108.27 MB
     "ragged_prefill:ragged_prefill_r16_h32kv8_d128": {
-        "src": "fe29602adfbe4d3a", "bytes_per_launch": 407071488},
+        "src": "ba1d5a8243b2d09f", "bytes_per_launch": 408506880},
     # ncu capture of one prefill_kernel<256,64,paged> launch on the chunked paged prefill:
-    # dram__bytes_read.sum 396.10 MB + dram__bytes_write.sum 23.06 MB
+    # dram__bytes_read.sum 387.76 MB + dram__bytes_write.sum 22.45 MB
     "ragged_prefill:chunked_paged_prefill_r8_h16kv8_d256": {
-        "src": "fe29602adfbe4d3a", "bytes_per_launch": 419157248},
+        "src": "ba1d5a8243b2d09f", "bytes_per_launch": 410207744},
     # ncu capture of one decode_tc8_kernel<4> launch on the Llama-8B decode workload over
-    # an FP8 cache: dram__bytes_read.sum 284.49 MB + dram__bytes_write.sum 4.33 MB
+    # an FP8 cache: dram__bytes_read.sum 284.48 MB + dram__bytes_write.sum 4.31 MB
     "decode_partitions:llama8b_decode_fp8_b64_h32kv8_d128": {
-        "src": "c96d19f3ccc7f4f1", "bytes_per_launch": 288820224},
+        "src": "69661ec026ed3d90", "bytes_per_launch": 288793344},
 }
 
 
