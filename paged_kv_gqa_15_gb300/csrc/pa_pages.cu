@@ -73,9 +73,9 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h2) {
 // A unit is one (sequence, page, kv head), its heads next to each other; a warp takes kUnits of
 // them in a row.  Lane u looks unit u up (lengths and page id: two dependent reads, once per
 // warp), and the rows of the next unit are on their way while one is compared.  A row is CPR
-// chunks of 16 bytes; a load instruction reads 32 / CPR rows.  Bound by streaming K: a warp per
-// unit reached 88 % of the measured copy rate on 618 MB of keys, its 4 KB waiting for the
-// look-up every time.
+// chunks of 16 bytes; a load instruction reads 32 / CPR rows.  Bound by streaming K: 104 us for
+// 578 MB of keys (8 prompts of 8k-65k tokens) with their 72 MB of bounds, 92 % of the measured copy
+// rate; a warp per unit reached 88 %, its 4 KB waiting for the look-up every time.
 constexpr int kUnits = 4;
 
 template <int HD, bool FP8>
@@ -269,14 +269,16 @@ __device__ __forceinline__ void unpack16(const uint4 &raw, float (&f)[FP8 ? 16 :
 }
 
 // The pass reads 2 head_dim elements a page and multiplies each once: streaming them is its
-// bound, so every SM holds 24 warps with up to 4 KB of bounds on their way each, and what comes
+// bound, so every SM holds 24 warps with up to 8 KB of bounds on their way each, and what comes
 // before the stream is paid once: the (sequence, kv head, group of pages) steps form a line
-// and every warp takes an equal run of it, with the next group's page ids read a group ahead.
-// (A warp per 32 pages paid its two dependent reads and its query heads for every 16 KB:
-// 37 us for 168 MB; bulk copies of single pages into shared memory were slower still, 47 us:
-// 512 bytes are too little for one.)  A page is UNITS units of 16 bytes (min row, then max
-// row): 32 / UNITS pages a load, and the sums of a group's pages are reduced over the lanes at
-// once by halving exchanges (16 shuffles for 16 sums instead of 80).
+// and every warp takes an equal run of it, with the next group's bounds sent for while one is
+// multiplied and the page ids of the one after it.  29 us for 140 MB of bounds (8 sequences of
+// 32k-131k tokens, 8 kv heads), 7 us of them the launch, the lengths and the last groups.  (A warp
+// per 32 pages paid its two dependent reads and its query heads for every 16 KB: 37 us; bulk copies
+// of single pages into shared memory were slower still, 47 us: 512 bytes are too little for one.)
+// A page is UNITS units of 16 bytes (min row, then max row): 32 / UNITS pages a load, and the sums
+// of a group's pages are reduced over the lanes at once by halving exchanges (9 shuffles for 8
+// sums instead of 40).  Over 8-bit bounds the conversions are as long as the stream (20 us for 39 MB).
 template <int HD, bool FP8>
 struct ScoreCfg {
     static constexpr int PAGE = 2 * HD * (FP8 ? 1 : 2);
@@ -613,7 +615,9 @@ size_t select_smem(int max_blocks, int threads, bool held) {
 // one scan over the words' counts gives every chosen page its place, in page order.  A row is one
 // chain of dependent steps, bound by their latency and by what its SM can issue, not by its 32 KB of
 // scores: passes take eight scores a thread at once, all read before any is used (one after another
-// they cost 11800 of a row's 31600 cycles in the first pass alone).
+// they cost 11800 of a row's 31600 cycles in the first pass alone).  A row of 131072 tokens takes
+// 14000 cycles, 64 rows 15 us; with passes of their own for the border's pages, the band around it
+// and every page's outcome they took 27500 and 21.
 template <int HD, bool FP8, int NT, bool HELD>
 __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p) {
     constexpr int ROW = HD * (FP8 ? 1 : 2);

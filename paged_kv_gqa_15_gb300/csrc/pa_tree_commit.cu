@@ -5,6 +5,10 @@
 // path in order.  The path ascends, so a_i >= i and a row is overwritten only after every
 // step that reads it (row i is read by steps i' <= i alone): no other thread touches the
 // chunk's column, so the move is safe in place without any barrier.
+//
+// Bound by latency: lengths, path, page ids and rows are four dependent reads, and a step moves
+// little (31 MB read and written for 118 accepted nodes in 32 layers: 9.4 us, 4.6 at the copy
+// rate).  Hence a thread per chunk, all pools in one launch, and four steps' rows read at once.
 #include <cstring>
 
 #include "../../include/pa.h"
