@@ -101,10 +101,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object (2.5 us of a call's host time), where torch
+# has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def pool_strides(cache: torch.Tensor, layout: str = "HND"):
@@ -113,26 +120,26 @@ def pool_strides(cache: torch.Tensor, layout: str = "HND"):
     HND: [num_blocks][num_kv_heads][block_size][head_dim];
     NHD: [num_blocks][block_size][num_kv_heads][head_dim]."""
     s = cache.stride()
-    assert cache.dim() == 4 and s[3] == 1, "pool must be 4-D with a contiguous head_dim"
+    assert len(s) == 4 and s[3] == 1, "pool must be 4-D with a contiguous head_dim"
     return (s[0], s[1], s[2]) if layout == "HND" else (s[0], s[2], s[1])
+
+
+_FP8_DTYPES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
 
 def kv_dtype_of(cache: torch.Tensor) -> int:
     """pa_kv_dtype of a pool tensor: bf16, or FP8 E4M3 codes (float8_e4m3fn or uint8)."""
-    if cache.dtype == torch.bfloat16:
+    dtype = cache.dtype
+    if dtype == torch.bfloat16:
         return PA_KV_BF16
-    if cache.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8)):
+    if dtype in _FP8_DTYPES:
         return PA_KV_FP8_E4M3
-    raise TypeError(f"unsupported KV cache dtype {cache.dtype}")
+    raise TypeError(f"unsupported KV cache dtype {dtype}")
 
 
 def _pool_geometry(cache, layout):
-    nb = cache.shape[0]
-    if layout == "HND":
-        nkv, bs, hd = cache.shape[1], cache.shape[2], cache.shape[3]
-    else:
-        bs, nkv, hd = cache.shape[1], cache.shape[2], cache.shape[3]
-    return nb, nkv, bs, hd
+    nb, a, b, hd = cache.shape
+    return (nb, a, b, hd) if layout == "HND" else (nb, b, a, hd)
 
 
 def _host_ptr(a):
@@ -370,12 +377,13 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, 
     nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
     sb, sh, st = pool_strides(k_cache, layout)
     rows, nq, _ = q.shape
-    assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and \
-        tree_mask.shape[0] == rows
+    mask_rows, words = tree_mask.shape
+    seqs, blocks = block_tables.shape
+    assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and mask_rows == rows
     _check(load().pa_tree_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                  _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
-                                 _ptr(tree_mask), tree_mask.shape[1], block_tables.shape[0], rows,
-                                 int(max_tree_len), nq, nkv, hd, bs, block_tables.shape[1], nb, sb,
+                                 _ptr(tree_mask), words, seqs, rows,
+                                 int(max_tree_len), nq, nkv, hd, bs, blocks, nb, sb,
                                  sh, st, float(sm_scale), int(sliding_window),
                                  kv_dtype_of(k_cache), float(k_scale), float(v_scale),
                                  _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -393,8 +401,10 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
     sb, sh, st = pool_strides(pools[0], layout)
     # a model has two pools a layer, so the checks go over whole lists
     n = len(pools)
-    for values in ([t.shape for t in pools], list(map(torch.Tensor.stride, pools)),
-                   [t.dtype for t in pools]):
+    layouts = list(map(torch.Tensor.is_contiguous, pools))   # contiguous ones need no strides
+    if not all(layouts):
+        layouts = list(map(torch.Tensor.stride, pools))
+    for values in ([t.shape for t in pools], layouts, [t.dtype for t in pools]):
         assert values.count(values[0]) == n, "pools differ in geometry"
     assert accepted.dtype == torch.int32 and accepted.is_contiguous()
     addresses = array.array("Q", list(map(torch.Tensor.data_ptr, pools)))
@@ -413,11 +423,12 @@ def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, firs
     max_new_tokens is at least seq_lens[b] - first_tokens[b] for every sequence."""
     nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
     sb, sh, st = pool_strides(k_cache, layout)
-    assert bounds.is_contiguous() and tuple(bounds.shape) == (nb, nkv, 2, hd) and \
+    seqs, blocks = block_tables.shape
+    assert bounds.is_contiguous() and bounds.shape == (nb, nkv, 2, hd) and \
         bounds.element_size() == k_cache.element_size()
     _check(load().pa_page_bounds(_ptr(bounds), _ptr(k_cache), _ptr(block_tables), _ptr(seq_lens),
-                                 _ptr(first_tokens), int(max_new_tokens), block_tables.shape[0],
-                                 nkv, hd, bs, block_tables.shape[1], nb, sb, sh, st,
+                                 _ptr(first_tokens), int(max_new_tokens), seqs,
+                                 nkv, hd, bs, blocks, nb, sb, sh, st,
                                  kv_dtype_of(k_cache), _stream(stream)))
 
 
@@ -432,10 +443,11 @@ def pa_select_pages(page_tables, page_lens, q, bounds, block_tables, seq_lens, w
     first sink_pages and the last recent_pages are always among them."""
     nb, nkv, _, hd = bounds.shape
     B, nq, _ = q.shape
-    assert bounds.is_contiguous() and page_tables.is_contiguous() and page_tables.shape[:2] == (B, nkv)
+    rows, heads, most = page_tables.shape
+    assert bounds.is_contiguous() and page_tables.is_contiguous() and rows == B and heads == nkv
     _check(load().pa_select_pages(_ptr(page_tables), _ptr(page_lens), _ptr(q), _ptr(bounds),
                                   _ptr(block_tables), _ptr(seq_lens), B, nq, nkv, hd, PAGE_TOKENS,
-                                  block_tables.shape[1], nb, page_tables.shape[2], int(sink_pages),
+                                  block_tables.shape[1], nb, most, int(sink_pages),
                                   int(recent_pages), kv_dtype_of(bounds), _ptr(workspace),
                                   workspace.numel(), _stream(stream)))
 
@@ -448,10 +460,11 @@ def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, 
     nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
     sb, sh, st = pool_strides(k_cache, layout)
     B, nq, _ = q.shape
-    assert page_tables.is_contiguous() and page_tables.shape[:2] == (B, nkv)
+    rows, heads, most = page_tables.shape
+    assert page_tables.is_contiguous() and rows == B and heads == nkv
     _check(load().pa_decode_pages(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(page_tables), _ptr(page_lens), B, nq, nkv, hd, bs,
-                                  page_tables.shape[2], nb, sb, sh, st, float(sm_scale),
+                                  most, nb, sb, sh, st, float(sm_scale),
                                   kv_dtype_of(k_cache), float(k_scale), float(v_scale),
                                   _ptr(workspace), workspace.numel(), _stream(stream)))
 
