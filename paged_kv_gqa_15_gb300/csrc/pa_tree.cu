@@ -290,11 +290,11 @@ __device__ __forceinline__ int mask_count(const uint64_t *mask, int T) {
     return n;
 }
 
-// The 64 mask bits from bit `at` (which may be negative) on.
-__device__ __forceinline__ uint64_t mask_bits_at(const uint64_t *mask, int at, int T) {
+// The 64 mask bits from bit `at` (which may be negative) on; word0 is the mask's first word.
+__device__ __forceinline__ uint64_t mask_bits_at(const uint64_t *mask, uint64_t word0, int at, int T) {
     if (at <= -64 || at >= T) return 0;
-    if (at < 0) return mask_word(mask, 0, T) << -at;
-    const uint64_t lo = mask_word(mask, at >> 6, T) >> (at & 63);
+    if (at < 0) return word0 << -at;
+    const uint64_t lo = (at < 64 ? word0 : mask_word(mask, at >> 6, T)) >> (at & 63);
     return at & 63 ? lo | mask_word(mask, (at >> 6) + 1, T) << (64 - (at & 63)) : lo;
 }
 
@@ -407,7 +407,14 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         tmem_alloc(&tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
-    // launched as a programmatic dependent: nothing before this point reads global memory
+    if (warp >= 2) {   // the first reads after the wait, into L2 beforehand
+        const unsigned t = blockIdx.x * 128 + threadIdx.x - 64, nt = gridDim.x * 128;
+        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, 1, p.max_blocks,
+                               static_cast<size_t>(p.total_rows) * p.num_q_heads * HD * 2, threadIdx.x - 64, 128);
+        prefetch_l2_lines(p.qo_indptr, (static_cast<size_t>(p.num_seqs) + 1) * 4, t, nt);
+        prefetch_l2_lines(p.tree_mask, static_cast<size_t>(p.total_rows) * p.mask_words * 8, t, nt);
+    }
+    // launched as a programmatic dependent: nothing before this point depends on global memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tree_prefix<FP8>(a, pref, run, blockIdx.x == 0);
     tc_fence_before_sync();
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             int page = page_fix(page_raw(w, w.j0), g);
             int raw = w.n > 1 ? page_raw(w, w.j0 + 1) : -2;
             load(0, g, page);
-            const TreeSegment next = stop ? w : next_segment();
+            TreeSegment next = w;
             for (int j = 0; j < w.n && !stop; ++j) {
                 if (j == 1) note_cut();
                 int page_next = 0;
@@ -575,6 +582,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 }
                 if (!stop) load(1, g + j, page);
                 page = page_next;
+                // the segment behind is looked up once this one's first tiles are on their way
+                if (j == 0 && !stop) next = next_segment();
             }
             g += w.n;
             w = next;
@@ -705,6 +714,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             const int head = w.head * a.group + (mine ? row % a.group : 0);
             const int ctx = w.L - w.T;
             const uint64_t *mask = p.tree_mask + static_cast<int64_t>(w.row0 + node) * p.mask_words;
+            // read now: the tile that needs it would wait for it
+            const uint64_t word0 = mine ? mask_word(mask, 0, w.T) : 0ull;
             int low = 0;                           // first context token this row sees
             if (p.window > 0) low = max(0, min(ctx, ctx + mask_count(mask, w.T) - p.window));
             const int seen_by_all = p.window > 0 ? max(0, min(ctx, ctx + w.T - p.window)) : 0;
@@ -818,7 +829,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                     if (edge) {
                         uint64_t see = 0;
                         if (mine) {
-                            see = (ones(ctx - base) & ~ones(low - base)) | mask_bits_at(mask, base - ctx, w.T);
+                            see = (ones(ctx - base) & ~ones(low - base)) | mask_bits_at(mask, word0, base - ctx, w.T);
 #pragma unroll
                             for (int e = 0; e < kPages; ++e)
                                 if (bad_pages >> e & 1) see &= ~(0xffffull << e * kBlockSize);
