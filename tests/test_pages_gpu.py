@@ -207,6 +207,31 @@ def test_pages_that_32_bits_cannot_tell_apart():
     check_select(c, 30, 0, 1)
 
 
+@pytest.mark.parametrize("most", [21, 25, 30])
+def test_a_few_pages_at_the_border_that_32_bits_cannot_tell_apart(most):
+    """20 pages above, 200 below, and 12 between whose scores differ below half a step of fp32."""
+    c = make([233 * 16], 1, 1, 128, 55)
+    c["q"].zero_()
+    c["q"][0, 0, :2] = torch.tensor([1024.0, 1.0])
+    rng = np.random.default_rng(3)
+    kind = rng.permutation(232)
+    first = np.where(kind < 20, 1200.0, np.where(kind < 32, 1024.0, 16.0 + 4 * (kind % 50)))
+    second = np.where((kind >= 20) & (kind < 32), kind * 2.0 ** -8, 0.0)
+    ids = c["table"][0, :232].long()
+    c["bounds"].zero_()
+    for d, x in ((0, first), (1, second)):
+        c["bounds"][ids, 0, :, d] = torch.from_numpy(x).to(torch.bfloat16).to(DEV)[:, None]
+    check_select(c, most, 0, 1)
+
+
+def test_more_sequences_than_a_launch_scores():
+    rng = np.random.default_rng(4)
+    c = make([int(n) for n in rng.integers(0, 120, 1100)], 2, 1, 64, 56)
+    fill_bounds(c)
+    check_select(c, 3, 1, 1)
+    assert pa.device_status() == 0
+
+
 def test_products_below_the_normal_numbers():
     """Products of about 2^-142, of which fp32 keeps seven bits."""
     c = make([1600, 1440], 4, 2, 64, 54)
