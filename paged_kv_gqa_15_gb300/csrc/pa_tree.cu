@@ -168,39 +168,45 @@ __device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
 constexpr int kMostTogether = 8;
 
 // pref[b] = tiles of the line before sequence b, run[b] the tiles of its runs, run[n] those of
-// the longest, run[n + 1] the row tiles that go together; all threads of the CTA call it.
+// the longest, run[n + 1] the row tiles that go together; all threads of the CTA call it, with
+// pref[0], run[n] and run[n + 1] cleared.
 template <bool FP8>
 __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, int *run, bool flag) {
     const TreeParams &p = a.p;
     const int n = p.num_seqs;
-    if (threadIdx.x == 0) {
-        pref[0] = 0;
-        run[n] = run[n + 1] = 0;
-    }
-    __syncthreads();
+    int most_tiles = 0, most_rows = 0;
     for (int b = threadIdx.x; b < n; b += kTreeThreads) {
         const TreeSeq s = tree_seq(p, b, flag);
         const int tiles = tree_tiles(s, p.window), row_tiles = (s.T + a.nodes - 1) / a.nodes;
         run[b] = tiles;
         pref[b + 1] = static_cast<int64_t>(tiles) * row_tiles * a.heads;
-        atomicMax(&run[n], tiles);
-        atomicMax(&run[n + 1], row_tiles);
+        most_tiles = max(most_tiles, tiles);
+        most_rows = max(most_rows, row_tiles);
+    }
+    most_tiles = __reduce_max_sync(kAll, most_tiles);
+    most_rows = __reduce_max_sync(kAll, most_rows);
+    if ((threadIdx.x & 31) == 0) {
+        atomicMax(&run[n], most_tiles);
+        atomicMax(&run[n + 1], most_rows);
     }
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         const int together = run[n + 1];
-        long long apart = 0, once = 0;   // tiles with row tiles one after another, and side by side
-        for (int b = lane; b < n; b += 32) {
-            apart += pref[b + 1];
-            once += static_cast<long long>(run[b]) * a.heads;
-        }
+        bool pair = !FP8 && together > 1 && together <= kMostTogether;
+        if (pair) {
+            long long apart = 0, once = 0;   // tiles with row tiles one after another, and side by side
+            for (int b = lane; b < n; b += 32) {
+                apart += pref[b + 1];
+                once += static_cast<long long>(run[b]) * a.heads;
+            }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            apart += __shfl_xor_sync(kAll, apart, o);
-            once += __shfl_xor_sync(kAll, once, o);
+            for (int o = 16; o; o >>= 1) {
+                apart += __shfl_xor_sync(kAll, apart, o);
+                once += __shfl_xor_sync(kAll, once, o);
+            }
+            pair = once * together * 3 <= apart * 4;
         }
-        const bool pair = !FP8 && together > 1 && together <= kMostTogether && once * together * 3 <= apart * 4;
         __syncwarp();
         if (pair)
             for (int b = lane; b < n; b += 32) pref[b + 1] = static_cast<int64_t>(run[b]) * a.heads;
@@ -242,14 +248,12 @@ struct TreeShares {
     static __device__ __forceinline__ int remainder(int64_t x, int d) {
         return x <= INT32_MAX ? static_cast<int>(x) % d : static_cast<int>(x % d);
     }
-    // the largest b with pref[b] <= u
+    // the largest b with pref[b] <= u, by a whole warp: every stride-th prefix, then those between
     __device__ __forceinline__ int sequence(int64_t u) const {
-        int lo = 0, hi = n;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pref[mid] <= u) lo = mid; else hi = mid;
-        }
-        return lo;
+        const int lane = threadIdx.x & 31, stride = (n + 31) >> 5;
+        const int lo = (__popc(__ballot_sync(kAll, lane * stride < n && pref[lane * stride] <= u)) - 1) * stride;
+        if (stride == 1) return lo;
+        return lo + __popc(__ballot_sync(kAll, lane < stride && lo + lane < n && pref[lo + lane] <= u)) - 1;
     }
     __device__ __forceinline__ int64_t begin(int c) const {
         if (c >= shares) return total;
@@ -378,6 +382,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x < 16) queue->bad_nodes[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
+        pref[0] = 0;
+        run[p.num_seqs] = run[p.num_seqs + 1] = 0;
         mbar_init(q_full, FP8 ? 4 : 1);
         mbar_init(q_empty, 1);
         mbar_init(o_free, 4);
@@ -415,6 +421,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         prefetch_l2_lines(p.tree_mask, static_cast<size_t>(p.total_rows) * p.mask_words * 8, t, nt);
     }
     // launched as a programmatic dependent: nothing before this point depends on global memory
+    __syncthreads();   // what tree_prefix adds to is cleared
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tree_prefix<FP8>(a, pref, run, blockIdx.x == 0);
     tc_fence_before_sync();
