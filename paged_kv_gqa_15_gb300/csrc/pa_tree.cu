@@ -67,10 +67,15 @@ constexpr int kTreeThreads = 192;
 constexpr int kMaxCtas = 304;       // two per SM of 152
 constexpr int kMaxSeqs = 960;       // sequences per launch (their prefix is in shared memory)
 
-// A cut run costs a partial tile's way out and back and a second kernel's work: about as much as
-// this many tiles (32 sequences of 500 tokens, 8 tiles a run, 128 rows: 39.6 us cut evenly, 26.0 in
-// whole runs; at 4000 tokens the two are level).
-constexpr int kCutTiles = 12;
+// A cut run costs a partial tile's way out and back and a second kernel's work: more than this many
+// tiles where the GPU is full (32 sequences of 500 tokens, 8 tiles a run, 128 rows: 39.6 us cut
+// evenly, 26.0 in whole runs; at 4000 tokens the two are level), and no more where it is not (3
+// sequences of 232-618 tokens at head_dim 256: 15 us cut, 25 in whole runs).
+constexpr int kCutTiles = 6;
+
+// Runs cut into this many pieces or more on average are joined by eight warps a row (4 runs of 680
+// tiles, 76 pieces each: 39 -> 29 us; 28 runs, 11 pieces: 20 -> 23 us).
+constexpr int kManyPieces = 12;
 
 constexpr uint32_t pow2_columns(uint32_t x) {
     uint32_t v = 32;
@@ -124,6 +129,7 @@ struct TreeLaunch {
     int group, kv_rep, heads;       // query heads per kernel group, groups per kv head, groups
     int nodes;                      // nodes of a row tile (its rows: nodes * group)
     int slot_rows;                  // rows of a partial slot
+    int ctas;                       // of the grid
 };
 
 // Sequence b's drafted rows and lengths; T = 0 (and the device status set when `flag`) if
@@ -254,6 +260,12 @@ struct TreeShares {
         const int lo = (__popc(__ballot_sync(kAll, lane * stride < n && pref[lane * stride] <= u)) - 1) * stride;
         if (stride == 1) return lo;
         return lo + __popc(__ballot_sync(kAll, lane < stride && lo + lane < n && pref[lo + lane] <= u)) - 1;
+    }
+    // the share tile u lies in, of an even cut
+    __device__ __forceinline__ int share_of(int64_t u) const {
+        const int64_t longer = (even + 1) * more;   // tiles of the shares that are one longer
+        return u < longer ? quotient(u, static_cast<int>(even) + 1)
+                          : more + quotient(u - longer, static_cast<int>(even));
     }
     __device__ __forceinline__ int64_t begin(int c) const {
         if (c >= shares) return total;
@@ -526,7 +538,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             TreeCut cut = {};
             if (run_begin >= 0 && run_begin >= line.begin(share - 1)) {
                 cut = run_cut;
-                while (line.begin(share - 1 + cut.pieces) < run_end) ++cut.pieces;
+                cut.pieces = line.share_of(run_end - 1) - share + 2;
             }
             if (lane == 0) a.cuts[blockIdx.x] = cut;
         };
@@ -999,33 +1011,22 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     }
 }
 
-// Joins the partial rows of every (sequence, kernel head group, row tile) that was cut: one
-// warp per row, the shares' partials in a fixed order, so the result does not depend on
-// timing.  Grid: x = CTA, y = eight rows; the CTA that had a cut run's second piece stands for
-// it.  The maxima and sums of up to 32 pieces are read at once, one per lane, and the
-// partial rows four at a time: a row costs a few memory round trips, not one per piece.  Bound by
-// them and by its launch: 6 us for the cut runs of 304 shares of 32 rows, 12 for 128 rows (the
-// partial rows, up to 40 MB, mostly come from L2).
-template <int HD>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a) {
-    constexpr int D = HD / 32;
-    const TreeParams &p = a.p;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int cta = static_cast<int>(blockIdx.x) + 1;
-    const TreeCut cut = a.cuts[cta];
+// One warp's sum over `count` partial rows, slot(0), slot(1), ...: the running maximum and sum, and
+// acc, whose lane holds channels lane, lane + 32, ...  The maxima and sums of up to 32 pieces are read
+// at once, one per lane, and the partial rows four at a time: a few memory round trips, not one per
+// piece.
+template <int HD, typename Slot>
+__device__ __forceinline__ void join_pieces(const TreeLaunch &a, Slot slot, int count, float &m, float &l,
+                                            float (&acc)[HD / 32]) {
+    constexpr int D = HD / 32, U = 4;
     const int lane = threadIdx.x & 31;
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (cut.pieces == 0 || row >= cut.rows) return;
-    // piece 0 is the last run of the share before, the others are the first runs of theirs
-    auto slot_of = [&](int i) -> int64_t {
-        return (2 * static_cast<int64_t>(cta + (i - 1) * cut.stride) + (i == 0 ? 1 : 0)) * a.slot_rows + row;
-    };
-    float m = -INFINITY, l = 0.f, acc[D];
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
     for (int d = 0; d < D; ++d) acc[d] = 0.f;
-    for (int base = 0; base < cut.pieces; base += 32) {
-        const int n = min(32, cut.pieces - base);
-        const float2 ml = lane < n ? a.part_ml[slot_of(base + lane)] : make_float2(-INFINITY, 0.f);
+    for (int base = 0; base < count; base += 32) {
+        const int n = min(32, count - base);
+        const float2 ml = lane < n ? a.part_ml[slot(base + lane)] : make_float2(-INFINITY, 0.f);
         float top = fmaxf(m, ml.x);
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
@@ -1038,16 +1039,16 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int d = 0; d < D; ++d) acc[d] *= f;
         m = top;
-        for (int i = 0; i < n; i += 4) {
-            float o[4][D];
+        for (int i = 0; i < n; i += U) {
+            float o[U][D];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float *src = a.part_o + slot_of(base + min(i + u, n - 1)) * HD;
+            for (int u = 0; u < U; ++u) {
+                const float *src = a.part_o + slot(base + min(i + u, n - 1)) * HD;
 #pragma unroll
                 for (int d = 0; d < D; ++d) o[u][d] = src[d * 32 + lane];
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const float wu = __shfl_sync(kAll, w, min(i + u, n - 1));
                 if (i + u < n && wu != 0.f) {
 #pragma unroll
@@ -1056,12 +1057,85 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
             }
         }
     }
+}
+
+// Partial row of piece i of a run whose second piece is CTA `cta`'s: piece 0 is the last run of the
+// share before, the others are the first runs of theirs.
+__device__ __forceinline__ int64_t piece_slot(const TreeLaunch &a, const TreeCut &cut, int cta, int row, int i) {
+    return (2 * static_cast<int64_t>(cta + (i - 1) * cut.stride) + (i == 0 ? 1 : 0)) * a.slot_rows + row;
+}
+
+template <int HD>
+__device__ __forceinline__ __nv_bfloat16 *joined_row(const TreeLaunch &a, const TreeCut &cut, int row) {
     const int64_t node = cut.node0 + row / a.group;
     const int h = cut.head * a.group + row % a.group;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (node * p.num_q_heads + h) * HD;
-    const float inv = l > 0.f ? p.v_scale / l : (l == 0.f ? 0.f : l);
+    return static_cast<__nv_bfloat16 *>(a.p.out) + (node * a.p.num_q_heads + h) * HD;
+}
+
+__device__ __forceinline__ float joined_scale(const TreeLaunch &a, float l) {
+    return l > 0.f ? a.p.v_scale / l : (l == 0.f ? 0.f : l);
+}
+
+// Joins the partial rows of every (sequence, kernel head group, row tile) that was cut: one
+// warp per row, the shares' partials in a fixed order, so the result does not depend on
+// timing.  Grid: x = CTA, y = eight rows; the CTA that had a cut run's second piece stands for
+// it.  Bound by its round trips to memory and its launch: 6 us for the cut runs of 304 shares of 32
+// rows, 12 for 128 rows (the partial rows, up to 40 MB, mostly come from L2).
+template <int HD>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeLaunch a) {
+    constexpr int D = HD / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cta = static_cast<int>(blockIdx.x) + 1;
+    const TreeCut cut = a.cuts[cta];
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (cut.pieces == 0 || row >= cut.rows) return;
+    float m, l, acc[D];
+    join_pieces<HD>(a, [&](int i) { return piece_slot(a, cut, cta, row, i); }, cut.pieces, m, l, acc);
+    __nv_bfloat16 *out = joined_row<HD>(a, cut, row);
+    const float inv = joined_scale(a, l);
 #pragma unroll
     for (int d = 0; d < D; ++d) out[d * 32 + lane] = __float2bfloat16_rn(acc[d] * inv);
+}
+
+// The same where few long runs are cut into many pieces each: eight warps share a row, every eighth
+// piece each, and add up in shared memory in the order of the warps.  Grid: x = eight CTAs, y = row.
+// (One sequence of 43545 tokens, 4 kv heads, 76 pieces a run: a warp per row took 18 us of the call.)
+template <int HD>
+__global__ void __launch_bounds__(256) tree_join_long_kernel(const __grid_constant__ TreeLaunch a) {
+    constexpr int D = HD / 32;
+    __shared__ float part[8][HD];
+    __shared__ float2 part_ml[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
+    const int cta0 = static_cast<int>(blockIdx.x) * 8 + 1;
+    const bool cuts_run = lane < 8 && cta0 + lane < a.ctas && a.cuts[cta0 + lane].pieces > 0;
+    for (unsigned which = __ballot_sync(kAll, cuts_run); which; which &= which - 1) {   // the same in every warp
+        const int cta = cta0 + __ffs(which) - 1;
+        const TreeCut cut = a.cuts[cta];
+        if (row >= cut.rows) continue;
+        float m, l, acc[D];
+        join_pieces<HD>(a, [&](int i) { return piece_slot(a, cut, cta, row, warp + 8 * i); },
+                        (cut.pieces - warp + 7) / 8, m, l, acc);
+        __syncthreads();   // the run before has been read
+#pragma unroll
+        for (int d = 0; d < D; ++d) part[warp][d * 32 + lane] = acc[d];
+        if (lane == 0) part_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        float top = -INFINITY, sum = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, part_ml[w].x);
+        for (int c = threadIdx.x; c < HD; c += 256) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float2 ml = part_ml[w];
+                const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2f(ml.x - top);
+                sum += f * ml.y;
+                if (f != 0.f) o = fmaf(part[w][c], f, o);
+            }
+            joined_row<HD>(a, cut, row)[c] = __float2bfloat16_rn(o * joined_scale(a, sum));
+        }
+    }
 }
 
 // ---- host side ------------------------------------------------------------------------------
@@ -1134,6 +1208,7 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = C::SMEM;
+    a.ctas = grid;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return e;
     // Runs of at most kCutTiles are never cut (TreeShares::whole), and one share cuts nothing.
@@ -1141,9 +1216,13 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     if (p.window > 0)
         longest = std::min(longest, (static_cast<int64_t>(p.window) + p.max_tree_len + kKeys - 1) / kKeys + 1);
     if (grid == 1 || longest <= kCutTiles) return cudaSuccess;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), static_cast<unsigned>((a.slot_rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
+    if (grid >= kManyPieces * p.num_seqs * a.heads * row_tiles) {
+        cfg.gridDim = dim3(static_cast<unsigned>((grid + 6) / 8), static_cast<unsigned>(a.slot_rows));
+        return cudaLaunchKernelEx(&cfg, tree_join_long_kernel<HD>, a);
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), static_cast<unsigned>((a.slot_rows + 7) / 8));
     return cudaLaunchKernelEx(&cfg, tree_join_kernel<HD>, a);
 }
 

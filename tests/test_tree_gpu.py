@@ -264,6 +264,16 @@ def test_row_tiles_side_by_side_and_one_after_another(fp8):
     assert pa.device_status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hd,nq,nkv,nodes", [(64, 3, 1, [3]), (128, 8, 2, [20]), (256, 2, 1, [5]), (128, 4, 1, [40])])
+def test_one_long_sequence_in_many_pieces(hd, nq, nkv, nodes, fp8):
+    c = gpu(make([9000 + nodes[0]], nodes, nq, nkv, hd, seed=60 + hd, fp8=fp8))
+    got = call(c)
+    check(c, got)
+    assert torch.equal(got, call(c))
+    assert pa.device_status() == 0
+
+
 def test_empty_trees_and_sequences():
     c = gpu(make([40, 30, 50], [3, 0, 2], 4, 2, 128, seed=16))
     check(c, call(c))
