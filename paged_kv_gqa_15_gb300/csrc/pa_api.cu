@@ -471,6 +471,11 @@ int pa_decode_pages(void *out, const void *q, const void *k_cache, const void *v
     rc = status_ptr(&p.status);
     if (rc) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pa::page_lists_on_tree(p, head_dim)) {
+        const cudaError_t e = pa::launch_page_lists(
+            p, head_dim, workspace, pa_decode_split_workspace_size(num_seqs, num_q_heads, head_dim, max_pages * 16), s);
+        return e == cudaSuccess ? PA_OK : cuda_fail(e, "page list decode launch");
+    }
     cudaError_t e = pa::launch_decode(p, head_dim, true, s);
     if (e != cudaSuccess) return cuda_fail(e, "decode partition launch");
     e = pa::launch_merge(p, head_dim, s);

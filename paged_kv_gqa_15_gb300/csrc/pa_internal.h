@@ -94,8 +94,8 @@ struct TreeParams {
     const void *k_cache, *v_cache;
     const int32_t *block_tables;  // [B][max_blocks]
     const int32_t *seq_lens;      // [B], drafted nodes included
-    const int32_t *qo_indptr;     // [B + 1]
-    const uint64_t *tree_mask;    // [total_rows][mask_words]
+    const int32_t *qo_indptr;     // [B + 1]; null for page lists
+    const uint64_t *tree_mask;    // [total_rows][mask_words]; null for page lists
     void *workspace;
     int64_t num_blocks;
     int64_t s_block, s_head, s_token;
@@ -139,6 +139,10 @@ cudaError_t launch_merge(const DecodeParams &p, int head_dim, cudaStream_t strea
 cudaError_t launch_prefill(PrefillParams &p, const PrefillLaunch &L, cudaStream_t stream);
 
 cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t stream);
+// Whether the tree kernel takes a decode over page lists, and that call.
+bool page_lists_on_tree(const DecodeParams &p, int head_dim);
+cudaError_t launch_page_lists(const DecodeParams &p, int head_dim, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
 
 // The argument checks of the entry points, shared by those in other translation units.
 int api_check_heads(int head_dim, int num_q_heads, int num_kv_heads);

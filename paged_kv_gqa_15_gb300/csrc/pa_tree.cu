@@ -37,15 +37,15 @@
 //    holds q to 2^-8 of its value.  P is split into three E5M2 terms: an f16 value's upper byte
 //    is an E5M2 value, so each term is a mask and a subtraction and four of them one byte
 //    permutation.  Three terms hold at least 9 bits (2^-8 of P, mostly better) over f16's range.
-//    P as E4M3 pairs has one product less and was 8 % faster where the products bound the call (154
-//    us against 167 for 32 sequences of 1k-8k, 64-node trees), but E4M3 reaches from 448 to 2^-9
+//    P as E4M3 pairs has one product less and was 8 % faster in an earlier build (154 us against 167
+//    for 32 sequences of 1k-8k, 64-node trees), but E4M3 reaches from 448 to 2^-9
 //    only: weights far under one large maximum lost their bits, and they can be most of the sum.
 //    Two more warps turning V into f16 left too little shared memory for tiles on their way: 261 us.
 //  * Every mbarrier wait is bounded.
-// Measured: 8 sequences of 32k-131k tokens, 24 nodes, 32 / 8 heads, bf16: 339 us for 2236 MB, 97 % of
-// the measured copy rate; 16 of 512-4096 tokens, 16 nodes: 35 us for 130 MB, start and join
-// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 171 us for 75 GFLOP, bound by the products
-// (five MMA terms) and the softmax of 256 rows.
+// Measured: 8 sequences of 32k-131k tokens, 24 nodes, 32 / 8 heads, bf16: 338 us for 2236 MB, 97 % of
+// the measured copy rate; 16 of 512-4096 tokens, 16 nodes: 36 us for 130 MB, start and join
+// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 155 us for 75 GFLOP, bound by the latency of
+// the softmax of 256 rows (tensor pipe 36 % busy, issue slots 37 %) between five MMA terms.
 #include <algorithm>
 #include <atomic>
 
@@ -129,8 +129,21 @@ struct TreeLaunch {
     int group, kv_rep, heads;       // query heads per kernel group, groups per kv head, groups
     int nodes;                      // nodes of a row tile (its rows: nodes * group)
     int slot_rows;                  // rows of a partial slot
+    int max_ctas;                   // bound of the grid
+    bool lists;                     // one query per sequence over page lists (launch_page_lists)
+    bool whole;                     // no run is to be cut (there is no room for partial rows)
     int ctas;                       // of the grid
 };
+
+// Slot of the partial rows of a run that starts or ends in CTA cta's share (`starts`: it starts
+// there).  Trees: two slots a CTA, for its first and its last run.  Page lists, whose workspace is
+// that of the split decode: the pieces are numbered along the line, where each next one lies in the
+// next share, the next run or both, so share + run is theirs alone (a run is its sequence's row
+// and head; there is one row tile).
+template <bool LISTS>
+__device__ __forceinline__ int piece_slot(const TreeLaunch &a, int cta, bool starts, int row0, int head) {
+    return LISTS ? cta + row0 * a.heads + head : 2 * cta + (starts ? 1 : 0);
+}
 
 // Sequence b's drafted rows and lengths; T = 0 (and the device status set when `flag`) if
 // they make no sense.
@@ -138,16 +151,19 @@ struct TreeSeq {
     int row0, T, L;
 };
 
+template <bool LISTS>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b, bool flag) {
     TreeSeq s;
-    s.row0 = p.qo_indptr[b];
-    const int row1 = p.qo_indptr[b + 1];
+    s.row0 = LISTS ? b : p.qo_indptr[b];
+    const int row1 = LISTS ? b + 1 : p.qo_indptr[b + 1];
     s.L = max(p.seq_lens[b], 0);
     const int cap = p.max_blocks * kBlockSize;
     bool bad = s.L > cap;
     s.L = min(s.L, cap);
     s.T = 0;
-    if (s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && row1 - s.row0 <= p.max_tree_len &&
+    if (LISTS)
+        s.T = 1;
+    else if (s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && row1 - s.row0 <= p.max_tree_len &&
         row1 - s.row0 <= s.L)
         s.T = row1 - s.row0;
     else
@@ -161,9 +177,9 @@ __device__ __forceinline__ int tree_first_key(const TreeSeq &s, int window) {
     return window > 0 ? max(0, s.L - s.T - window) : 0;
 }
 
-// Key tiles of one (sequence, kv head, row tile), and its row tiles.
+// Key tiles of one (sequence, kv head, row tile); one that masks everything for an empty page list.
 __device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
-    return s.T > 0 ? (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys : 0;
+    return s.T > 0 ? max(1, (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys) : 0;
 }
 
 // Row tiles that go together are worked on by as many CTAs at once (see TreeShares); with fewer
@@ -176,13 +192,13 @@ constexpr int kMostTogether = 8;
 // pref[b] = tiles of the line before sequence b, run[b] the tiles of its runs, run[n] those of
 // the longest, run[n + 1] the row tiles that go together; all threads of the CTA call it, with
 // pref[0], run[n] and run[n + 1] cleared.
-template <bool FP8>
+template <bool FP8, bool LISTS>
 __device__ __forceinline__ void tree_prefix(const TreeLaunch &a, int64_t *pref, int *run, bool flag) {
     const TreeParams &p = a.p;
     const int n = p.num_seqs;
     int most_tiles = 0, most_rows = 0;
     for (int b = threadIdx.x; b < n; b += kTreeThreads) {
-        const TreeSeq s = tree_seq(p, b, flag);
+        const TreeSeq s = tree_seq<LISTS>(p, b, flag);
         const int tiles = tree_tiles(s, p.window), row_tiles = (s.T + a.nodes - 1) / a.nodes;
         run[b] = tiles;
         pref[b + 1] = static_cast<int64_t>(tiles) * row_tiles * a.heads;
@@ -300,6 +316,12 @@ __device__ __forceinline__ uint64_t mask_word(const uint64_t *mask, int w, int T
     return w * 64 < T ? mask[w] & ones(T - w * 64) : 0ull;
 }
 
+// The block-table row of sequence b for pool kv head kvh.
+template <bool LISTS>
+__device__ __forceinline__ const int32_t *tree_table_row(const TreeParams &p, int b, int kvh) {
+    return p.block_tables + (LISTS ? static_cast<int64_t>(b) * p.num_kv_heads + kvh : b) * p.max_blocks;
+}
+
 __device__ __forceinline__ int mask_count(const uint64_t *mask, int T) {
     int n = 0;
     for (int w = 0; w * 64 < T; ++w) n += __popcll(mask_word(mask, w, T));
@@ -359,7 +381,9 @@ __device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float
     }
 }
 
-template <int HD, bool FP8>
+// LISTS: one query per sequence over page lists (launch_page_lists), as a tree of one node, the
+// list's last key, which sees itself.
+template <int HD, bool FP8, bool LISTS>
 __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     tree_kernel(const __grid_constant__ TreeLaunch a) {
     using C = TreeCfg<HD, FP8>;
@@ -427,15 +451,17 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
     }
     if (warp >= 2) {   // the first reads after the wait, into L2 beforehand
         const unsigned t = blockIdx.x * 128 + threadIdx.x - 64, nt = gridDim.x * 128;
-        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, 1, p.max_blocks,
+        prefetch_decode_inputs(p.seq_lens, p.block_tables, p.q, p.num_seqs, LISTS ? p.num_kv_heads : 1, p.max_blocks,
                                static_cast<size_t>(p.total_rows) * p.num_q_heads * HD * 2, threadIdx.x - 64, 128);
-        prefetch_l2_lines(p.qo_indptr, (static_cast<size_t>(p.num_seqs) + 1) * 4, t, nt);
-        prefetch_l2_lines(p.tree_mask, static_cast<size_t>(p.total_rows) * p.mask_words * 8, t, nt);
+        if constexpr (!LISTS) {
+            prefetch_l2_lines(p.qo_indptr, (static_cast<size_t>(p.num_seqs) + 1) * 4, t, nt);
+            prefetch_l2_lines(p.tree_mask, static_cast<size_t>(p.total_rows) * p.mask_words * 8, t, nt);
+        }
     }
     // launched as a programmatic dependent: nothing before this point depends on global memory
     __syncthreads();   // what tree_prefix adds to is cleared
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    tree_prefix<FP8>(a, pref, run, blockIdx.x == 0);
+    tree_prefix<FP8, LISTS>(a, pref, run, blockIdx.x == 0);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -451,7 +477,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         // an even share and a run.
         const int64_t longest = run[p.num_seqs];
         const int64_t most = line.even < longest ? longest : line.even + longest;
-        line.whole = most <= line.even + kCutTiles;
+        line.whole = (LISTS && a.whole) || most <= line.even + kCutTiles;
     }
     const int64_t u_begin = line.begin(share);
     const int64_t u_end = line.begin(share + 1);
@@ -470,7 +496,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             s.n = -1;
             while (u < u_end) {
                 const int lo = line.sequence(u);
-                const TreeSeq q = tree_seq(p, lo, false);
+                const TreeSeq q = tree_seq<LISTS>(p, lo, false);
                 const int tiles = run[lo];
                 const int row_tiles = together > 1 ? 1 : (q.T + a.nodes - 1) / a.nodes;
                 const int64_t rel = u - pref[lo];
@@ -491,7 +517,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 s.L = q.L;
                 s.n = n;
                 s.j0 = tree_first_key(q, p.window) / kKeys + j;
-                s.slot = s.n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                s.slot = s.n == tiles ? -1 : piece_slot<LISTS>(a, static_cast<int>(blockIdx.x), j == 0, s.row0, s.head);
                 if (j > 0) {   // only in the share's first segment
                     run_begin = u - j;
                     run_end = run_begin + tiles;
@@ -524,7 +550,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
         auto page_raw = [&](const TreeSegment &s, int j) -> int {
             const int i = j * kPages + lane;
             if (lane >= kPages || i * kBlockSize >= s.L || i < s.page_lo) return -2;
-            return p.block_tables[static_cast<int64_t>(s.b) * p.max_blocks + i];
+            return tree_table_row<LISTS>(p, s.b, s.head / a.kv_rep)[i];
         };
         const uint64_t policy = l2_policy_evict_first();
         TreeSegment w = next_segment();
@@ -540,7 +566,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 cut = run_cut;
                 cut.pieces = line.share_of(run_end - 1) - share + 2;
             }
-            if (lane == 0) a.cuts[blockIdx.x] = cut;
+            if (lane == 0 && !(LISTS && a.whole)) a.cuts[blockIdx.x] = cut;
         };
         while (!stop && w.n >= 0) {
             const int kvh = w.head / a.kv_rep;
@@ -732,9 +758,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             const int node = w.node0 + (mine ? row / a.group : 0);
             const int head = w.head * a.group + (mine ? row % a.group : 0);
             const int ctx = w.L - w.T;
-            const uint64_t *mask = p.tree_mask + static_cast<int64_t>(w.row0 + node) * p.mask_words;
+            const uint64_t *mask = LISTS ? nullptr : p.tree_mask + static_cast<int64_t>(w.row0 + node) * p.mask_words;
             // read now: the tile that needs it would wait for it
-            const uint64_t word0 = mine ? mask_word(mask, 0, w.T) : 0ull;
+            const uint64_t word0 = !mine ? 0ull : LISTS ? 1ull : mask_word(mask, 0, w.T);
             int low = 0;                           // first context token this row sees
             if (p.window > 0) low = max(0, min(ctx, ctx + mask_count(mask, w.T) - p.window));
             const int seen_by_all = p.window > 0 ? max(0, min(ctx, ctx + w.T - p.window)) : 0;
@@ -979,9 +1005,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                     for (int at = 0; at < 512; ++at) {
                         if (!(*static_cast<volatile uint32_t *>(&queue->bad_nodes[at >> 5]) >> (at & 31) & 1)) continue;
                         const int key = at < 256 ? ctx + at : first_key + at - 256;
-                        const bool see = at < 256 ? (mask_word(mask, at >> 6, w.T) >> (at & 63) & 1) : key >= low;
+                        const bool see = at >= 256 ? key >= low
+                                         : LISTS   ? at == 0
+                                                   : (mask_word(mask, at >> 6, w.T) >> (at & 63) & 1);
                         if (!see) continue;
-                        const int page = p.block_tables[static_cast<int64_t>(w.b) * p.max_blocks + key / kBlockSize];
+                        const int page = tree_table_row<LISTS>(p, w.b, w.head / a.kv_rep)[key / kBlockSize];
                         const int64_t off = page * p.s_block + (w.head / a.kv_rep) * p.s_head +
                                             (key % kBlockSize) * p.s_token;
                         for (int d = 0; d < HD; ++d) {
@@ -1061,8 +1089,11 @@ __device__ __forceinline__ void join_pieces(const TreeLaunch &a, Slot slot, int 
 
 // Partial row of piece i of a run whose second piece is CTA `cta`'s: piece 0 is the last run of the
 // share before, the others are the first runs of theirs.
-__device__ __forceinline__ int64_t piece_slot(const TreeLaunch &a, const TreeCut &cut, int cta, int row, int i) {
-    return (2 * static_cast<int64_t>(cta + (i - 1) * cut.stride) + (i == 0 ? 1 : 0)) * a.slot_rows + row;
+__device__ __forceinline__ int64_t piece_row(const TreeLaunch &a, const TreeCut &cut, int cta, int row, int i) {
+    const int c = cta + (i - 1) * cut.stride;
+    const int slot = a.lists ? piece_slot<true>(a, c, i == 0, cut.node0, cut.head)
+                             : piece_slot<false>(a, c, i == 0, cut.node0, cut.head);
+    return static_cast<int64_t>(slot) * a.slot_rows + row;
 }
 
 template <int HD>
@@ -1091,7 +1122,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (cut.pieces == 0 || row >= cut.rows) return;
     float m, l, acc[D];
-    join_pieces<HD>(a, [&](int i) { return piece_slot(a, cut, cta, row, i); }, cut.pieces, m, l, acc);
+    join_pieces<HD>(a, [&](int i) { return piece_row(a, cut, cta, row, i); }, cut.pieces, m, l, acc);
     __nv_bfloat16 *out = joined_row<HD>(a, cut, row);
     const float inv = joined_scale(a, l);
 #pragma unroll
@@ -1115,7 +1146,7 @@ __global__ void __launch_bounds__(256) tree_join_long_kernel(const __grid_consta
         const TreeCut cut = a.cuts[cta];
         if (row >= cut.rows) continue;
         float m, l, acc[D];
-        join_pieces<HD>(a, [&](int i) { return piece_slot(a, cut, cta, row, warp + 8 * i); },
+        join_pieces<HD>(a, [&](int i) { return piece_row(a, cut, cta, row, warp + 8 * i); },
                         (cut.pieces - warp + 7) / 8, m, l, acc);
         __syncthreads();   // the run before has been read
 #pragma unroll
@@ -1154,7 +1185,7 @@ int tree_nodes(int group, int max_tree_len) {
     return n < max_tree_len ? n : max_tree_len;
 }
 
-template <int HD, bool FP8>
+template <int HD, bool FP8, bool LISTS>
 cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     using C = TreeCfg<HD, FP8>;
     const TreeParams &p = a.p;
@@ -1176,7 +1207,7 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
         if (!encode(&a.tm_k, p.k_cache, 4, dims, str, box) || !encode(&a.tm_v, p.v_cache, 4, dims, str, box))
             return cudaErrorInvalidValue;
     }
-    auto kern = tree_kernel<HD, FP8>;
+    auto kern = tree_kernel<HD, FP8, LISTS>;
     static std::atomic<int> configured{-1};   // last device whose attributes are set
     static std::atomic<int> sm_count{0};
     int dev = 0;
@@ -1196,7 +1227,7 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     const int row_tiles = (p.max_tree_len + a.nodes - 1) / a.nodes;
     const int64_t line = static_cast<int64_t>(p.num_seqs) * a.heads * row_tiles *
                          ((static_cast<int64_t>(p.max_blocks) * kBlockSize + kKeys - 1) / kKeys);
-    int grid = sms * C::CTAS_PER_SM < kMaxCtas ? sms * C::CTAS_PER_SM : kMaxCtas;
+    int grid = std::min(sms * C::CTAS_PER_SM, a.max_ctas);
     if (line < grid) grid = static_cast<int>(line);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -1215,10 +1246,10 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
     int64_t longest = (static_cast<int64_t>(p.max_blocks) * kBlockSize + kKeys - 1) / kKeys;
     if (p.window > 0)
         longest = std::min(longest, (static_cast<int64_t>(p.window) + p.max_tree_len + kKeys - 1) / kKeys + 1);
-    if (grid == 1 || longest <= kCutTiles) return cudaSuccess;
+    if (grid == 1 || longest <= kCutTiles || a.whole) return cudaSuccess;
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    if (grid >= kManyPieces * p.num_seqs * a.heads * row_tiles) {
+    if (grid >= static_cast<int64_t>(kManyPieces) * p.num_seqs * a.heads * row_tiles) {
         cfg.gridDim = dim3(static_cast<unsigned>((grid + 6) / 8), static_cast<unsigned>(a.slot_rows));
         return cudaLaunchKernelEx(&cfg, tree_join_long_kernel<HD>, a);
     }
@@ -1228,31 +1259,100 @@ cudaError_t launch_tree(TreeLaunch &a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t stream) {
+namespace {
+
+TreeLaunch tree_launch(const TreeParams &p, size_t slots, int head_dim) {
     TreeLaunch a = {};
+    a.p = p;
     a.group = tree_group(p.num_q_heads, p.num_kv_heads);
     a.kv_rep = p.num_q_heads / p.num_kv_heads / a.group;
     a.heads = p.num_q_heads / a.group;
     a.nodes = tree_nodes(a.group, p.max_tree_len);
     a.slot_rows = a.nodes * a.group;
-    const size_t slots = 2 * kMaxCtas;
+    a.max_ctas = kMaxCtas;
     a.part_o = static_cast<float *>(p.workspace);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots * a.slot_rows * head_dim);
     a.cuts = reinterpret_cast<TreeCut *>(a.part_ml + slots * a.slot_rows);
+    return a;
+}
+
+}  // namespace
+
+cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t stream) {
+    TreeLaunch a = tree_launch(p, 2 * kMaxCtas, head_dim);
     // the line's prefix holds kMaxSeqs sequences: more go in several launches, one after another
     for (int at = 0; at < p.num_seqs; at += kMaxSeqs) {
-        a.p = p;
-        a.p.num_seqs = p.num_seqs - at < kMaxSeqs ? p.num_seqs - at : kMaxSeqs;
+        a.p.num_seqs = std::min(p.num_seqs - at, kMaxSeqs);
         a.p.seq_lens = p.seq_lens + at;
         a.p.qo_indptr = p.qo_indptr + at;
         a.p.block_tables = p.block_tables + static_cast<int64_t>(at) * p.max_blocks;
         cudaError_t e;
         switch (head_dim) {
-            case 64: e = p.kv_fp8 ? launch_tree<64, true>(a, stream) : launch_tree<64, false>(a, stream); break;
-            case 128: e = p.kv_fp8 ? launch_tree<128, true>(a, stream) : launch_tree<128, false>(a, stream); break;
-            case 256: e = p.kv_fp8 ? launch_tree<256, true>(a, stream) : launch_tree<256, false>(a, stream); break;
+            case 64: e = p.kv_fp8 ? launch_tree<64, true, false>(a, stream) : launch_tree<64, false, false>(a, stream); break;
+            case 128: e = p.kv_fp8 ? launch_tree<128, true, false>(a, stream) : launch_tree<128, false, false>(a, stream); break;
+            case 256: e = p.kv_fp8 ? launch_tree<256, true, false>(a, stream) : launch_tree<256, false, false>(a, stream); break;
             default: return cudaErrorNotSupported;
         }
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// A page list is a tree of one node, the list's last key, whose other keys are its context.
+// The tree kernel takes the calls that the split decode has no tensor-core kernel for and enough
+// query heads to pay (8 sequences, 8 kv heads, 128 pages; split decode against this one, us: head_dim
+// 256 with 2 / 4 / 8 / 16 query heads a kv head 30 / 42 / 111 / 212 against 36, FP8 28 / 40 / 153 / 293
+// against 42; head_dim 64 with 8 / 12 / 16: 17 / 24 / 26 against 19, FP8 with 4 / 8 / 16: 15 / 29 / 52
+// against 21).
+bool page_lists_on_tree(const DecodeParams &p, int head_dim) {
+    const int group = p.num_q_heads / p.num_kv_heads;
+    const bool sizes = head_dim == 256 ? group >= 4 : head_dim == 64 && group > (p.kv_fp8 ? 4 : 8);
+    return sizes && p.scale_log2 > 0.f && p.scale_log2 < INFINITY && p.num_blocks < INT32_MAX;
+}
+
+cudaError_t launch_page_lists(const DecodeParams &d, int head_dim, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+    TreeParams p = {};
+    p.out = d.out;
+    p.q = d.q;
+    p.k_cache = d.k_cache;
+    p.v_cache = d.v_cache;
+    p.block_tables = d.block_tables;
+    p.seq_lens = d.seq_lens;
+    p.workspace = workspace;
+    p.num_blocks = d.num_blocks;
+    p.s_block = d.s_block;
+    p.s_head = d.s_head;
+    p.s_token = d.s_token;
+    p.max_tree_len = 1;
+    p.num_q_heads = d.num_q_heads;
+    p.num_kv_heads = d.num_kv_heads;
+    p.max_blocks = d.max_blocks;
+    p.kv_fp8 = d.kv_fp8;
+    p.scale_log2 = d.scale_log2;
+    p.k_scale = d.k_scale;
+    p.v_scale = d.v_scale;
+    p.status = d.status;
+    const int group = tree_group(p.num_q_heads, p.num_kv_heads);
+    const size_t slot_bytes = static_cast<size_t>(group) * (static_cast<size_t>(head_dim) * 4 + 8);
+    const size_t cut_bytes = kMaxCtas * sizeof(TreeCut);
+    const size_t slots = workspace_bytes > cut_bytes ? (workspace_bytes - cut_bytes) / slot_bytes : 0;
+    for (int at = 0; at < d.num_seqs; at += kMaxSeqs) {
+        p.num_seqs = p.total_rows = std::min(d.num_seqs - at, kMaxSeqs);
+        p.seq_lens = d.seq_lens + at;
+        p.block_tables = d.block_tables + static_cast<int64_t>(at) * d.num_kv_heads * d.max_blocks;
+        p.q = static_cast<const __nv_bfloat16 *>(d.q) + static_cast<int64_t>(at) * d.num_q_heads * head_dim;
+        p.out = static_cast<__nv_bfloat16 *>(d.out) + static_cast<int64_t>(at) * d.num_q_heads * head_dim;
+        TreeLaunch a = tree_launch(p, slots, head_dim);
+        a.lists = true;
+        // pieces number fewer than shares + runs
+        const int64_t runs = static_cast<int64_t>(p.num_seqs) * a.heads;
+        const int64_t shares = static_cast<int64_t>(slots) - runs;
+        a.whole = shares <= runs;
+        if (!a.whole) a.max_ctas = static_cast<int>(std::min<int64_t>(shares, kMaxCtas));
+        const cudaError_t e =
+            head_dim == 64 ? (p.kv_fp8 ? launch_tree<64, true, true>(a, stream) : launch_tree<64, false, true>(a, stream))
+                           : (p.kv_fp8 ? launch_tree<256, true, true>(a, stream) : launch_tree<256, false, true>(a, stream));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -284,6 +284,50 @@ def test_decode_over_selected_pages(nq, nkv, hd, fp8):
     assert pa.device_status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,nkv,hd", [(8, 2, 256), (16, 1, 256), (10, 2, 256), (24, 2, 64), (17, 1, 64), (16, 2, 64)])
+@pytest.mark.parametrize("lens,most", [([1500, 40, 0, 977], 37), ([9000, 20, 0, 5007], 301), ([7000], 400), ([33] * 3, 2)])
+def test_decode_over_lists_of_wide_groups(lens, most, nq, nkv, hd, fp8):
+    c = make(lens, nq, nkv, hd, nq + hd + most, fp8, "NHD" if nq % 4 else "HND")
+    fill_bounds(c)
+    pages, kept = select(c, most, 1, 1)
+    got = decode(c, pages, kept)
+    out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages.cpu(), kept.cpu(), c["scale"], c["layout"],
+                                    c["kv_scale"], c["kv_scale"])
+    ref64.assert_attention(got, out, bound, FP8_EXTRA if fp8 else 0.0)
+    assert bool((got[c["lens"] == 0] == 0).all())
+    # no byte behind the workspace it asks for is written
+    need = pa.decode_split_workspace_size(len(lens), nq, hd, most * PAGE)
+    room = torch.full((need + 4096,), 171, dtype=torch.uint8, device=DEV)
+    assert torch.equal(decode(c, pages, kept, room[:need]), got)
+    assert bool((room[need:] == 171).all())
+    assert pa.device_status() == 0
+
+
+def test_decode_over_lists_of_more_sequences_than_a_launch():
+    rng = np.random.default_rng(6)
+    c = make([int(n) for n in rng.integers(0, 200, 1000)], 4, 1, 256, 62)
+    fill_bounds(c)
+    pages, kept = select(c, 9, 1, 1)
+    out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages.cpu(), kept.cpu(), c["scale"], c["layout"],
+                                    c["kv_scale"], c["kv_scale"])
+    ref64.assert_attention(decode(c, pages, kept), out, bound)
+    assert pa.device_status() == 0
+
+
+def test_wide_groups_flag_bad_page_lists():
+    c = make([500, 300], 8, 2, 256, 63)
+    fill_bounds(c)
+    pages, lens = select(c, 16, 1, 1)
+    pages[0, 1, 3], pages[1, 0, 2] = c["k"].shape[0], -5
+    assert torch.isfinite(decode(c, pages, lens)).all()
+    assert pa.device_status() == 1 << pa.PA_ERR_DEVICE_BOUNDS
+    pages, lens = select(c, 16, 1, 1)
+    lens[1] = 10 ** 6
+    decode(c, pages, lens)
+    assert pa.device_status() == 1 << pa.PA_ERR_DEVICE_BOUNDS
+
+
 def test_all_pages_selected_is_the_split_decode():
     c = make([1500, 40, 977], 8, 2, 128, 60)
     fill_bounds(c)
