@@ -103,7 +103,7 @@ struct TreeCfg {
     static constexpr uint32_t OFF_PREF = OFF_V + STAGES * KV_BYTES;    // int64 [kMaxSeqs + 1]
     static constexpr uint32_t OFF_RUN = OFF_PREF + (kMaxSeqs + 1) * 8; // int [kMaxSeqs + 1]
     static constexpr uint32_t OFF_BAR = OFF_RUN + (kMaxSeqs + 2) * 4;
-    static constexpr uint32_t SMEM_USED = OFF_BAR + 1024;
+    static constexpr uint32_t SMEM_USED = OFF_BAR + 1280;
     static constexpr int CTAS_PER_SM = HD == 256 ? 1 : 2;
     static constexpr uint32_t SMEM = SMEM_USED + 1024;           // + realignment of the base
     static constexpr uint32_t TM_O = 2 * kKeys;                  // TMEM: S / P twice, then O
@@ -306,8 +306,18 @@ struct TreeQueue {
     TreeSegment seg[4];
     uint32_t bad_nodes[16];        // partly seen rows with non-finite values (see the cleaning of V)
     uint32_t bad_pages[16];        // ring by tile: pages whose ids are out of range
+    float row_factor[kRows];       // FP8: the power of two that q's rows are scaled by
 };
-static_assert(48 * 8 + sizeof(TreeQueue) <= 1024, "queue fits behind the barriers");
+
+__device__ __forceinline__ TreeSegment read_again(const TreeSegment &s) {
+    const volatile TreeSegment &v = s;
+    TreeSegment r;
+    r.b = v.b, r.head = v.head, r.node0 = v.node0, r.n_nodes = v.n_nodes;
+    r.row0 = v.row0, r.T = v.T, r.L = v.L;
+    r.j0 = v.j0, r.n = v.n, r.page_lo = v.page_lo, r.slot = v.slot;
+    return r;
+}
+static_assert(48 * 8 + sizeof(TreeQueue) <= 1280, "queue fits behind the barriers");
 
 __device__ __forceinline__ uint64_t ones(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
 
@@ -379,6 +389,50 @@ __device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(ta));
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(tb));
     }
+}
+
+// The largest magnitude of eight bf16 values.
+__device__ __forceinline__ float largest(const uint4 &raw) {
+    float f[8], most = 0.f;
+    unpack_bf16x8(raw, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+    return most;
+}
+
+// The power of two s with most * s in [128, 256); an infinite row becomes NaN, as its scores are.
+__device__ __forceinline__ float row_factor(float most) {
+    const int ex = static_cast<int>(__float_as_uint(most) >> 23 & 0xff);
+    if (ex == 255) return NAN;
+    return ex > 0 ? __uint_as_float(static_cast<uint32_t>(min(max(127 + 7 + 127 - ex, 1), 254)) << 23) : 1.f;
+}
+
+// 16 channels of q (unit c of its row) times s as E4M3 pairs, into Q's hi and lo rows.
+template <typename C>
+__device__ __forceinline__ void store_pair(uint8_t *q, int row, int c, const uint4 &a, const uint4 &b, float s) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        float f[8];
+        unpack_bf16x8(v ? b : a, f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t h[2], l[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const float x = f[4 * e + 2 * d] * s, y = f[4 * e + 2 * d + 1] * s;
+                h[d] = float2_to_e4m3x2(x, y);
+                const float2 back = e4m3x2_to_float2(h[d]);
+                l[d] = float2_to_e4m3x2(x - back.x, y - back.y);
+            }
+            hi[2 * v + e] = h[0] | h[1] << 16;
+            lo[2 * v + e] = l[0] | l[1] << 16;
+        }
+    }
+    constexpr int UNITS = C::ROWB / 16;
+    uint8_t *dst = q + (c / UNITS) * C::Q_CHUNK + swizzled<C::ROWB>(row, c % UNITS);
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(dst + C::CH * C::Q_CHUNK) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 // LISTS: one query per sequence over page lists (launch_page_lists), as a tree of one node, the
@@ -749,16 +803,12 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             // the four warps leave the loop at the same barrier, after a wait that ran out too
             if (named_barrier_or(1, 128, !ok)) break;
             const TreeSegment w = queue->seg[slot];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[slot]);
             if (w.n < 0) break;
             const int rows = w.n_nodes * a.group;
             const bool busy = quad * 32 < rows;    // this warp has rows
             const bool mine = row < rows;
-            const int node = w.node0 + (mine ? row / a.group : 0);
-            const int head = w.head * a.group + (mine ? row % a.group : 0);
             const int ctx = w.L - w.T;
-            const uint64_t *mask = LISTS ? nullptr : p.tree_mask + static_cast<int64_t>(w.row0 + node) * p.mask_words;
+            const uint64_t *mask = LISTS ? nullptr : p.tree_mask + static_cast<int64_t>(w.row0 + w.node0 + (mine ? row / a.group : 0)) * p.mask_words;
             // read now: the tile that needs it would wait for it
             const uint64_t word0 = !mine ? 0ull : LISTS ? 1ull : mask_word(mask, 0, w.T);
             int low = 0;                           // first context token this row sees
@@ -770,60 +820,31 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 // q's rows as E4M3 pairs, once the segment before has finished with Q
                 if (k > 0) ok = mbar_wait(q_empty, (k - 1) & 1, p.status, abort_flag);
                 ok = !__any_sync(kAll, !ok);
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(p.q) +
-                    (static_cast<int64_t>(w.row0 + node) * p.num_q_heads + head) * HD);
-                // up to 128 channels stay in registers between the two passes over them
-                constexpr int HELD = HD < 256 ? HD / 8 : 8;
-                uint4 held[HELD];
-                float most = 0.f;
+                // four threads a row, a quarter of its channels each, 32 rows at a time
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += 32) {
+                    const int r = r0 + (tid >> 2), part = tid & 3;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(p.q) +
+                        (static_cast<int64_t>(w.row0 + w.node0 + r / a.group) * p.num_q_heads + w.head * a.group +
+                         r % a.group) * HD) + part * (HD / 32);
+                    uint4 held[HD / 32];
 #pragma unroll
-                for (int c0 = 0; c0 < HD / 8; c0 += HELD) {
+                    for (int c = 0; c < HD / 32; ++c) held[c] = r < rows ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    float most = 0.f;
 #pragma unroll
-                    for (int c = 0; c < HELD; ++c) held[c] = mine ? src[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+                    for (int c = 0; c < HD / 32; ++c) most = fmaxf(most, largest(held[c]));
+                    most = fmaxf(most, __shfl_xor_sync(kAll, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
+                    const float s = row_factor(most);
 #pragma unroll
-                    for (int c = 0; c < HELD; ++c) {
-                        float f[8];
-                        unpack_bf16x8(held[c], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
-                    }
+                    for (int c = 0; c < HD / 64; ++c)
+                        store_pair<C>(smem, r, part * (HD / 64) + c, held[2 * c], held[2 * c + 1], s);
+                    if (part == 0) queue->row_factor[r] = s;
                 }
-                // s: the power of two with most * s in [128, 256); an infinite row becomes NaN, as
-                // its scores are
-                const int ex = static_cast<int>(__float_as_uint(most) >> 23 & 0xff);
-                const float s = ex == 255 ? NAN : ex > 0 ? __uint_as_float(static_cast<uint32_t>(min(max(127 + 7 + 127 - ex, 1), 254)) << 23) : 1.f;
-                scale = fmaxf(p.scale_log2 * p.k_scale / s, 0x1p-126f);   // above zero: -inf times it stays so
-                if (busy) {
-#pragma unroll
-                    for (int c = 0; c < HD / 16; ++c) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            float f[8];
-                            uint4 raw = held[(2 * c + v) % HELD];
-                            if constexpr (HELD < HD / 8) raw = mine ? src[2 * c + v] : make_uint4(0u, 0u, 0u, 0u);
-                            unpack_bf16x8(raw, f);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint32_t h[2], l[2];
-#pragma unroll
-                                for (int d = 0; d < 2; ++d) {
-                                    const float x = f[4 * e + 2 * d] * s, y = f[4 * e + 2 * d + 1] * s;
-                                    h[d] = float2_to_e4m3x2(x, y);
-                                    const float2 b = e4m3x2_to_float2(h[d]);
-                                    l[d] = float2_to_e4m3x2(x - b.x, y - b.y);
-                                }
-                                hi[2 * v + e] = h[0] | h[1] << 16;
-                                lo[2 * v + e] = l[0] | l[1] << 16;
-                            }
-                        }
-                        constexpr int UNITS = C::ROWB / 16;
-                        uint8_t *dst = smem + (c / UNITS) * C::Q_CHUNK + swizzled<C::ROWB>(row, c % UNITS);
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(dst + C::CH * C::Q_CHUNK) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
+                named_barrier(1, 128);
+                // above zero: -inf times it stays so
+                if (mine) scale = fmaxf(p.scale_log2 * p.k_scale / queue->row_factor[row], 0x1p-126f);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
@@ -963,11 +984,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
             ok = ok && mbar_wait(&v_empty[(g - 1) % C::STAGES], ((g - 1) / C::STAGES) & 1, p.status, abort_flag);
             if (named_barrier_or(1, 128, !ok)) break;
             tc_fence_after_sync();
-            const bool whole = w.slot < 0;
+            // read again: what only the epilogue needs is not held in registers through the tiles
+            const TreeSegment e = read_again(queue->seg[slot]);
+            const int node = e.node0 + (mine ? row / a.group : 0);
+            const int head = e.head * a.group + (mine ? row % a.group : 0);
+            const bool whole = e.slot < 0;
             const float inv = l > 0.f ? p.v_scale / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
-                                 (static_cast<int64_t>(w.row0 + node) * p.num_q_heads + head) * HD;
-            float *part = a.part_o + (static_cast<int64_t>(max(w.slot, 0)) * a.slot_rows + row) * HD;
+                                 (static_cast<int64_t>(e.row0 + node) * p.num_q_heads + head) * HD;
+            float *part = a.part_o + (static_cast<int64_t>(max(e.slot, 0)) * a.slot_rows + row) * HD;
             if (busy) {
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
@@ -990,7 +1015,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                     }
                     __syncwarp();
                 }
-                if (mine && !whole) a.part_ml[static_cast<int64_t>(w.slot) * a.slot_rows + row] = make_float2(m, l);
+                if (mine && !whole) a.part_ml[static_cast<int64_t>(e.slot) * a.slot_rows + row] = make_float2(m, l);
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -1007,10 +1032,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                         const int key = at < 256 ? ctx + at : first_key + at - 256;
                         const bool see = at >= 256 ? key >= low
                                          : LISTS   ? at == 0
-                                                   : (mask_word(mask, at >> 6, w.T) >> (at & 63) & 1);
+                                                   : (mask_word(mask, at >> 6, e.T) >> (at & 63) & 1);
                         if (!see) continue;
-                        const int page = tree_table_row<LISTS>(p, w.b, w.head / a.kv_rep)[key / kBlockSize];
-                        const int64_t off = page * p.s_block + (w.head / a.kv_rep) * p.s_head +
+                        const int page = tree_table_row<LISTS>(p, e.b, e.head / a.kv_rep)[key / kBlockSize];
+                        const int64_t off = page * p.s_block + (e.head / a.kv_rep) * p.s_head +
                                             (key % kBlockSize) * p.s_token;
                         for (int d = 0; d < HD; ++d) {
                             const float v = FP8 ? e4m3x2_to_float2(static_cast<const uint8_t *>(p.v_cache)[off + d]).x
@@ -1029,6 +1054,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 if (tid < 16) queue->bad_nodes[tid] = 0;
                 named_barrier(1, 128);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[slot]);
         }
     }
     tc_fence_before_sync();
