@@ -44,7 +44,7 @@
 //  * Every mbarrier wait is bounded.
 // Measured: 8 sequences of 32k-131k tokens, 24 nodes, 32 / 8 heads, bf16: 338 us for 2236 MB, 97 % of
 // the measured copy rate; 16 of 512-4096 tokens, 16 nodes: 36 us for 130 MB, start and join
-// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 155 us for 75 GFLOP, bound by the latency of
+// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 157 us for 75 GFLOP, bound by the latency of
 // the softmax of 256 rows (tensor pipe 36 % busy, issue slots 37 %) between five MMA terms.
 #include <algorithm>
 #include <atomic>
@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 const int base = (w.j0 + j) * kKeys;
                 const uint32_t bad_pages = *static_cast<volatile uint32_t *>(&queue->bad_pages[t & 15]);
                 const bool edge = base + kKeys > ctx || base < seen_by_all || bad_pages;
-                if (edge && (base + kKeys > ctx || base < seen_by_all)) {
+                if (__builtin_expect(edge && (base + kKeys > ctx || base < seen_by_all), 0)) {
                     // Clean V: rows that no row sees are zeroed (past the sequence, before the
                     // window), partly seen ones lose and note what is not finite.
                     const int s = t % C::STAGES;
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 if (busy) {
                     uint32_t sr[kKeys];
                     tmem_load_64(tmem + t_lane + s_col, sr);
-                    if (edge) {
+                    if (__builtin_expect(edge, 0)) {
                         uint64_t see = 0;
                         if (mine) {
                             see = (ones(ctx - base) & ~ones(low - base)) | mask_bits_at(mask, word0, base - ctx, w.T);
