@@ -362,6 +362,49 @@ def pa_ragged_prefill(o, q, k, v, qo_indptr_h, kv_indptr_h, qo_indptr_d, kv_indp
         workspace.numel(), _stream(stream)))
 
 
+# The kernels take addresses: a tensor of another type, with gaps or on another device would be read
+# as if it were what they expect.  The calls below look at every operand first, and read each
+# property once (a short tree's call is as long as its kernel).
+_INT32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _addresses(*tensors):
+    """Data pointers of tensors that are all on the current device, where the library launches."""
+    devices = list(map(torch.Tensor.get_device, tensors))   # -1: not on a GPU
+    device = devices[0]
+    assert device >= 0 and devices.count(device) == len(devices) and \
+        device == torch.cuda.current_device(), "tensors must be on the current CUDA device"
+    return list(map(torch.Tensor.data_ptr, tensors))
+
+
+def _check_int32(n, *arrays):
+    for t in arrays:
+        assert t.dtype is _INT32 and t.is_contiguous() and t.numel() >= n, \
+            "tables, lengths and offsets must be dense int32 tensors that cover the batch"
+
+
+def _kv_pools(k_cache, v_cache, layout):
+    """(num_blocks, kv heads, block size, head_dim, strides of a block, head, token, kv_dtype)."""
+    shape, strides, kind = k_cache.shape, k_cache.stride(), kv_dtype_of(k_cache)
+    assert len(shape) == 4 and strides[3] == 1, "pool must be 4-D with a contiguous head_dim"
+    assert v_cache.shape == shape and v_cache.stride() == strides and \
+        (v_cache.dtype is k_cache.dtype or kv_dtype_of(v_cache) == kind), \
+        "the K and V pools differ in geometry or type"
+    nb, x, y, hd = shape
+    sb, sx, sy, _ = strides
+    return (nb, x, y, hd, sb, sx, sy, kind) if layout == "HND" else (nb, y, x, hd, sb, sy, sx, kind)
+
+
+def _rows(out, q, head_dim):
+    """(rows, query heads) of q, which out is to be like."""
+    shape = q.shape
+    rows, heads, hd = shape
+    assert hd == head_dim and out.shape == shape and q.dtype is out.dtype is _BF16 and \
+        q.is_contiguous() and out.is_contiguous(), \
+        "q and out must be dense bf16 tensors of one shape, with the pools' head_dim"
+    return rows, heads
+
+
 def tree_decode_workspace_size(num_seqs, max_tree_len, num_q_heads, num_kv_heads, head_dim) -> int:
     return int(load().pa_tree_decode_workspace_size(num_seqs, max_tree_len, num_q_heads,
                                                     num_kv_heads, head_dim))
@@ -374,19 +417,21 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, 
     qo_indptr[b] .. qo_indptr[b + 1] - 1 of q and the last tokens of its cache (counted in
     seq_lens); each sees the context and the nodes whose bits tree_mask [rows, words] (int64)
     sets for it.  max_tree_len is at least the largest tree."""
-    nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
-    sb, sh, st = pool_strides(k_cache, layout)
-    rows, nq, _ = q.shape
+    nb, nkv, bs, hd, sb, sh, st, kind = _kv_pools(k_cache, v_cache, layout)
+    rows, nq = _rows(out, q, hd)
     mask_rows, words = tree_mask.shape
     seqs, blocks = block_tables.shape
-    assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and mask_rows == rows
-    _check(load().pa_tree_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
-                                 _ptr(tree_mask), words, seqs, rows,
-                                 int(max_tree_len), nq, nkv, hd, bs, blocks, nb, sb,
-                                 sh, st, float(sm_scale), int(sliding_window),
-                                 kv_dtype_of(k_cache), float(k_scale), float(v_scale),
-                                 _ptr(workspace), workspace.numel(), _stream(stream)))
+    assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and mask_rows == rows, \
+        "tree_mask must be a dense int64 tensor with a row of words per row of q"
+    _check_int32(seqs, block_tables, seq_lens)
+    _check_int32(seqs + 1, qo_indptr)
+    assert workspace.is_contiguous(), "workspace must be dense"
+    o, q, k, v, tables, lens, indptr, mask, ws = _addresses(
+        out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, tree_mask, workspace)
+    _check(load().pa_tree_decode(o, q, k, v, tables, lens, indptr, mask, words, seqs, rows,
+                                 int(max_tree_len), nq, nkv, hd, bs, blocks, nb, sb, sh, st,
+                                 float(sm_scale), int(sliding_window), kind, float(k_scale),
+                                 float(v_scale), ws, workspace.numel(), _stream(stream)))
 
 
 def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, accepted,
@@ -406,14 +451,18 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
         layouts = list(map(torch.Tensor.stride, pools))
     for values in ([t.shape for t in pools], layouts, [t.dtype for t in pools]):
         assert values.count(values[0]) == n, "pools differ in geometry"
-    assert accepted.dtype == torch.int32 and accepted.is_contiguous()
-    addresses = array.array("Q", list(map(torch.Tensor.data_ptr, pools)))
-    _check(load().pa_tree_commit(addresses.buffer_info()[0], n, _ptr(block_tables),
-                                 _ptr(seq_lens), _ptr(qo_indptr), _ptr(accepted),
-                                 _ptr(accept_lens), _ptr(new_seq_lens), block_tables.shape[0],
-                                 int(max_tree_len), accepted.shape[1], nkv, hd, bs,
-                                 block_tables.shape[1], nb, sb, sh, st, kv_dtype_of(pools[0]),
-                                 _stream(stream)))
+    seqs, blocks = block_tables.shape
+    paths, most = accepted.shape
+    assert accepted.dtype is _INT32 and accepted.is_contiguous() and paths == seqs, \
+        "accepted must be a dense int32 tensor with a row per sequence"
+    _check_int32(seqs, block_tables, seq_lens, accept_lens, new_seq_lens)
+    _check_int32(seqs + 1, qo_indptr)
+    tables, lens, indptr, path, kept, new, *at = _addresses(
+        block_tables, seq_lens, qo_indptr, accepted, accept_lens, new_seq_lens, *pools)
+    at = array.array("Q", at)
+    _check(load().pa_tree_commit(at.buffer_info()[0], n, tables, lens, indptr, path, kept, new,
+                                 seqs, int(max_tree_len), most, nkv, hd, bs, blocks, nb, sb, sh,
+                                 st, kv_dtype_of(pools[0]), _stream(stream)))
 
 
 def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, first_tokens=None,
@@ -424,12 +473,16 @@ def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, firs
     nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
     sb, sh, st = pool_strides(k_cache, layout)
     seqs, blocks = block_tables.shape
+    kind = kv_dtype_of(k_cache)
     assert bounds.is_contiguous() and bounds.shape == (nb, nkv, 2, hd) and \
-        bounds.element_size() == k_cache.element_size()
-    _check(load().pa_page_bounds(_ptr(bounds), _ptr(k_cache), _ptr(block_tables), _ptr(seq_lens),
-                                 _ptr(first_tokens), int(max_new_tokens), seqs,
-                                 nkv, hd, bs, blocks, nb, sb, sh, st,
-                                 kv_dtype_of(k_cache), _stream(stream)))
+        kv_dtype_of(bounds) == kind, \
+        "bounds must be a dense [num_blocks, nkv, 2, hd] tensor of the pool's type"
+    first = () if first_tokens is None else (first_tokens,)
+    _check_int32(seqs, block_tables, seq_lens, *first)
+    out, k, tables, lens, *first = _addresses(bounds, k_cache, block_tables, seq_lens, *first)
+    _check(load().pa_page_bounds(out, k, tables, lens, first[0] if first else None,
+                                 int(max_new_tokens), seqs, nkv, hd, bs, blocks, nb, sb, sh, st,
+                                 kind, _stream(stream)))
 
 
 def select_pages_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
@@ -442,14 +495,21 @@ def pa_select_pages(page_tables, page_lens, q, bounds, block_tables, seq_lens, w
     pages' key bounds, into page_tables [B, nkv, max_pages] and page_lens [B] (int32); the
     first sink_pages and the last recent_pages are always among them."""
     nb, nkv, _, hd = bounds.shape
-    B, nq, _ = q.shape
+    B, nq, qd = q.shape
     rows, heads, most = page_tables.shape
-    assert bounds.is_contiguous() and page_tables.is_contiguous() and rows == B and heads == nkv
-    _check(load().pa_select_pages(_ptr(page_tables), _ptr(page_lens), _ptr(q), _ptr(bounds),
-                                  _ptr(block_tables), _ptr(seq_lens), B, nq, nkv, hd, PAGE_TOKENS,
-                                  block_tables.shape[1], nb, most, int(sink_pages),
-                                  int(recent_pages), kv_dtype_of(bounds), _ptr(workspace),
-                                  workspace.numel(), _stream(stream)))
+    blocks = block_tables.shape[1]
+    assert bounds.is_contiguous(), "bounds must be dense"
+    assert q.dtype is _BF16 and q.is_contiguous() and qd == hd, \
+        "q must be a dense bf16 tensor with the bounds' head_dim"
+    assert rows == B and heads == nkv, "page_tables must be [B, nkv, max_pages]"
+    _check_int32(B, page_tables, page_lens, seq_lens)
+    _check_int32(B * blocks, block_tables)
+    assert workspace.is_contiguous(), "workspace must be dense"
+    pages, kept, at, bnd, tables, lens, ws = _addresses(
+        page_tables, page_lens, q, bounds, block_tables, seq_lens, workspace)
+    _check(load().pa_select_pages(pages, kept, at, bnd, tables, lens, B, nq, nkv, hd, PAGE_TOKENS,
+                                  blocks, nb, most, int(sink_pages), int(recent_pages),
+                                  kv_dtype_of(bounds), ws, workspace.numel(), _stream(stream)))
 
 
 def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, workspace,
@@ -457,16 +517,17 @@ def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, 
     """Split decode of q [B, nq, hd] over the pages page_tables [B, nkv, max_pages] lists per
     (sequence, kv head), page_lens[b] tokens each; the workspace is that of a split decode
     of max_pages pages."""
-    nb, nkv, bs, hd = _pool_geometry(k_cache, layout)
-    sb, sh, st = pool_strides(k_cache, layout)
-    B, nq, _ = q.shape
+    nb, nkv, bs, hd, sb, sh, st, kind = _kv_pools(k_cache, v_cache, layout)
+    B, nq = _rows(out, q, hd)
     rows, heads, most = page_tables.shape
-    assert page_tables.is_contiguous() and rows == B and heads == nkv
-    _check(load().pa_decode_pages(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(page_tables), _ptr(page_lens), B, nq, nkv, hd, bs,
-                                  most, nb, sb, sh, st, float(sm_scale),
-                                  kv_dtype_of(k_cache), float(k_scale), float(v_scale),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)))
+    assert rows == B and heads == nkv, "page_tables must be [B, nkv, max_pages]"
+    _check_int32(B, page_tables, page_lens)
+    assert workspace.is_contiguous(), "workspace must be dense"
+    o, q, k, v, tables, lens, ws = _addresses(out, q, k_cache, v_cache, page_tables, page_lens,
+                                              workspace)
+    _check(load().pa_decode_pages(o, q, k, v, tables, lens, B, nq, nkv, hd, bs, most, nb, sb, sh,
+                                  st, float(sm_scale), kind, float(k_scale), float(v_scale), ws,
+                                  workspace.numel(), _stream(stream)))
 
 
 def selftest_wait_timeout(stream=None):
