@@ -354,8 +354,7 @@ int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_
  *                 before it (a path from the root down); entries past accept_lens[b]
  *                 are not read
  *   accept_lens   [num_seqs] int32
- *   new_seq_lens  [num_seqs] int32, written; shares no memory with seq_lens, accept_lens
- *                 or qo_indptr
+ *   new_seq_lens  [num_seqs] int32, written; shares no memory with what the call reads
  * A path is cut before its first entry that is out of range or not ascending, and
  * before max_accept entries; a sequence whose T_b is negative or exceeds max_tree_len
  * or seq_lens[b] keeps its length and rows; both set PA_ERR_DEVICE_BOUNDS.  A page id

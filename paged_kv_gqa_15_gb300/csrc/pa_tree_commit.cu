@@ -130,8 +130,10 @@ extern "C" int pa_tree_commit(void *const *pools, int num_pools, const int32_t *
         return api_fail(PA_ERR_INVALID, "null pointer argument");
     if (api_overlap(new_seq_lens, num_seqs, seq_lens, num_seqs) ||
         api_overlap(new_seq_lens, num_seqs, accept_lens, num_seqs) ||
-        api_overlap(new_seq_lens, num_seqs, qo_indptr, num_seqs + 1))
-        return api_fail(PA_ERR_INVALID, "new_seq_lens must not be seq_lens, accept_lens or qo_indptr");
+        api_overlap(new_seq_lens, num_seqs, qo_indptr, num_seqs + 1) ||
+        api_overlap(new_seq_lens, num_seqs, accepted, static_cast<int64_t>(num_seqs) * max_accept) ||
+        api_overlap(new_seq_lens, num_seqs, block_tables, static_cast<int64_t>(num_seqs) * max_blocks_per_seq))
+        return api_fail(PA_ERR_INVALID, "new_seq_lens must not overlap what the call reads");
     for (int i = 0; i < num_pools; ++i)
         if (!pools[i] || (reinterpret_cast<uintptr_t>(pools[i]) & 15u))
             return api_fail(PA_ERR_INVALID, "pools[%d] is NULL or not 16-byte aligned", i);

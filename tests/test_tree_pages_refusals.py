@@ -1,0 +1,38 @@
+"""Host-side refusals of the tree and page-selection entry points (no GPU: validation comes before any
+CUDA call): outputs that share memory with what the kernels still read."""
+import ctypes
+
+import pytest
+
+import paged_kv_gqa_15_gb300 as pa
+
+
+def at(i):
+    """Buffers far from one another."""
+    return 0x1000000 * (i + 1)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    return pa.load()
+
+
+def commit(lib, **kw):
+    a = dict(pools=(ctypes.c_void_p * 2)(at(0), at(1)), bt=at(2), sl=at(3), ip=at(4), acc=at(5), al=at(6),
+             new=at(7), B=8, A=4, mb=4)
+    a.update(kw)
+    code = lib.pa_tree_commit(a["pools"], 2, a["bt"], a["sl"], a["ip"], a["acc"], a["al"], a["new"], a["B"], 8, a["A"],
+                              2, 128, 16, a["mb"], 10, 4096, 2048, 128, 0, None)
+    return code, lib.pa_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(new=at(5)), dict(new=at(5) + 8 * 4 * 4 - 4), dict(new=at(5) - 8 * 4 + 4),   # accepted
+    dict(new=at(2)), dict(new=at(2) + 8 * 4 * 4 - 4), dict(new=at(2) - 8 * 4 + 4),   # block_tables
+    dict(new=at(3)), dict(new=at(4) + 8 * 4), dict(new=at(6)),
+])
+def test_new_lengths_over_what_the_commit_reads(lib, kw):
+    code, why = commit(lib, **kw)
+    assert code == pa.PA_ERR_INVALID and "new_seq_lens" in why
