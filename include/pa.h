@@ -411,7 +411,7 @@ size_t pa_select_pages_workspace_size(int num_seqs, int num_kv_heads, int max_bl
  * max_pages > 0, sink_pages >= 0, recent_pages >= 1 (a newest page's bounds may lag its
  * rows), sink_pages + recent_pages <= max_pages, max_blocks_per_seq <= 524288.  A page id
  * outside the pool scores lowest and sets PA_ERR_DEVICE_BOUNDS.  page_tables and page_lens
- * share no memory with block_tables and seq_lens.
+ * share no memory with block_tables, seq_lens or one another.
  */
 int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const void *q, const void *bounds,
                     const int32_t *block_tables, const int32_t *seq_lens, int num_seqs,

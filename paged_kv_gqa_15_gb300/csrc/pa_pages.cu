@@ -1082,10 +1082,12 @@ extern "C" int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const v
         return api_fail(PA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (!workspace || !aligned(workspace, 256))
         return api_fail(PA_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
-    if (api_overlap(page_lens, num_seqs, seq_lens, num_seqs) ||
-        api_overlap(page_tables, static_cast<int64_t>(num_seqs) * num_kv_heads * max_pages, block_tables,
-                    static_cast<int64_t>(num_seqs) * max_blocks_per_seq))
-        return api_fail(PA_ERR_INVALID, "page_lens and page_tables must not be seq_lens and block_tables");
+    const int64_t listed = static_cast<int64_t>(num_seqs) * num_kv_heads * max_pages;
+    const int64_t tables = static_cast<int64_t>(num_seqs) * max_blocks_per_seq;
+    if (api_overlap(page_lens, num_seqs, seq_lens, num_seqs) || api_overlap(page_lens, num_seqs, block_tables, tables) ||
+        api_overlap(page_tables, listed, seq_lens, num_seqs) || api_overlap(page_tables, listed, block_tables, tables) ||
+        api_overlap(page_tables, listed, page_lens, num_seqs))
+        return api_fail(PA_ERR_INVALID, "page_lens and page_tables must not overlap seq_lens, block_tables or one another");
     char *ws = static_cast<char *>(workspace);
     SelectParams p = {};
     p.page_tables = page_tables;

@@ -36,3 +36,22 @@ def commit(lib, **kw):
 def test_new_lengths_over_what_the_commit_reads(lib, kw):
     code, why = commit(lib, **kw)
     assert code == pa.PA_ERR_INVALID and "new_seq_lens" in why
+
+
+def select(lib, **kw):
+    a = dict(pt=at(0), pl=at(1), bt=at(2), sl=at(3), B=8, nkv=2, most=4, mb=8)
+    a.update(kw)
+    code = lib.pa_select_pages(a["pt"], a["pl"], at(4), at(5), a["bt"], a["sl"], a["B"], 8, a["nkv"], 128, 16, a["mb"], 10,
+                               a["most"], 1, 1, 0, at(6), 1 << 40, None)
+    return code, lib.pa_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(pl=at(2)), dict(pl=at(2) + 8 * 8 * 4 - 4), dict(pl=at(2) - 8 * 4 + 4),      # page_lens, block_tables
+    dict(pt=at(3)), dict(pt=at(3) + 8 * 4 - 4), dict(pt=at(3) - 8 * 2 * 4 * 4 + 4),  # page_tables, seq_lens
+    dict(pt=at(1)), dict(pl=at(0) + 8 * 2 * 4 * 4 - 4),                              # one another
+    dict(pl=at(3)), dict(pt=at(2)),
+])
+def test_page_lists_over_what_the_selection_reads(lib, kw):
+    code, why = select(lib, **kw)
+    assert code == pa.PA_ERR_INVALID and "page_lens and page_tables" in why
