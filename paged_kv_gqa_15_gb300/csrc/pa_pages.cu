@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(256) bounds_kernel(const __grid_constant__ Bou
         // a sequence's first unit sees whether its pages go on past the launch's
         bad = bad || (L + kBlockSize - 1) / kBlockSize - first / kBlockSize > p.pages;
         if (bad && rest == 0) atomicOr(p.status, kStatusBounds);
-        my_rows = first < L ? max(0, min(kBlockSize, L - page * kBlockSize)) : 0;
+        // (a page past the table could pass 2^31 tokens)
+        my_rows = first < L && page < p.max_blocks ? max(0, min(kBlockSize, L - page * kBlockSize)) : 0;
         if (my_rows > 0) {
             my_id = p.block_tables[b * p.max_blocks + page];
             if (my_id < 0 || my_id >= p.num_blocks) {
@@ -1006,7 +1007,8 @@ extern "C" int pa_page_bounds(void *bounds, const void *k_cache, const int32_t *
     // pages that max_new_tokens tokens can touch: one more when they start inside a page
     const int64_t touched = (static_cast<int64_t>(max_new_tokens) + (first_tokens ? 2 : 1) * (kBlockSize - 1)) / kBlockSize;
     const int pages = static_cast<int>(touched < max_blocks_per_seq ? touched : max_blocks_per_seq);
-    if (static_cast<int64_t>(num_seqs) * pages * num_kv_heads / 8 >= INT32_MAX)
+    if (static_cast<int64_t>(num_seqs) * pages * num_kv_heads / 8 >= INT32_MAX ||
+        static_cast<int64_t>(pages) * num_kv_heads > INT32_MAX)   // the kernel counts a sequence's in 32 bits
         return api_fail(PA_ERR_UNSUPPORTED, "too many pages for one launch");
     const int elem = kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2;
     BoundsParams p = {};

@@ -55,3 +55,13 @@ def select(lib, **kw):
 def test_page_lists_over_what_the_selection_reads(lib, kw):
     code, why = select(lib, **kw)
     assert code == pa.PA_ERR_INVALID and "page_lens and page_tables" in why
+
+
+@pytest.mark.parametrize("nkv,blocks,new,code", [
+    (17, (1 << 27) - 1, 2 ** 31 - 1, pa.PA_ERR_UNSUPPORTED),      # a sequence's (page, head) pairs pass 2^31
+    (128, (1 << 27) - 1, 2 ** 31 - 1, pa.PA_ERR_UNSUPPORTED),
+    (1 << 20, 1 << 12, 1 << 16, pa.PA_ERR_UNSUPPORTED),
+])
+def test_bounds_of_more_pages_than_32_bits_count(lib, nkv, blocks, new, code):
+    assert lib.pa_page_bounds(at(0), at(1), at(2), at(3), None, new, 1, nkv, 64, 16, blocks, 10, 16 * nkv * 64, 1024, 64, 0,
+                              None) == code
