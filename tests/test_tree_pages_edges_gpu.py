@@ -1,0 +1,146 @@
+"""Edges of the tree and page-selection calls: lengths and page ids out of range where nothing is
+ranked, bounds of pages that are never ranked, query groups split over several kernel groups, padded
+pools, captured commits, tables of 2^27 pages."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_gqa_15_gb300 as pa
+from tests import ref64
+from tests import test_pages_gpu as P
+from tests import test_tree_gpu as T
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BOUNDS = 1 << pa.PA_ERR_DEVICE_BOUNDS
+
+
+# ---- lengths and page ids out of range ------------------------------------------------------
+
+def test_a_commit_whose_length_passes_its_table_is_skipped():
+    c = T.gpu(T.make([60, 64], [4, 4], 8, 2, 128, seed=16))
+    pools = [c["k"].clone(), c["v"].clone()]
+    c["lens"][1] = 65
+    new = T.run_commit(c, pools, torch.tensor([[3], [3]], dtype=torch.int32), torch.tensor([1, 1], dtype=torch.int32))
+    assert pa.device_status() == BOUNDS and new.tolist() == [57, 65]
+    want, _ = ref64.commit([c["k"], c["v"]], c["table"].cpu(), [60, 60], [0, 4, 8], torch.tensor([[3], [3]]), [1, 0])
+    assert all(torch.equal(g.cpu().view(torch.uint8), w.view(torch.uint8)) for g, w in zip(pools, want))
+
+
+# ---- groups that are split ------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,nkv,lens,nodes", [(320, 2, [150, 90], [3, 2]), (393, 3, [70], [2])])
+def test_trees_of_groups_beyond_a_row_tile(nq, nkv, lens, nodes, fp8):
+    """Several kernel groups per kv head, each kv head with keys of its own."""
+    c = T.gpu(T.make(lens, nodes, nq, nkv, 64, seed=74, fp8=fp8))
+    T.check(c, T.call(c))
+    assert pa.device_status() == 0
+
+
+def test_values_that_are_not_finite_in_split_groups():
+    """The values taken out of a tile are looked up again under the pool's kv head."""
+    c = T.make([90], [4], 320, 2, 64, seed=75)
+    for kh, node in ((0, 1), (1, 2)):
+        c["v"][c["table"][0, (86 + node) // 16], kh, (86 + node) % 16] = math.inf
+    c["mask"][:, 0] = torch.tensor([1, 2, 4, 8])
+    got = T.call(T.gpu(c)).cpu()
+    want = torch.zeros(4, 320, dtype=torch.bool)
+    want[1, :160] = want[2, 160:] = True
+    assert torch.equal(torch.isinf(got).all(-1), want) and torch.equal(torch.isfinite(got).all(-1), ~want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,nkv,hd", [(48, 2, 128), (24, 2, 128), (34, 2, 128), (51, 3, 128), (22, 2, 64), (6, 2, 256)])
+def test_page_lists_of_split_groups(nq, nkv, hd, fp8):
+    """Every kv head has a list of its own, also where its query heads are several kernel groups."""
+    c = P.make([1500, 40, 977], nq, nkv, hd, 76, fp8)
+    P.fill_bounds(c)
+    pages, lens = P.check_select(c, 37, 1, 2)
+    assert not torch.equal(pages[0, 0], pages[0, 1])
+    out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages.cpu(), lens.cpu(), c["scale"], "HND", c["kv_scale"],
+                                    c["kv_scale"])
+    ref64.assert_attention(P.decode(c, pages, lens), out, bound, P.FP8_EXTRA if fp8 else 0.0)
+    assert pa.device_status() == 0
+
+
+# ---- padded pools ---------------------------------------------------------------------------
+
+def padded(pool):
+    """The pool's values with room between pages, heads and tokens; codes of NaN in the room."""
+    n, h, t, d = pool.shape
+    raw = pool.view(torch.uint8)
+    wide = torch.full((n, h + 1, t, d + 16), math.nan).to(pool.dtype).to(pool.device)
+    view = wide[:, :h, :, :d]
+    view.copy_(pool) if pool.dtype == torch.bfloat16 else view.view(torch.uint8).copy_(raw)
+    return wide, view
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_commit_in_padded_pools(layout, fp8):
+    c = T.gpu(T.make([40, 23], [12, 23], 4, 2, 64, seed=77, fp8=fp8, layout=layout))
+    paths, kept = torch.tensor([[0, 3, 4, 11], [2, 5, 21, 22]], dtype=torch.int32), torch.tensor([4, 3], dtype=torch.int32)
+    want, lens = ref64.commit([c["k"], c["v"]], c["table"].cpu(), c["lens"].cpu(), c["indptr"].cpu(), paths, kept, layout)
+    whole, pools = zip(*(padded(c[n]) for n in ("k", "v")))
+    before = [w.view(torch.uint8).clone() for w in whole]
+    assert T.run_commit(c, list(pools), paths, kept).tolist() == lens
+    for got, ref, w, b in zip(pools, want, whole, before):
+        assert torch.equal(got.contiguous().cpu().view(torch.uint8), ref.view(torch.uint8))
+        outside = torch.ones(w.shape, dtype=torch.bool, device=DEV)
+        outside[:, :got.shape[1], :, :got.shape[3]] = False
+        now = w.view(torch.uint8)
+        if now.shape != w.shape:
+            outside = outside.repeat_interleave(2, -1)
+        assert torch.equal(now[outside], b[outside])
+    assert pa.device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+@pytest.mark.parametrize("nq,nkv,hd", [(2, 2, 64), (8, 2, 128), (4, 1, 64), (16, 2, 256), (24, 2, 64)])
+def test_bounds_and_page_lists_over_padded_pools(nq, nkv, hd, layout, fp8):
+    c = P.make([700, 40], nq, nkv, hd, 78, fp8, layout)
+    P.fill_bounds(c)
+    dense = c["bounds"].clone()
+    pages, lens = P.check_select(c, 17, 1, 2)
+    want = P.decode(c, pages, lens)
+    c["k"], c["v"] = padded(c["k"])[1], padded(c["v"])[1]
+    c["bounds"].zero_()
+    P.fill_bounds(c)
+    assert torch.equal(c["bounds"].view(torch.uint8), dense.view(torch.uint8))
+    assert torch.equal(P.decode(c, pages, lens), want)
+    assert pa.device_status() == 0
+
+
+# ---- capture --------------------------------------------------------------------------------
+
+def test_a_captured_step_of_trees_and_commit_replays():
+    """Verification and commit of all layers as one graph, replayed with other paths and trees."""
+    c = T.gpu(T.make([100, 61], [6, 6], 8, 2, 128, seed=79))
+    c["k"], c["v"] = c["k"].nan_to_num(0.0), c["v"].nan_to_num(0.0)
+    keys, vals = [c["k"].clone() for _ in range(3)], [c["v"].clone() for _ in range(3)]
+    path, kept = torch.tensor([[0, 2, 5], [1, 3, 0]], dtype=torch.int32, device=DEV), torch.tensor([3, 2], dtype=torch.int32, device=DEV)
+    new, out, ws = torch.zeros(2, dtype=torch.int32, device=DEV), torch.full_like(c["q"], 7.0), T.space(c)
+
+    def step():
+        T.call(c, out=out, ws=ws)
+        pa.pa_tree_commit(keys, vals, c["table"], c["lens"], c["indptr"], path, kept, new, 6)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for paths, n in (([[1, 2, 4], [0, 4, 5]], [3, 3]), ([[5, 0, 0], [2, 3, 4]], [1, 0]), ([[3, 4, 5], [3, 0, 0]], [3, 1])):
+        path.copy_(torch.tensor(paths)), kept.copy_(torch.tensor(n))
+        for i in range(3):
+            keys[i].copy_(c["k"] + i), vals[i].copy_(c["v"] - i)
+        pools = [t for kv in zip(keys, vals) for t in kv]
+        want, lens = ref64.commit(pools, c["table"].cpu(), c["lens"].cpu(), c["indptr"].cpu(), path.cpu(), kept.cpu())
+        graph.replay()
+        torch.cuda.synchronize()
+        T.check(c, out)
+        assert new.tolist() == lens
+        assert all(torch.equal(g.cpu().view(torch.uint8), w.view(torch.uint8)) for g, w in zip(pools, want))
+    assert pa.device_status() == 0
