@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b = threadIdx.x; b < p.num_seqs; b += kScoreThreads) {
-        const int np = (select_len(p, b, blockIdx.x == 0) + kBlockSize - 1) / kBlockSize;
+        const int np = (select_len(p, b, false) + kBlockSize - 1) / kBlockSize;
         pages[b] = np;
         pref[b + 1] = np > p.max_pages ? static_cast<int64_t>((np + C::GROUP - 1) / C::GROUP) * p.nkv : 0;
     }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     __shared__ int bin_at, bin_above, near_n, few_n;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int L = select_len(p, b, false);
+    const int L = select_len(p, b, kh == 0 && tid == 0);
     const int np = (L + kBlockSize - 1) / kBlockSize;
     const int kept = min(np, p.max_pages);
     const int64_t row = static_cast<int64_t>(b) * p.nkv + kh;
@@ -643,8 +643,12 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
     int32_t *out = p.page_tables + row * p.max_pages;
     if (kh == 0 && tid == 0) p.page_lens[b] = kept * kBlockSize - (np * kBlockSize - L);
     for (int i = kept + tid; i < p.max_pages; i += NT) out[i] = -1;
-    if (np <= p.max_pages) {
-        for (int i = tid; i < np; i += NT) out[i] = bt[i];
+    if (np <= p.max_pages) {   // no score pass has seen these pages' ids
+        for (int i = tid; i < np; i += NT) {
+            const int id = bt[i];
+            out[i] = id;
+            if (id < 0 || id >= p.num_blocks) atomicOr(p.status, kStatusBounds);
+        }
         return;
     }
     // f of the candidates [lo, hi) join the sinks and the newest pages

@@ -18,6 +18,35 @@ BOUNDS = 1 << pa.PA_ERR_DEVICE_BOUNDS
 
 # ---- lengths and page ids out of range ------------------------------------------------------
 
+def test_selection_of_every_page_flags_bad_pages():
+    for most in (50, 64):                           # the table's width, and more than it
+        c = P.make([800, 333], 4, 2, 64, 70)
+        P.fill_bounds(c)
+        P.check_select(c, most, 1, 1)
+        assert pa.device_status() == 0
+        for bad in (-3, c["k"].shape[0], 2 ** 31 - 1):
+            c["table"][1, 20] = bad                 # the last page of sequence 1
+            P.check_select(c, most, 1, 1)
+            assert pa.device_status() == BOUNDS
+
+
+def test_selection_of_every_page_of_one_sequence_flags_its_bad_page():
+    c = P.make([800, 100], 4, 2, 64, 71)
+    P.fill_bounds(c)
+    c["table"][1, 2] = -1
+    P.check_select(c, 12, 1, 1)                     # sequence 0's pages are ranked, sequence 1's are not
+    assert pa.device_status() == BOUNDS
+
+
+def test_selection_of_every_page_flags_a_length_past_the_table():
+    c = P.make([800, 800], 4, 2, 64, 72)
+    P.fill_bounds(c)
+    c["lens"][1] = 801
+    pages, lens = P.select(c, 50, 1, 1)
+    assert pa.device_status() == BOUNDS
+    assert lens.tolist() == [800, 800] and torch.equal(pages[1, 0], c["table"][1])
+
+
 def test_a_commit_whose_length_passes_its_table_is_skipped():
     c = T.gpu(T.make([60, 64], [4, 4], 8, 2, 128, seed=16))
     pools = [c["k"].clone(), c["v"].clone()]
