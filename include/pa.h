@@ -325,8 +325,9 @@ size_t pa_tree_decode_workspace_size(int num_seqs, int max_tree_len, int num_q_h
  *   tree_mask     [total_rows][mask_words] 64-bit words, device, 8-byte aligned;
  *                 mask_words >= ceil(max_tree_len / 64)
  *   max_tree_len  >= every T_b, at most PA_MAX_TREE_LEN
- * A sequence whose T_b is negative, exceeds max_tree_len or seq_lens[b], or whose rows
- * leave [0, total_rows) is skipped (its rows are not written) and sets
+ * A sequence whose T_b is negative, exceeds max_tree_len or seq_lens[b], whose rows leave
+ * [0, total_rows), or whose seq_lens[b] exceeds max_blocks_per_seq * block_size (its nodes
+ * are not in the table) is skipped (its rows are not written) and sets
  * PA_ERR_DEVICE_BOUNDS.  Block tables, pools, kv_dtype and scales are those of
  * pa_decode; sm_scale must be positive and finite.  The call reads qo_indptr, lengths
  * and masks on the device only, so a captured call can be replayed with new trees.
@@ -357,8 +358,9 @@ int pa_tree_decode(void *out, const void *q, const void *k_cache, const void *v_
  *   new_seq_lens  [num_seqs] int32, written; shares no memory with what the call reads
  * A path is cut before its first entry that is out of range or not ascending, and
  * before max_accept entries; a sequence whose T_b is negative or exceeds max_tree_len
- * or seq_lens[b] keeps its length and rows; both set PA_ERR_DEVICE_BOUNDS.  A page id
- * outside the pool is neither read nor written and sets it too.  Pages that hold
+ * or seq_lens[b], or whose seq_lens[b] exceeds max_blocks_per_seq * block_size, keeps its
+ * length and rows; both set PA_ERR_DEVICE_BOUNDS.  A page id outside the pool is neither
+ * read nor written and sets it too.  Pages that hold
  * drafted tokens must belong to one sequence only.  One launch per 128 pools.
  */
 int pa_tree_commit(void *const *pools, int num_pools, const int32_t *block_tables,

@@ -146,7 +146,8 @@ __device__ __forceinline__ int piece_slot(const TreeLaunch &a, int cta, bool sta
 }
 
 // Sequence b's drafted rows and lengths; T = 0 (and the device status set when `flag`) if
-// they make no sense.
+// they make no sense, a length past the table among them: its nodes are then not in the table.
+// (A page list that claims more tokens than it has pages ends with its pages, as in the split decode.)
 struct TreeSeq {
     int row0, T, L;
 };
@@ -163,7 +164,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b, bool fla
     s.T = 0;
     if (LISTS)
         s.T = 1;
-    else if (s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && row1 - s.row0 <= p.max_tree_len &&
+    else if (!bad && s.row0 >= 0 && row1 >= s.row0 && row1 <= p.total_rows && row1 - s.row0 <= p.max_tree_len &&
         row1 - s.row0 <= s.L)
         s.T = row1 - s.row0;
     else

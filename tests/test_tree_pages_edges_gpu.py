@@ -47,6 +47,19 @@ def test_selection_of_every_page_flags_a_length_past_the_table():
     assert lens.tolist() == [800, 800] and torch.equal(pages[1, 0], c["table"][1])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_tree_whose_length_passes_its_table_is_skipped(fp8):
+    """Its nodes would be tokens that the table does not hold: no row of it is written."""
+    c = T.gpu(T.make([60, 64, 60], [4, 4, 4], 8, 2, 128, seed=15, fp8=fp8))
+    good = T.call(c)
+    assert pa.device_status() == 0
+    for n in (65, 10 ** 6, 2 ** 31 - 1):
+        c["lens"][1] = n
+        got = T.call(c)
+        assert pa.device_status() == BOUNDS
+        assert torch.equal(got[:4], good[:4]) and torch.equal(got[8:], good[8:]) and bool((got[4:8] == 7).all())
+
+
 def test_a_commit_whose_length_passes_its_table_is_skipped():
     c = T.gpu(T.make([60, 64], [4, 4], 8, 2, 128, seed=16))
     pools = [c["k"].clone(), c["v"].clone()]
