@@ -10,7 +10,7 @@
 // than one head, and the pass is bound by reading the bounds (2 head_dim elements a page).
 //
 // Selection is by exact scores.  A score computed in fp32 is off by at most
-//     E = (group + 24) 2^-24 S + 2^-140,  S >= sum_d |P_d max_d| + |N_d min_d| of any page
+//     E = (group + 24) 2^-24 S + 2^-140,  S >= sum_d |P_d max_d| + |N_d min_d| of any ranked page
 // (P and N are sums of `group` terms of one sign: group - 1 roundings; a product is rounded
 // once at most, added in a chain of up to 16, joined over at most 32 lanes in five sums; S
 // itself and T +- 2E are rounded: fewer than group + 24 act on any term.  Products below the
@@ -200,7 +200,7 @@ struct SelectParams {
     const uint8_t *bounds;
     const int32_t *block_tables, *seq_lens;
     float *score;       // [B][nkv][max_blocks]
-    float *span;        // [B][nkv][groups]: largest S of a group's pages
+    float *span;        // [B][nkv][groups]: largest S of a group's ranked pages (0: it has none)
     double *exact;      // [B][nkv][max_blocks], of the pages that are scored again
     int64_t num_blocks;
     int num_seqs, nq, nkv, max_blocks, group, groups, max_pages, sink, recent;   // group: pages of one S
@@ -368,10 +368,12 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
     auto send = [&](int stage, int b, int kh, int grp, int id) -> unsigned {
         const bool known = id >= 0 && id < p.num_blocks;
         if (!known) atomicOr(p.status, kStatusBounds);
-        const int n = min(C::GROUP, pages[b] - grp * C::GROUP);
         // lane i knows where page i's bounds are, in units of 16 bytes (the host sees to it that 32
-        // bits hold them); lanes past the group's pages take its first
-        const uint32_t place = (static_cast<uint32_t>(__shfl_sync(kAll, known ? id : 0, lane < n ? lane : 0)) * p.nkv + kh) * UNITS;
+        // bits hold them).  Pages that are not ranked (the first ones, the newest, those past the end)
+        // take the group's first ranked one's: their own may hold anything, and S is not to know.
+        const int from = max(p.sink - grp * C::GROUP, 0), past = pages[b] - p.recent - grp * C::GROUP;
+        const int whose = lane >= from && lane < past ? lane : from;
+        const uint32_t place = (static_cast<uint32_t>(__shfl_sync(kAll, known ? id : 0, whose < C::GROUP ? whose : 0)) * p.nkv + kh) * UNITS;
         const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds) + unit;
 #pragma unroll
         for (int k = 0; k < LOADS; ++k) {
@@ -504,7 +506,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(const __grid_co
             const float y = __shfl_xor_sync(kAll, most, o);
             most = o < LANES ? most + y : max_nan(most, y);
         }
-        if (lane == 0) p.span[row * p.groups + grp] = most;
+        const bool ranked = max(p.sink, first) < min(pages[b] - p.recent, first + C::GROUP);
+        if (lane == 0) p.span[row * p.groups + grp] = ranked ? most : 0.f;
         fresh = kh1 != kh || b1 != b;
         b = b1, kh = kh1, grp = grp1;
         b1 = b2, kh1 = kh2, grp1 = grp2;

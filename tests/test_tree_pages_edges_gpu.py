@@ -70,6 +70,27 @@ def test_a_commit_whose_length_passes_its_table_is_skipped():
     assert all(torch.equal(g.cpu().view(torch.uint8), w.view(torch.uint8)) for g, w in zip(pools, want))
 
 
+# ---- bounds of pages that are never ranked --------------------------------------------------
+
+@pytest.mark.parametrize("fp8,poison", [(False, math.nan), (False, math.inf), (False, 3e38), (True, math.nan), (True, 448.0)])
+def test_bounds_of_pages_that_are_not_ranked_do_not_widen_the_border(fp8, poison):
+    """A newest page's bounds may lag its rows, so that they may hold anything; nor are the first
+    pages ranked.  Such bounds must not send every page through the scores in 64 bits: the
+    workspace's place for those, its last part, stays as it was."""
+    c = P.make([1600, 1440, 690], 4, 2, 64, 73, fp8)
+    P.fill_bounds(c)
+    for b, n in enumerate((100, 90, 44)):
+        ids = c["table"][b, [0, 1, n - 3, n - 2, n - 1]].long()
+        c["bounds"][ids] = torch.tensor(poison).to(c["bounds"].dtype).to(DEV)
+    want = ref64.select(c["q"], c["bounds"], c["table"].cpu(), c["lens"].cpu(), 20, 2, 3)
+    ws = pa.alloc_workspace(pa.select_pages_workspace_size(3, 2, c["table"].shape[1]), DEV)
+    ws.fill_(171)
+    pages, lens = P.select(c, 20, 2, 3, ws)
+    assert torch.equal(pages.cpu(), want[0]) and torch.equal(lens.cpu(), want[1])
+    assert bool((ws[-3 * 2 * 100 * 8:] == 171).all())
+    assert pa.device_status() == 0
+
+
 # ---- groups that are split ------------------------------------------------------------------
 
 @pytest.mark.parametrize("fp8", [False, True])
