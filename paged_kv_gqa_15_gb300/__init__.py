@@ -106,11 +106,12 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """The stream's handle, or the current one's of the current device, if the caller knows that."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -369,12 +370,12 @@ _INT32, _BF16 = torch.int32, torch.bfloat16
 
 
 def _addresses(*tensors):
-    """Data pointers of tensors that are all on the current device, where the library launches."""
+    """(device, data pointers...) of tensors on the current device, where the library launches."""
     devices = list(map(torch.Tensor.get_device, tensors))   # -1: not on a GPU
     device = devices[0]
     assert device >= 0 and devices.count(device) == len(devices) and \
         device == torch.cuda.current_device(), "tensors must be on the current CUDA device"
-    return list(map(torch.Tensor.data_ptr, tensors))
+    return (device, *map(torch.Tensor.data_ptr, tensors))
 
 
 def _check_int32(n, *arrays):
@@ -426,12 +427,12 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, 
     _check_int32(seqs, block_tables, seq_lens)
     _check_int32(seqs + 1, qo_indptr)
     assert workspace.is_contiguous(), "workspace must be dense"
-    o, q, k, v, tables, lens, indptr, mask, ws = _addresses(
+    device, o, q, k, v, tables, lens, indptr, mask, ws = _addresses(
         out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, tree_mask, workspace)
     _check(load().pa_tree_decode(o, q, k, v, tables, lens, indptr, mask, words, seqs, rows,
                                  int(max_tree_len), nq, nkv, hd, bs, blocks, nb, sb, sh, st,
                                  float(sm_scale), int(sliding_window), kind, float(k_scale),
-                                 float(v_scale), ws, workspace.numel(), _stream(stream)))
+                                 float(v_scale), ws, workspace.numel(), _stream(stream, device)))
 
 
 def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, accepted,
@@ -457,12 +458,12 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
         "accepted must be a dense int32 tensor with a row per sequence"
     _check_int32(seqs, block_tables, seq_lens, accept_lens, new_seq_lens)
     _check_int32(seqs + 1, qo_indptr)
-    tables, lens, indptr, path, kept, new, *at = _addresses(
+    device, tables, lens, indptr, path, kept, new, *at = _addresses(
         block_tables, seq_lens, qo_indptr, accepted, accept_lens, new_seq_lens, *pools)
     at = array.array("Q", at)
     _check(load().pa_tree_commit(at.buffer_info()[0], n, tables, lens, indptr, path, kept, new,
                                  seqs, int(max_tree_len), most, nkv, hd, bs, blocks, nb, sb, sh,
-                                 st, kv_dtype_of(pools[0]), _stream(stream)))
+                                 st, kv_dtype_of(pools[0]), _stream(stream, device)))
 
 
 def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, first_tokens=None,
@@ -479,10 +480,11 @@ def pa_page_bounds(bounds, k_cache, block_tables, seq_lens, max_new_tokens, firs
         "bounds must be a dense [num_blocks, nkv, 2, hd] tensor of the pool's type"
     first = () if first_tokens is None else (first_tokens,)
     _check_int32(seqs, block_tables, seq_lens, *first)
-    out, k, tables, lens, *first = _addresses(bounds, k_cache, block_tables, seq_lens, *first)
+    device, out, k, tables, lens, *first = _addresses(bounds, k_cache, block_tables, seq_lens,
+                                                      *first)
     _check(load().pa_page_bounds(out, k, tables, lens, first[0] if first else None,
                                  int(max_new_tokens), seqs, nkv, hd, bs, blocks, nb, sb, sh, st,
-                                 kind, _stream(stream)))
+                                 kind, _stream(stream, device)))
 
 
 def select_pages_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq) -> int:
@@ -505,11 +507,12 @@ def pa_select_pages(page_tables, page_lens, q, bounds, block_tables, seq_lens, w
     _check_int32(B, page_tables, page_lens, seq_lens)
     _check_int32(B * blocks, block_tables)
     assert workspace.is_contiguous(), "workspace must be dense"
-    pages, kept, at, bnd, tables, lens, ws = _addresses(
+    device, pages, kept, at, bnd, tables, lens, ws = _addresses(
         page_tables, page_lens, q, bounds, block_tables, seq_lens, workspace)
     _check(load().pa_select_pages(pages, kept, at, bnd, tables, lens, B, nq, nkv, hd, PAGE_TOKENS,
                                   blocks, nb, most, int(sink_pages), int(recent_pages),
-                                  kv_dtype_of(bounds), ws, workspace.numel(), _stream(stream)))
+                                  kv_dtype_of(bounds), ws, workspace.numel(),
+                                  _stream(stream, device)))
 
 
 def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, workspace,
@@ -523,11 +526,11 @@ def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, 
     assert rows == B and heads == nkv, "page_tables must be [B, nkv, max_pages]"
     _check_int32(B, page_tables, page_lens)
     assert workspace.is_contiguous(), "workspace must be dense"
-    o, q, k, v, tables, lens, ws = _addresses(out, q, k_cache, v_cache, page_tables, page_lens,
-                                              workspace)
+    device, o, q, k, v, tables, lens, ws = _addresses(out, q, k_cache, v_cache, page_tables,
+                                                      page_lens, workspace)
     _check(load().pa_decode_pages(o, q, k, v, tables, lens, B, nq, nkv, hd, bs, most, nb, sb, sh,
                                   st, float(sm_scale), kind, float(k_scale), float(v_scale), ws,
-                                  workspace.numel(), _stream(stream)))
+                                  workspace.numel(), _stream(stream, device)))
 
 
 def selftest_wait_timeout(stream=None):

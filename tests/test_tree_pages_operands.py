@@ -91,7 +91,7 @@ def test_one_host_tensor_among_device_tensors(call, monkeypatch):
         def __getattr__(self, name):
             return lambda *args: pa.PA_OK
     monkeypatch.setattr(pa, "load", Library)
-    monkeypatch.setattr(pa, "_stream", lambda stream: None)
+    monkeypatch.setattr(pa, "_stream", lambda *args: None)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     seen = []
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: seen.append(t) or 0)
