@@ -36,7 +36,8 @@
 //    hi + lo with s a power of two that puts the row's largest |q s| in [128, 256): the pair
 //    holds q to 2^-8 of its value.  P is split into three E5M2 terms: an f16 value's upper byte
 //    is an E5M2 value, so each term is a mask and a subtraction and four of them one byte
-//    permutation.  Three terms hold at least 9 bits (2^-8 of P, mostly better) over f16's range.
+//    permutation.  Three terms hold at least 9 bits, rounded (2^-9 of P, mostly better), over f16's
+//    range.
 //    P as E4M3 pairs has one product less and was 8 % faster in an earlier build (154 us against 167
 //    for 32 sequences of 1k-8k, 64-node trees), but E4M3 reaches from 448 to 2^-9
 //    only: weights far under one large maximum lost their bits, and they can be most of the sum.
@@ -377,13 +378,17 @@ __device__ __forceinline__ bool drop_non_finite(uint4 &v) {
 }
 
 // Four P values (0 to 2^15) as E5M2 codes of three terms that add up to them: by way of f16,
-// whose upper byte is the value cut to E5M2; what is cut off goes to the next term, exactly.
+// whose upper byte is the value cut to E5M2; what is cut off goes to the next term, exactly.  The
+// last term is rounded (cut, it left P up to 2^-8 too small and the outputs, whose sum of weights
+// is not cut, 2^-10 on average): half a step up for two keys, a hair less for the next two, so that
+// what lies half-way between does not all go one way.
 __device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float x3, uint32_t (&t)[3]) {
     uint32_t a, b;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x1), "f"(x0));
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x3), "f"(x2));
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
+        if (i == 2) a += 0x00800080u, b += 0x007f007fu;
         t[i] = __byte_perm(a, b, 0x7531);   // the upper bytes
         if (i == 2) break;
         const uint32_t ta = a & 0xff00ff00u, tb = b & 0xff00ff00u;

@@ -132,3 +132,28 @@ def test_wide_page_lists_within_the_kernels_own_precision(lens, most, nq, nkv, h
     out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages.cpu(), kept.cpu(), c["scale"], "HND", c["kv_scale"], c["kv_scale"])
     ref64.assert_attention(P.decode(c, pages, kept), out, bound,
                            extra(c["q"], c["k"], c["scale"], c["kv_scale"], most * 16))
+
+
+@gpu
+def test_weights_are_rounded_and_not_cut():
+    """One key of weight 1 and 199 of e^-x = 1 - 2^-11, whose f16 value 128 (1 - 2^-11) has eleven ones: cut
+    to nine bits it loses 0.1875 (2^-9.4 of its value), rounded it gains 0.0625.  All values are one
+    number, 64 of them in a row over a step of bf16, so that the outputs' own rounding averages out
+    to a 64th of a step: the mean of the outputs is off by at most half a step of nine bits just
+    under 128, 2^-10, and that."""
+    c = T.make([200], [1], 4, 1, 64, seed=94, fp8=True)
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = 1.0
+    k = torch.zeros(c["k"].shape)
+    k[c["table"][0, 3], :, 5, 0] = 1.0
+    c["k"], c["v"] = k.to(torch.float8_e4m3fn), torch.ones(c["v"].shape).to(torch.float8_e4m3fn)
+    c = T.gpu(c)
+    scale = -math.log1p(-2.0 ** -11)
+    off = []
+    for i in range(64):
+        value = 1.0 + (i + 0.5) / 64 * 2.0 ** -7
+        out = torch.empty_like(c["q"])
+        pa.pa_tree_decode(out, c["q"], c["k"], c["v"], c["table"], c["lens"], c["indptr"], c["mask"], scale, 1, T.space(c),
+                          k_scale=1.0, v_scale=value)
+        off.append(float(out.double().mean()) / value - 1.0)
+    assert abs(sum(off) / 64) <= 2.0 ** -10 + 2.0 ** -7 / 64
