@@ -181,7 +181,8 @@ __device__ __forceinline__ int tree_first_key(const TreeSeq &s, int window) {
 
 // Key tiles of one (sequence, kv head, row tile); one that masks everything for an empty page list.
 __device__ __forceinline__ int tree_tiles(const TreeSeq &s, int window) {
-    return s.T > 0 ? max(1, (s.L + kKeys - 1) / kKeys - tree_first_key(s, window) / kKeys) : 0;
+    // (a table may hold up to 2^31 - 16 tokens: L + 63 would not fit)
+    return s.T > 0 ? (s.L - 1) / kKeys + 1 - tree_first_key(s, window) / kKeys : 0;
 }
 
 // Row tiles that go together are worked on by as many CTAs at once (see TreeShares); with fewer
@@ -867,8 +868,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                 tc_fence_after_sync();
                 const int base = (w.j0 + j) * kKeys;
                 const uint32_t bad_pages = *static_cast<volatile uint32_t *>(&queue->bad_pages[t & 15]);
-                const bool edge = base + kKeys > ctx || base < seen_by_all || bad_pages;
-                if (__builtin_expect(edge && (base + kKeys > ctx || base < seen_by_all), 0)) {
+                const bool edge = base + (kKeys - 1) >= ctx || base < seen_by_all || bad_pages;
+                if (__builtin_expect(edge && (base + (kKeys - 1) >= ctx || base < seen_by_all), 0)) {
                     // Clean V: rows that no row sees are zeroed (past the sequence, before the
                     // window), partly seen ones lose and note what is not finite.
                     const int s = t % C::STAGES;

@@ -207,3 +207,38 @@ def test_a_captured_step_of_trees_and_commit_replays():
         assert new.tolist() == lens
         assert all(torch.equal(g.cpu().view(torch.uint8), w.view(torch.uint8)) for g, w in zip(pools, want))
     assert pa.device_status() == 0
+
+
+# ---- the longest table ----------------------------------------------------------------------
+
+def test_a_tree_behind_as_many_tokens_as_a_table_can_hold():
+    """2^31 - 16 tokens in 2^27 - 1 pages, three pages over and over: the softmax over their 48 rows,
+    weighted by how often each comes.  A CTA adds up 2^25 / 304 tiles in four products each, in fp32, each
+    sum off by at most one step (2^-23); the sum of the weights, over two adds a tile and thread, by
+    half as much: 0.053 + 0.027 of sum p |v|."""
+    n_pages, nodes = (1 << 27) - 1, 3
+    n = n_pages * 16
+    c = T.make([48], [nodes], 2, 1, 64, seed=80)
+    pages = c["table"][0, :3].clone()
+    order = torch.arange(n_pages, dtype=torch.int32, device=DEV).remainder_(3)
+    c = T.gpu(c)
+    small = c["table"][0, :3].cpu().long()
+    c["table"] = pages.to(DEV)[order.long()].view(1, -1).contiguous()
+    c["lens"] = torch.tensor([n], dtype=torch.int32, device=DEV)
+    got = T.call(c)
+    assert pa.device_status() == 0
+    last = (n_pages - 1) % 3
+    times = torch.tensor([[(n_pages - p + 2) // 3] for p in range(3)], dtype=torch.float64).expand(3, 16).clone()
+    times[last, 13:] -= 1                               # the nodes: rows 13 to 15 of the last page
+    k, v = (c[x].cpu().double()[small, 0].flatten(0, 1) for x in ("k", "v"))
+    out, bound = torch.zeros(nodes, 2, 64, dtype=torch.float64), torch.zeros(nodes, 2, 64, dtype=torch.float64)
+    for i in range(nodes):
+        w = times.clone()
+        for j in ref64.mask_bits(c["mask"][i].cpu(), nodes):
+            w[last, 13 + j] += 1
+        for h in range(2):
+            x = c["q"][i, h].cpu().double() @ k.T * c["scale"]
+            p = torch.exp(x - x.max()) * w.flatten()
+            p /= p.sum()
+            out[i, h], bound[i, h] = p @ v, p @ v.abs()
+    ref64.assert_attention(got, out, bound, extra=0.08)
