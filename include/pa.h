@@ -425,10 +425,10 @@ int pa_select_pages(int32_t *page_tables, int32_t *page_lens, const void *q, con
 /*
  * pa_decode_pages -- the split decode with one page list per (sequence, kv head): the
  * query heads of kv head kh attend over the page_lens[b] tokens of the pages
- * page_tables[b][kh], as pa_decode_split over a block table does (wide groups at head_dim
- * 64 and 256 run on the tree kernel, whose roundings differ from that call's).  Takes
- * what pa_select_pages writes, or any lists whose pages are full but the last; an empty
- * one gives zeros.
+ * page_tables[b][kh], as pa_decode_split over a block table does.  Wide groups at head_dim 64
+ * and 256 run on the tree kernel, whose roundings differ from that call's, where num_seqs,
+ * num_kv_heads and max_pages multiply to enough reading.  Takes what pa_select_pages writes,
+ * or any lists whose pages are full but the last; an empty one gives zeros.
  * workspace: pa_decode_split_workspace_size(num_seqs, num_q_heads, head_dim,
  * max_pages * block_size) bytes, 256-byte aligned.
  */

@@ -1333,15 +1333,34 @@ cudaError_t launch_tree_decode(const TreeParams &p, int head_dim, cudaStream_t s
 }
 
 // A page list is a tree of one node, the list's last key, whose other keys are its context.
-// The tree kernel takes the calls that the split decode has no tensor-core kernel for and enough
-// query heads to pay (8 sequences, 8 kv heads, 128 pages; split decode against this one, us: head_dim
-// 256 with 2 / 4 / 8 / 16 query heads a kv head 30 / 42 / 111 / 212 against 36, FP8 28 / 40 / 153 / 293
-// against 42; head_dim 64 with 8 / 12 / 16: 17 / 24 / 26 against 19, FP8 with 4 / 8 / 16: 15 / 29 / 52
-// against 21).
+// The split decode has no tensor-core kernel for head_dim 256, nor at head_dim 64 for groups above 8
+// (over FP8 for any), and walks a list once per sub-group of query heads that it has a kernel for, a
+// CTA for every 32 pages.  The tree kernel walks it once, but a list is a chain of tiles to it: about
+// 20 us (35 at head_dim 256) for lists of more than 32 pages, down to half of that for short ones,
+// however few there are.  So it takes the calls whose CTAs the split decode would need more than a
+// wave or two of, half as many where lists are short.
+// Measured, split decode / this, us (sequences x kv heads x pages of a list):
+//   head_dim 256, group 3: 1 x 8 x 128 14 / 29, 4 x 8 x 64 24 / 34, 8 x 8 x 64 34 / 35, 16 x 8 x 64 62 / 36,
+//     8 x 8 x 8 12 / 13, 32 x 8 x 8 25 / 19; group 4: 22 / 29, 22 / 35, 24 / 35, 41 / 35, 13 / 13, 23 / 19;
+//     7: 24 / 29, 33 / 34, 61 / 35, 116 / 36, 15 / 13, 45 / 19; 8: 56 / 28, 56 / 34, 58 / 35, 111 / 35, 27 / 13, 51 / 19
+//     (FP8 group 4: 21 / 27, 21 / 28, 22 / 29, 39 / 29, 12 / 11, 20 / 20; 8: 74 / 27, 74 / 28, 78 / 29, 151 / 29, 31 / 12, 62 / 20)
+//   head_dim 64, group 9: 11 / 20, 14 / 22, 18 / 22, 30 / 23, 10 / 10, 20 / 10;
+//     11: 18 / 20, 26 / 22, 42 / 22, 78 / 23, 12 / 10, 32 / 10; 16: 12 / 19, 12 / 22, 17 / 22, 28 / 23, 9 / 10, 20 / 10
+//     (FP8 group 3: 11 / 24, 11 / 23, 18 / 23, 27 / 24, 7 / 9, 12 / 10; 5: 11 / 23, 18 / 23, 26 / 23, 41 / 24, 9 / 9, 18 / 10;
+//     8: 16 / 21, 16 / 23, 16 / 23, 28 / 24, 9 / 9, 15 / 10; 4, on the split decode: 41 / 41 at 32 x 8 x 128)
 bool page_lists_on_tree(const DecodeParams &p, int head_dim) {
     const int group = p.num_q_heads / p.num_kv_heads;
-    const bool sizes = head_dim == 256 ? group >= 4 : head_dim == 64 && group > (p.kv_fp8 ? 4 : 8);
-    return sizes && p.scale_log2 > 0.f && p.scale_log2 < INFINITY && p.num_blocks < INT32_MAX;
+    if (head_dim == 256 ? group < 3 : head_dim != 64 || (p.kv_fp8 ? group < 3 || group == 4 : group <= 8)) return false;
+    int sub = 0;                                  // the split decode's sub-groups: on the tensor cores ...
+    for (int g = 8; head_dim == 64 && !p.kv_fp8 && g >= 3 && !sub; --g)
+        if (group % g == 0) sub = g;
+    const bool tensor = sub > 0;
+    for (int g = 8; !sub; g /= 2)                 // ... or not
+        if (group % g == 0) sub = g;
+    const int64_t ctas = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * (group / sub) * ((p.max_blocks + 31) / 32);
+    int border = head_dim == 256 ? (sub == 8 ? 0 : sub == 4 ? 160 : 320) : tensor ? 320 : sub == 8 ? 160 : 640;
+    if (p.max_blocks <= 32) border /= 2;
+    return ctas >= border && p.scale_log2 > 0.f && p.scale_log2 < INFINITY && p.num_blocks < INT32_MAX;
 }
 
 cudaError_t launch_page_lists(const DecodeParams &d, int head_dim, void *workspace, size_t workspace_bytes,

@@ -1,6 +1,6 @@
 """Edges of the tree and page-selection calls: lengths and page ids out of range where nothing is
 ranked, bounds of pages that are never ranked, query groups split over several kernel groups, padded
-pools, captured commits, tables of 2^27 pages."""
+pools, captured commits, tables of 2^27 pages, which kernel takes page lists."""
 import math
 
 import pytest
@@ -8,6 +8,7 @@ import torch
 
 import paged_kv_gqa_15_gb300 as pa
 from tests import ref64
+from tests import test_fp8_trees_gpu as F
 from tests import test_pages_gpu as P
 from tests import test_tree_gpu as T
 
@@ -125,6 +126,45 @@ def test_page_lists_of_split_groups(nq, nkv, hd, fp8):
     out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages.cpu(), lens.cpu(), c["scale"], "HND", c["kv_scale"],
                                     c["kv_scale"])
     ref64.assert_attention(P.decode(c, pages, lens), out, bound, P.FP8_EXTRA if fp8 else 0.0)
+    assert pa.device_status() == 0
+
+
+# ---- which kernel takes page lists ----------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,nkv,hd", [(4, 1, 256), (6, 1, 256), (14, 2, 256), (24, 2, 256), (9, 1, 64), (24, 2, 64),
+                                       (16, 1, 64)])
+def test_few_pages_are_the_split_decode_for_wide_groups_too(nq, nkv, hd, fp8):
+    """The tree kernel takes longer there (a list is a chain of tiles), so all pages of short sequences
+    give the split decode's bits."""
+    c = P.make([900, 40, 477], nq, nkv, hd, 81, fp8)
+    P.fill_bounds(c)
+    pages, lens = P.select(c, 57, 0, 1)
+    ws = pa.alloc_workspace(pa.decode_split_workspace_size(3, nq, hd, 57 * 16), DEV)
+    want = torch.empty_like(c["q"])
+    pa.pa_decode_split(want, c["q"], c["k"], c["v"], c["table"], c["lens"], c["scale"], 57 * 16, ws, k_scale=c["kv_scale"],
+                       v_scale=c["kv_scale"])
+    assert torch.equal(P.decode(c, pages, lens), want)
+    assert pa.device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,nkv,hd,seqs,most", [(9, 1, 64, 24, 290), (24, 2, 64, 18, 190), (11, 1, 64, 3, 640), (3, 1, 64, 30, 230),
+                                                 (16, 2, 256, 3, 70), (3, 1, 256, 20, 180), (10, 2, 256, 12, 70),
+                                                 (12, 3, 256, 9, 190), (9, 1, 64, 60, 8), (12, 2, 256, 30, 31)])
+def test_many_pages_of_wide_groups(nq, nkv, hd, seqs, most, fp8):
+    """Enough reading for the tree kernel, in whole and in cut runs; every kv head's list is its own."""
+    lens = [most * 16 + 700 - 37 * (i % 19) for i in range(seqs - 2)] + [0, 33]
+    c = P.make(lens, nq, nkv, hd, 82, fp8)
+    gen = torch.Generator().manual_seed(5)
+    pages = torch.stack([torch.stack([torch.randperm(c["k"].shape[0] - 3, generator=gen)[:most] for _ in range(nkv)])
+                         for _ in lens]).int()
+    c["k"], c["v"] = (x.float().nan_to_num(0.0).to(x.dtype) for x in (c["k"], c["v"]))
+    kept = torch.tensor([min(n, most * 16 - 5 * (i % 4)) for i, n in enumerate(lens)], dtype=torch.int32)
+    got = P.decode(c, pages.to(DEV), kept.to(DEV))
+    out, bound = ref64.decode_pages(c["q"], c["k"], c["v"], pages, kept, c["scale"], "HND", c["kv_scale"], c["kv_scale"])
+    ref64.assert_attention(got, out, bound, F.extra(c["q"], c["k"], c["scale"], c["kv_scale"], most * 16) if fp8 else 0.0)
+    assert bool((got[-2] == 0).all()) and torch.equal(P.decode(c, pages.to(DEV), kept.to(DEV)), got)
     assert pa.device_status() == 0
 
 
