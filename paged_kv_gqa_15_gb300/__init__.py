@@ -454,7 +454,7 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
         assert values.count(values[0]) == n, "pools differ in geometry"
     seqs, blocks = block_tables.shape
     paths, most = accepted.shape
-    assert accepted.dtype is _INT32 and accepted.is_contiguous() and paths == seqs, \
+    assert accepted.dtype is _INT32 and accepted.is_contiguous() and paths >= seqs, \
         "accepted must be a dense int32 tensor with a row per sequence"
     _check_int32(seqs, block_tables, seq_lens, accept_lens, new_seq_lens)
     _check_int32(seqs + 1, qo_indptr)
@@ -496,11 +496,11 @@ def pa_select_pages(page_tables, page_lens, q, bounds, block_tables, seq_lens, w
     """Chooses up to max_pages pages per (sequence, kv head) for the queries q [B, nq, hd] by the
     pages' key bounds, into page_tables [B, nkv, max_pages] and page_lens [B] (int32); the
     first sink_pages and the last recent_pages are always among them."""
-    nb, nkv, _, hd = bounds.shape
+    nb, nkv, two, hd = bounds.shape
     B, nq, qd = q.shape
     rows, heads, most = page_tables.shape
     blocks = block_tables.shape[1]
-    assert bounds.is_contiguous(), "bounds must be dense"
+    assert bounds.is_contiguous() and two == 2, "bounds must be dense, [num_blocks, nkv, 2, hd]"
     assert q.dtype is _BF16 and q.is_contiguous() and qd == hd, \
         "q must be a dense bf16 tensor with the bounds' head_dim"
     assert rows == B and heads == nkv, "page_tables must be [B, nkv, max_pages]"

@@ -157,6 +157,7 @@ def test_one_host_tensor_among_device_tensors(call, monkeypatch):
     (select, dict(q=rows(B).half()), "q must"),
     (select, dict(q=torch.zeros((B, NQ, 128), dtype=torch.bfloat16)), "q must"),
     (select, dict(bounds=wide(torch.zeros((NB, NKV, 2, HD), dtype=torch.bfloat16))), "bounds"),
+    (select, dict(bounds=torch.zeros((NB, NKV, 1, HD), dtype=torch.bfloat16)), "bounds"),
     (select, dict(block_tables=wide(i32(B, 4))), "int32"),
     (select, dict(block_tables=i32(B - 1, 4)), "int32"),
     (select, dict(seq_lens=i32(B).long()), "int32"),
@@ -191,6 +192,7 @@ def test_operands_the_kernels_would_misread(call, kw, what):
     (tree, dict(k_cache=wide(pool()), v_cache=wide(pool()))),                    # padded pools
     (tree, dict(seq_lens=i32(B + 5), qo_indptr=i32(B + 6))),                     # buffers of a larger batch
     (commit, dict(key_caches=[wide(pool())], value_caches=[wide(pool())])),
+    (commit, dict(accepted=i32(B + 4, 2), accept_lens=i32(B + 4), new_seq_lens=i32(B + 4))),
     (bounds, dict(first_tokens=None)),
     (bounds, dict(k_cache=pool(torch.uint8), bounds=torch.zeros((NB, NKV, 2, HD), dtype=torch.float8_e4m3fn))),
     (pages, dict(k_cache=pool(torch.uint8), v_cache=pool(torch.uint8).view(torch.float8_e4m3fn))),
