@@ -317,6 +317,8 @@ size_t pa_tree_decode_workspace_size(int num_seqs, int max_tree_len, int num_q_h
  *   - the nodes j < T_b whose bit is set in its mask row: bit j % 64 of word
  *     tree_mask[row][j / 64].  A node sees itself only if its own bit is set; any
  *     mask is allowed, not only those of trees, and bits at or past T_b are ignored.
+ *     The window hides no node: for a path longer than it, clear the bits of the ancestors
+ *     that have left it (n_i is then sliding_window, and no context token is seen).
  * A row that sees nothing is written as zeros.  Nodes it does not see and tokens past
  * seq_lens[b] contribute nothing, whatever their K/V rows hold (NaN included).
  *   out, q        [total_rows][num_q_heads][head_dim] bf16; rows outside
@@ -384,8 +386,10 @@ int pa_tree_commit(void *const *pools, int num_pools, const int32_t *block_table
  *   bounds          [num_blocks][num_kv_heads][2][head_dim] of the pool's type (FP8
  *                   pools: E4M3 codes, without k_scale)
  *   max_new_tokens  >= seq_lens[b] - first_tokens[b] for every b (>= seq_lens[b] when
- *                   first_tokens is NULL); bounds the launch.  Tokens beyond it are not
- *                   covered and set PA_ERR_DEVICE_BOUNDS.
+ *                   first_tokens is NULL); bounds the launch: pages beyond those that so
+ *                   many tokens can touch are not rewritten and set PA_ERR_DEVICE_BOUNDS (0:
+ *                   the call does nothing).  Pages x num_kv_heads of a sequence that pass
+ *                   2^31 are refused with PA_ERR_UNSUPPORTED.
  * A page that two sequences share must have the same rows in both.
  */
 int pa_page_bounds(void *bounds, const void *k_cache, const int32_t *block_tables,

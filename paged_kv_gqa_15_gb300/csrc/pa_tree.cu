@@ -13,9 +13,11 @@
 //    one kv head, loaded by one TMA box (64 columns, g heads, 128 / g nodes).  A tree with
 //    more rows takes several row tiles, worked on side by side where that pays (TreeShares).
 //  * The work is a line of key tiles: for every (sequence, kv head, row tile) its 64-key
-//    tiles, one after another.  CTA c of n takes an equal share of that line, whatever the
-//    lengths: no list is sorted, no counter claimed, and no CTA has more than one tile more
-//    than another.  A share is a run of segments; a segment that holds all tiles of its
+//    tiles, one after another.  CTA c of n takes an equal share of that line (one tile more at
+//    most), whatever the lengths: no list is sorted and no counter claimed.  Where runs are short
+//    against a share, the cuts move to the nearest run boundaries (a share is then up to a run
+//    longer than another); where row tiles go side by side (TreeShares), CTAs whose sequence has
+//    no such row tile are idle.  A share is a run of segments; a segment that holds all tiles of its
 //    (sequence, kv head, row tile) writes the output, the others (at most two per CTA: its
 //    first and its last) write fp32 partial rows that a second kernel joins in a fixed order,
 //    so results do not depend on timing.
@@ -33,8 +35,10 @@
 //    noted, to be added in the epilogue to the rows that do see them.
 //  * 8-bit caches (FP8): K and V tiles go to the 8-bit tensor cores as they are, and MMAs with
 //    the same B operand add up the terms of the other.  q is split into two E4M3 rows, q s =
-//    hi + lo with s a power of two that puts the row's largest |q s| in [128, 256): the pair
-//    holds q to 2^-8 of its value.  P is split into three E5M2 terms: an f16 value's upper byte
+//    hi + lo with s a power of two that puts the row's largest |q s| in [128, 256).  hi takes the
+//    four leading bits of bf16's eight and lo the others, so the pair is exact where |q s| >= 2^-2;
+//    below, E4M3's smallest step leaves up to 2^-10: 2^-17 of the row's largest |q| (a channel
+//    2^13 times the others leaves them a few bits).  P is split into three E5M2 terms: an f16 value's upper byte
 //    is an E5M2 value, so each term is a mask and a subtraction and four of them one byte
 //    permutation.  Three terms hold at least 9 bits, rounded (2^-9 of P, mostly better), over f16's
 //    range.
@@ -45,7 +49,7 @@
 //  * Every mbarrier wait is bounded.
 // Measured: 8 sequences of 32k-131k tokens, 24 nodes, 32 / 8 heads, bf16: 338 us for 2236 MB, 97 % of
 // the measured copy rate; 16 of 512-4096 tokens, 16 nodes: 36 us for 130 MB, start and join
-// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 157 us for 75 GFLOP, bound by the latency of
+// included; 32 of 1k-8k over an FP8 cache, 64 nodes: 160 us for 75 GFLOP, bound by the latency of
 // the softmax of 256 rows (tensor pipe 36 % busy, issue slots 37 %) between five MMA terms.
 #include <algorithm>
 #include <atomic>
@@ -947,7 +951,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<HD, FP8>::CTAS_PER_SM)
                         l *= corr;
                         m = m_new;
                     }
-                    // P = 2^(s scale - m + lift); the sum takes the unrounded values
+                    // P = 2^(s scale - m + lift).  The sum takes the fp32 values, P goes to the MMA as bf16,
+                    // the type of the tile it multiplies: nearest, so off by 2^-9 of a weight on average
+                    // and either way (outputs 2.3e-3 from 64 bits in relative norm, 1.7e-3 of it their own
+                    // rounding to bf16).
                     const float sub = m == -INFINITY ? 0.f : m - lift;
                     constexpr int P_WORDS = FP8 ? 48 : 32;
                     uint32_t pk[P_WORDS];
