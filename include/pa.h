@@ -29,6 +29,12 @@
  *                       per-page bounds of the keys rank highest for the step's
  *                       query, chosen per sequence and kv head (no page defines
  *                       them)
+ *   pa_rope, pa_rope_append  rotary positions of q and k, alone and on k's way into
+ *                       the cache; pa_rope_table makes their frequencies (no page
+ *                       defines them)
+ *   pa_beam_select, pa_beam_reorder  beam search: the best continuations over beams
+ *                       and vocabulary, and the cache following the chosen beams (no
+ *                       page defines them)
  *   pa_block_table_sync upload of the changed rows of a block table, for
  *                       CUDA-graph replays of the decode ("libmir-cuda
  *                       attention/mod.rs", captured decode nodes)
@@ -443,6 +449,153 @@ int pa_decode_pages(void *out, const void *q, const void *k_cache, const void *v
                     int64_t stride_head, int64_t stride_token, float sm_scale, int kv_dtype,
                     float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
                     void *stream);
+
+/*
+ * Rotary positions.  The token at position P turns its channels pair by pair: pair i of
+ * R / 2 (R = rotary_dim) by the angle a = P * f_i,
+ *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a),
+ * where (x1, x2) are channels (i, i + R / 2), or (2 i, 2 i + 1) if interleaved != 0, and m
+ * is the attention factor.  Channels from R on pass unchanged.  The angle is held to 2^-24
+ * of a half turn at positions up to 2^31, products and sums are fp32, each result is
+ * rounded once.
+ *
+ * Frequencies come as a table of rotary_dim / 2 numbers made once per model on the HOST
+ * and copied to the device: entry i is the fraction of a turn per position, in units of
+ * 2^-64.
+ *
+ * pa_rope_table writes the table and the attention factor of f_i = base^(-2 i / R) under a
+ * scaling for long contexts by factor s:
+ *   PA_ROPE_NONE    f_i
+ *   PA_ROPE_LINEAR  f_i / s (positions interpolated)
+ *   PA_ROPE_NTK     base * s^(R / (R - 2)) in place of base
+ *   PA_ROPE_BANDS   by the turns t = original_len * f_i / 2 pi a pair makes in the original
+ *                   context: f_i / s below `low` turns, f_i above `high`, between them
+ *                   f_i ((1 - r) / s + r) with r = (t - low) / (high - low) (usual: 1, 4)
+ *   PA_ROPE_YARN    f_i (r / s + 1 - r), r rising from 0 to 1 between the pair numbers
+ *                   floor(n(high)) and ceil(n(low)), where n(t) = R ln(original_len /
+ *                   (2 pi t)) / (2 ln base), cut to [0, R - 1] (usual: low 1, high 32);
+ *                   attention factor 0.1 ln s + 1 for s > 1
+ * (attention factor 1 for the others).  factor, low, high and original_len are read by the
+ * scalings that name them.  pa_rope_table_of takes any other frequencies, in radians per
+ * position.
+ *   turns_h  [rotary_dim / 2] HOST; attention_factor_h HOST, may be NULL
+ */
+typedef enum {
+    PA_ROPE_NONE = 0,
+    PA_ROPE_LINEAR = 1,
+    PA_ROPE_NTK = 2,
+    PA_ROPE_BANDS = 3,
+    PA_ROPE_YARN = 4
+} pa_rope_scaling;
+int pa_rope_table(uint64_t *turns_h, float *attention_factor_h, int rotary_dim, double base,
+                  int scaling, double factor, double low, double high, int64_t original_len);
+int pa_rope_table_of(uint64_t *turns_h, const double *frequencies_h, int num_pairs);
+
+/*
+ * pa_rope -- q and k of num_tokens tokens, turned to their positions.
+ *   q, k          [num_tokens][heads][head_dim] bf16 by element strides (token, head), each
+ *                 a multiple of 16 bytes; head_dim contiguous.  0 heads: not touched.
+ *   q_out, k_out  the same shape by strides of their own; q_out may be q and k_out k with
+ *                 the same strides (in place), else outputs share no memory with inputs
+ *   positions     [num_tokens] int64, any value (negative ones turn back)
+ *   turns         [rotary_dim / 2], device, from pa_rope_table
+ *   inverse       != 0: by -a.  That is the gradient of the call with inverse == 0 (the
+ *                 transposed map), and takes its rotation back where m is 1.
+ * head_dim in {64, 128, 256}, rotary_dim even, at most head_dim.
+ */
+int pa_rope(void *q_out, void *k_out, const void *q, const void *k, const int64_t *positions,
+            const uint64_t *turns, int64_t num_tokens, int num_q_heads, int num_k_heads,
+            int head_dim, int rotary_dim, int64_t q_out_stride_token, int64_t q_out_stride_head,
+            int64_t k_out_stride_token, int64_t k_out_stride_head, int64_t q_stride_token,
+            int64_t q_stride_head, int64_t k_stride_token, int64_t k_stride_head,
+            int interleaved, int inverse, float attention_factor, void *stream);
+
+/*
+ * pa_rope_append -- pa_rope and pa_write_cache in one pass: q turned into q_out, k turned
+ * into the cache at slot_mapping, v into the cache as it is.  An FP8 pool takes the E4M3
+ * codes of the turned fp32 values (k_scale, v_scale as in pa_write_cache).
+ *   q, k, v, q_out  as in pa_rope (num_q_heads may be 0; k, v share num_kv_heads)
+ *   slot_mapping    [num_tokens] int64; a token whose slot is negative is padding: nothing of
+ *                   it is written, its row of q_out included.  A slot outside the pool is
+ *                   treated the same and sets PA_ERR_DEVICE_BOUNDS.
+ */
+int pa_rope_append(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                   void *v_cache, const int64_t *slot_mapping, const int64_t *positions,
+                   const uint64_t *turns, int64_t num_tokens, int num_q_heads,
+                   int num_kv_heads, int head_dim, int rotary_dim, int block_size,
+                   int64_t num_blocks, int64_t q_out_stride_token, int64_t q_out_stride_head,
+                   int64_t q_stride_token, int64_t q_stride_head, int64_t k_stride_token,
+                   int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,
+                   int64_t stride_block, int64_t stride_head, int64_t stride_token,
+                   int interleaved, float attention_factor, int kv_dtype, float k_scale,
+                   float v_scale, void *stream);
+
+/*
+ * Beam search.  A request has num_beams beams, each a sequence of its own in the cache:
+ * sequence r * num_beams + b.  A step runs the model on every beam's newest token, chooses
+ * the best continuations (pa_beam_select) and lets the cache follow them
+ * (pa_beam_reorder with parents = the chosen beams).
+ */
+#define PA_MAX_BEAMS 32          /* num_beams */
+#define PA_MAX_BEAM_OUT 64       /* num_out */
+#define PA_MAX_BEAM_VOCAB (1 << 24)
+typedef enum { PA_LOGITS_F32 = 0, PA_LOGITS_BF16 = 1 } pa_logits_dtype;
+
+/* Bytes of workspace pa_beam_select needs (256-byte aligned; nothing in it has to be
+ * initialised, and no call leaves anything in it for the next). */
+size_t pa_beam_select_workspace_size(int num_requests, int num_beams, int vocab);
+
+/*
+ * pa_beam_select -- for every request the num_out best of all pairs (beam b, token t) by
+ *   score = cum_scores[r][b] + x_t - log sum_u exp x_u,   x the beam's row of logits,
+ * best first; equal scores go to the lower beam, then to the lower token.  Scores are
+ * compared as sums of two fp32; a row's log-sum-exp is known to 2^-20, so pairs of two beams whose
+ * scores are closer than that may come in either order.  Equal rows have equal sums.
+ *   logits      [num_requests * num_beams] rows of vocab values of logits_dtype, stride_row
+ *               elements apart (rows of any alignment; multiples of 16 bytes are faster).
+ *               -inf rules a token out.
+ *   cum_scores  [num_requests][num_beams] fp32.  -inf takes a beam out: its logits are not
+ *               read (a first step has one beam at 0 and the others at -inf).
+ *   finished    [num_requests][num_beams] bytes, or NULL.  A beam with a nonzero flag offers
+ *               one pair, end_token at the score cum_scores; its logits are not read.
+ *   scores      [num_requests][num_out] fp32, beams and tokens [num_requests][num_out] int32,
+ *               written whole: behind the pairs there are, -inf, -1 and -1.  A pair whose
+ *               score rounds to -inf is none.
+ * A beam whose logits hold NaN or +inf, or whose cum_scores is one of them, offers nothing
+ * and sets the PA_ERR_INVALID bit of the device status word.  The outputs share no memory
+ * with what the call reads or one another.
+ */
+int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, const void *logits,
+                   const float *cum_scores, const uint8_t *finished, int end_token,
+                   int num_requests, int num_beams, int vocab, int num_out,
+                   int64_t stride_row, int logits_dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * pa_beam_reorder -- the cache follows the chosen beams: sequence j of each request goes on
+ * from what sequence p = parents[r][j] held, in every one of the pools.  With L its length,
+ *   - its block-table row takes p's ids of the full pages (the first L / block_size): full
+ *     pages are shared, not copied;
+ *   - the L % block_size rows of the page that its next token goes to become p's rows, bit
+ *     for bit.  That page, block_tables[j][L / block_size], must be named by no other
+ *     sequence; the entry stays.
+ * All sequences move at once: p's rows and ids are those before the call.  parents < 0 (-1)
+ * or the sequence itself leaves it as it is.  After a prompt whose pages the beams share,
+ * parents 0 and a page of its own at L / block_size make each beam's copy of the last one.
+ *   pools         HOST array of num_pools device pointers, as in pa_tree_commit
+ *   block_tables  [num_requests * num_beams][max_blocks_per_seq], changed in place
+ *   seq_lens      [num_requests * num_beams]; parents [num_requests][num_beams] int32
+ * A sequence is left as it is and PA_ERR_DEVICE_BOUNDS set where its parent is no beam of
+ * the request or has another length, the length is negative or passes the table, or (unless L %
+ * block_size is 0) its own or its parent's page is not in the pool or its own is another
+ * beam's too.  Pages that no sequence names any more are the caller's to find.  One launch
+ * per 128 pools.
+ */
+int pa_beam_reorder(void *const *pools, int num_pools, int32_t *block_tables,
+                    const int32_t *seq_lens, const int32_t *parents, int num_requests,
+                    int num_beams, int num_kv_heads, int head_dim, int block_size,
+                    int max_blocks_per_seq, int64_t num_blocks, int64_t stride_block,
+                    int64_t stride_head, int64_t stride_token, int kv_dtype, void *stream);
 
 /*
  * Block-table upload for CUDA-graph replays ("libmir-cuda attention/mod.rs",

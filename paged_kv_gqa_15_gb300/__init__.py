@@ -81,10 +81,22 @@ def load():
     lib.pa_select_pages_workspace_size.argtypes = [I, I, I]
     lib.pa_select_pages_workspace_size.restype = Z
     lib.pa_select_pages.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, L, I, I, I, I, P, Z, P]
+    D = ctypes.c_double
+    lib.pa_rope_table.argtypes = [P, P, I, D, I, D, D, D, L]
+    lib.pa_rope_table_of.argtypes = [P, P, I]
+    lib.pa_rope.argtypes = [P, P, P, P, P, P, L, I, I, I, I, L, L, L, L, L, L, L, L, I, I, F, P]
+    lib.pa_rope_append.argtypes = [P, P, P, P, P, P, P, P, P, L, I, I, I, I, I, L, L, L, L, L, L, L, L,
+                                   L, L, L, L, I, F, I, F, F, P]
+    lib.pa_beam_select_workspace_size.argtypes = [I, I, I]
+    lib.pa_beam_select_workspace_size.restype = Z
+    lib.pa_beam_select.argtypes = [P, P, P, P, P, P, I, I, I, I, I, L, I, P, Z, P]
+    lib.pa_beam_reorder.argtypes = [P, I, P, P, P, I, I, I, I, I, I, L, L, L, L, I, P]
     lib.pa_last_error.restype = ctypes.c_char_p
     for name in ("pa_write_cache", "pa_decode", "pa_decode_split", "pa_decode_partitions",
                  "pa_decode_merge", "pa_ragged_prefill", "pa_decode_pages", "pa_tree_decode",
-                 "pa_tree_commit", "pa_page_bounds", "pa_select_pages",
+                 "pa_tree_commit", "pa_page_bounds", "pa_select_pages", "pa_rope_table",
+                 "pa_rope_table_of", "pa_rope", "pa_rope_append", "pa_beam_select",
+                 "pa_beam_reorder",
                  "pa_get_device_status"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -435,16 +447,12 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, 
                                  float(v_scale), ws, workspace.numel(), _stream(stream, device)))
 
 
-def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, accepted,
-                   accept_lens, new_seq_lens, max_tree_len, layout="HND", stream=None):
-    """Moves the K/V rows of each sequence's accepted nodes (accepted int32 [B, n], ascending,
-    accept_lens[b] of them) behind its context in every layer's pools, and writes the
-    sequences' new lengths into new_seq_lens (not seq_lens itself).  Layers that share a cache
-    list it once."""
-    assert len(key_caches) == len(value_caches) > 0
+def _all_pools(key_caches, value_caches, layout):
+    """The pools [k_0, v_0, k_1, ...] of all layers, of one geometry, and that geometry:
+    (num_blocks, kv heads, block size, head_dim), strides of a block, head and token."""
+    assert len(key_caches) == len(value_caches) > 0, "every layer has a key and a value pool"
     pools = [t for kv in zip(key_caches, value_caches) for t in kv]
-    nb, nkv, bs, hd = _pool_geometry(pools[0], layout)
-    sb, sh, st = pool_strides(pools[0], layout)
+    geometry = _pool_geometry(pools[0], layout), pool_strides(pools[0], layout)
     # a model has two pools a layer, so the checks go over whole lists
     n = len(pools)
     layouts = list(map(torch.Tensor.is_contiguous, pools))   # contiguous ones need no strides
@@ -452,6 +460,16 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
         layouts = list(map(torch.Tensor.stride, pools))
     for values in ([t.shape for t in pools], layouts, [t.dtype for t in pools]):
         assert values.count(values[0]) == n, "pools differ in geometry"
+    return pools, *geometry
+
+
+def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, accepted,
+                   accept_lens, new_seq_lens, max_tree_len, layout="HND", stream=None):
+    """Moves the K/V rows of each sequence's accepted nodes (accepted int32 [B, n], ascending,
+    accept_lens[b] of them) behind its context in every layer's pools, and writes the
+    sequences' new lengths into new_seq_lens (not seq_lens itself).  Layers that share a cache
+    list it once."""
+    pools, (nb, nkv, bs, hd), (sb, sh, st) = _all_pools(key_caches, value_caches, layout)
     seqs, blocks = block_tables.shape
     paths, most = accepted.shape
     assert accepted.dtype is _INT32 and accepted.is_contiguous() and paths >= seqs, \
@@ -461,7 +479,7 @@ def pa_tree_commit(key_caches, value_caches, block_tables, seq_lens, qo_indptr, 
     device, tables, lens, indptr, path, kept, new, *at = _addresses(
         block_tables, seq_lens, qo_indptr, accepted, accept_lens, new_seq_lens, *pools)
     at = array.array("Q", at)
-    _check(load().pa_tree_commit(at.buffer_info()[0], n, tables, lens, indptr, path, kept, new,
+    _check(load().pa_tree_commit(at.buffer_info()[0], len(pools), tables, lens, indptr, path, kept, new,
                                  seqs, int(max_tree_len), most, nkv, hd, bs, blocks, nb, sb, sh,
                                  st, kv_dtype_of(pools[0]), _stream(stream, device)))
 
@@ -531,6 +549,163 @@ def pa_decode_pages(out, q, k_cache, v_cache, page_tables, page_lens, sm_scale, 
     _check(load().pa_decode_pages(o, q, k, v, tables, lens, B, nq, nkv, hd, bs, most, nb, sb, sh,
                                   st, float(sm_scale), kind, float(k_scale), float(v_scale), ws,
                                   workspace.numel(), _stream(stream, device)))
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}   # pa_rope_scaling
+_LOW_HIGH = {"bands": (1.0, 4.0), "yarn": (1.0, 32.0)}
+
+
+def rope_table(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, low=None,
+               high=None, device="cuda"):
+    """(turns, attention_factor) of the frequencies base^(-2 i / rotary_dim) under a scaling of
+    ROPE_SCALINGS for long contexts: the int64 device table that pa_rope and pa_rope_append take,
+    and the factor for their attention_factor.  low and high default to the usual 1 and 4 turns
+    ("bands") or 1 and 32 ("yarn")."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is none of {sorted(ROPE_SCALINGS)}")
+    usual = _LOW_HIGH.get(scaling, (1.0, 4.0))
+    turns = torch.empty(max(0, int(rotary_dim) // 2), dtype=torch.int64)
+    m = ctypes.c_float(1.0)
+    _check(load().pa_rope_table(turns.data_ptr(), ctypes.addressof(m), int(rotary_dim), float(base),
+                                ROPE_SCALINGS[scaling], float(factor),
+                                float(usual[0] if low is None else low),
+                                float(usual[1] if high is None else high), int(original_len)))
+    return turns.to(device), m.value
+
+
+def rope_table_of(frequencies, device="cuda"):
+    """The table of any other frequencies (radians per position, one per pair)."""
+    f = torch.as_tensor(frequencies, dtype=torch.float64).cpu().contiguous()
+    turns = torch.empty(f.numel(), dtype=torch.int64)
+    _check(load().pa_rope_table_of(turns.data_ptr(), f.data_ptr(), f.numel()))
+    return turns.to(device)
+
+
+_INT64 = torch.int64
+
+
+def _head_rows(x, tokens=None, head_dim=None):
+    """(tokens, heads, head_dim, strides of a token and a head) of x [tokens, heads, head_dim]."""
+    t, heads, hd = x.shape
+    st, sh, one = x.stride()
+    assert x.dtype is _BF16 and (one == 1 or x.numel() == 0) and t == (t if tokens is None else tokens) and \
+        hd == (hd if head_dim is None else head_dim), \
+        "q, k, v and their outputs must be bf16 [tokens, heads, head_dim] of one token count and " \
+        "head_dim, with a contiguous head_dim"
+    return t, heads, hd, st, sh
+
+
+def _check_int64(n, *arrays):
+    for t in arrays:
+        assert t.dtype is _INT64 and t.is_contiguous() and t.numel() == n, \
+            "positions, slots and frequencies must be dense int64 tensors, one entry a token or pair"
+
+
+def pa_rope(q_out, k_out, q, k, positions, turns, interleaved=False, attention_factor=1.0,
+            inverse=False, stream=None):
+    """q [T, nq, hd] and k [T, nk, hd] turned to positions [T] (int64) into q_out and k_out, which
+    may be q and k themselves; k and k_out may be None.  turns and attention_factor are those of
+    rope_table; the first 2 * len(turns) channels turn.  Slices of a fused projection are taken as
+    they are.  inverse: by the negated angles, the gradient of the call without it."""
+    t, nq, hd, qt, qh = _head_rows(q)
+    _, heads, _, qot, qoh = _head_rows(q_out, t, hd)
+    assert heads == nq and (k is None) == (k_out is None), "q_out must be like q, k_out like k"
+    nk = kt = kh = kot = koh = 0
+    more = ()
+    if k is not None:
+        _, nk, _, kt, kh = _head_rows(k, t, hd)
+        _, heads, _, kot, koh = _head_rows(k_out, t, hd)
+        assert heads == nk, "q_out must be like q, k_out like k"
+        more = (k_out, k)
+    _check_int64(t, positions)
+    _check_int64(turns.numel(), turns)
+    device, qo, qi, pos, table, *more = _addresses(q_out, q, positions, turns, *more)
+    ko, ki = more or (None, None)
+    _check(load().pa_rope(qo, ko, qi, ki, pos, table, t, nq, nk, hd, 2 * turns.numel(), qot, qoh, kot,
+                          koh, qt, qh, kt, kh, 1 if interleaved else 0, 1 if inverse else 0,
+                          float(attention_factor), _stream(stream, device)))
+
+
+def pa_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, turns, layout="HND",
+                   interleaved=False, attention_factor=1.0, stream=None, k_scale=1.0, v_scale=1.0):
+    """pa_rope and pa_write_cache in one pass: q [T, nq, hd] turned into q_out, k [T, nkv, hd]
+    turned into its slots of the cache, v into them as it is.  A token with a negative slot is
+    padding and leaves its row of q_out as it was.  q and q_out may be None."""
+    nb, nkv, bs, hd, sb, sh, st, kind = _kv_pools(k_cache, v_cache, layout)
+    t, heads, _, kt, kh = _head_rows(k, None, hd)
+    _, vheads, _, vt, vh = _head_rows(v, t, hd)
+    assert heads == vheads == nkv and (q is None) == (q_out is None), \
+        "k and v must have the pools' heads, q_out must be like q"
+    nq = qt = qh = qot = qoh = 0
+    more = ()
+    if q is not None:
+        _, nq, _, qt, qh = _head_rows(q, t, hd)
+        _, heads, _, qot, qoh = _head_rows(q_out, t, hd)
+        assert heads == nq, "k and v must have the pools' heads, q_out must be like q"
+        more = (q_out, q)
+    _check_int64(t, slot_mapping, positions)
+    _check_int64(turns.numel(), turns)
+    device, ki, vi, kc, vc, slots, pos, table, *more = _addresses(k, v, k_cache, v_cache, slot_mapping,
+                                                                  positions, turns, *more)
+    qo, qi = more or (None, None)
+    _check(load().pa_rope_append(qo, qi, ki, vi, kc, vc, slots, pos, table, t, nq, nkv, hd,
+                                 2 * turns.numel(), bs, nb, qot, qoh, qt, qh, kt, kh, vt, vh, sb, sh, st,
+                                 1 if interleaved else 0, float(attention_factor), kind, float(k_scale),
+                                 float(v_scale), _stream(stream, device)))
+
+
+def beam_select_workspace_size(num_requests, num_beams, vocab) -> int:
+    return int(load().pa_beam_select_workspace_size(num_requests, num_beams, vocab))
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1}   # pa_logits_dtype
+
+
+def pa_beam_select(scores, beams, tokens, logits, cum_scores, workspace, finished=None, end_token=0,
+                   stream=None):
+    """The best pairs of beam and token of each request by cum_scores + log_softmax(logits), best
+    first, into scores (float32), beams and tokens (int32), all [R, num_out].  logits [R * B, vocab]
+    (float32 or bfloat16, rows any stride apart), cum_scores [R, B] (-inf: not in the search),
+    finished [R, B] (uint8 or bool): those beams offer end_token at their score alone."""
+    requests, num_beams = cum_scores.shape
+    rows, vocab = logits.shape
+    outs, num_out = scores.shape
+    row_stride, one = logits.stride()
+    assert logits.dtype in _LOGITS and rows == requests * num_beams and (one == 1 or vocab == 1), \
+        "logits must be float32 or bfloat16 [requests * beams, vocab] with contiguous rows"
+    assert cum_scores.dtype is scores.dtype is torch.float32 and cum_scores.is_contiguous() and \
+        scores.is_contiguous() and outs == requests and beams.shape == tokens.shape == scores.shape, \
+        "scores and cum_scores must be dense float32, scores, beams and tokens [requests, num_out]"
+    _check_int32(outs * num_out, beams, tokens)
+    assert workspace.is_contiguous(), "workspace must be dense"
+    flags = ()
+    if finished is not None:
+        assert finished.dtype in (torch.uint8, torch.bool) and finished.is_contiguous() and \
+            finished.shape == cum_scores.shape, "finished must be dense uint8 or bool, like cum_scores"
+        flags = (finished,)
+    device, sc, bm, tk, lg, cum, ws, *flags = _addresses(scores, beams, tokens, logits, cum_scores, workspace,
+                                                         *flags)
+    _check(load().pa_beam_select(sc, bm, tk, lg, cum, flags[0] if flags else None, int(end_token), requests,
+                                 num_beams, vocab, num_out, row_stride, _LOGITS[logits.dtype], ws,
+                                 workspace.numel() * workspace.element_size(), _stream(stream, device)))
+
+
+def pa_beam_reorder(key_caches, value_caches, block_tables, seq_lens, parents, layout="HND",
+                    stream=None):
+    """The cache follows the chosen beams: sequence j of each request goes on from what sequence
+    parents[r, j] (int32 [R, B]; negative: left as it is) held, in every layer's pools.  The full
+    pages' ids move in block_tables [R * B, blocks] (in place), the rows of the page that the next
+    token goes to, each sequence's own, are copied.  Layers that share a cache list it once."""
+    pools, (nb, nkv, bs, hd), (sb, sh, st) = _all_pools(key_caches, value_caches, layout)
+    requests, num_beams = parents.shape
+    seqs, blocks = block_tables.shape
+    assert seqs == requests * num_beams, "block_tables must have a row per request and beam"
+    _check_int32(seqs, block_tables, seq_lens, parents)
+    device, tables, lens, of, *at = _addresses(block_tables, seq_lens, parents, *pools)
+    at = array.array("Q", at)
+    _check(load().pa_beam_reorder(at.buffer_info()[0], len(pools), tables, lens, of, requests, num_beams,
+                                  nkv, hd, bs, blocks, nb, sb, sh, st, kv_dtype_of(pools[0]),
+                                  _stream(stream, device)))
 
 
 def selftest_wait_timeout(stream=None):

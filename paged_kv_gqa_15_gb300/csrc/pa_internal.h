@@ -155,6 +155,24 @@ inline bool api_overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m
 int api_check_pool(int head_dim, int block_size, int64_t num_blocks, int num_kv_heads, int64_t sb,
                    int64_t sh, int64_t st, int kv_dtype);
 
+// Launches a kernel as a programmatic dependent of the work before it in the stream: its CTAs may
+// start while that finishes, and wait for it before they read anything.
+template <typename Kernel, typename Params>
+cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const Params &p, cudaStream_t stream,
+                         size_t smem = 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 // Records `msg` as this thread's pa_last_error() text and returns `code`.
 int set_error(int code, const char *msg);
 // Device address of the current device's status word (PA_OK or an error status).

@@ -165,24 +165,6 @@ __global__ void __launch_bounds__(256) bounds_kernel(const __grid_constant__ Bou
     }
 }
 
-// Launches a kernel as a programmatic dependent of the work before it in the stream: its CTAs may
-// start while that finishes, and wait for it before they read anything.
-template <typename Kernel, typename Params>
-cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const Params &p, cudaStream_t stream,
-                         size_t smem = 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <int HD>
 cudaError_t launch_bounds(const BoundsParams &p, bool fp8, cudaStream_t stream) {
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.pages * p.num_kv_heads;
