@@ -27,8 +27,8 @@ namespace {
 
 constexpr int kChunk = 256;                  // logits whose maximum is kept
 constexpr int kScanThreads = 256;
+constexpr int kScanWarps = 152 * 32;         // that are on the GPU at a time
 constexpr int kPickThreads = 1024;
-constexpr int kAhead = 4;                    // chunks of a warp's run that are on their way at once
 constexpr int kMostCandidates = 1024;        // ranked by counting; more of them take the slow way
 
 struct BeamParams {
@@ -42,6 +42,7 @@ struct BeamParams {
     int64_t row_stride;
     int num_requests, num_beams, vocab, num_out, end_token;
     int chunks, run_chunks, num_runs;
+    uint64_t per_chunk;                      // 2^40 / chunks, rounded up: i * per_chunk >> 40 is i / chunks
     int *status;
 };
 
@@ -51,10 +52,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// The warp's largest x that is a number (-inf if there is none).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    return x;
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(fmaxf(x, -INFINITY)));
+    return y;
 }
 
 // s + e plus x, the rounding error of the sum gathered in e.
@@ -64,83 +66,170 @@ __device__ __forceinline__ void add_compensated(float &s, float &e, float x) {
     s = t;
 }
 
+// Two fp32 in one register pair, for the instructions that work on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 split(uint64_t a) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+
 // Whether a row's logits are read: not those of a beam that is finished or out of the search.
 __device__ __forceinline__ bool row_is_read(const BeamParams &p, int64_t row) {
     return p.cum[row] > -INFINITY && !(p.finished && p.finished[row]);
 }
 
-// The eight logits of a lane in one chunk: adjacent ones in vectors where rows start at 16 bytes, else
-// every 32nd; past the row's end -inf.
-template <typename T, bool VECTORS>
-__device__ __forceinline__ void load8(const T *row, int at, int vocab, int lane, float (&x)[8]) {
-    constexpr bool kWide = sizeof(T) == 4;
-    if (VECTORS && at + kChunk <= vocab) {
-        if (kWide) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(row + at) + lane + 32 * i);
-                x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-            }
-        } else {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + at) + lane);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = at + (!VECTORS ? lane + 32 * i : kWide ? 4 * lane + i % 4 + i / 4 * 128 : 8 * lane + i);
-        x[i] = c < vocab ? static_cast<float>(row[c]) : -INFINITY;
-    }
-}
+// A lane's eight logits of one chunk as they lie in memory: adjacent ones where rows start at 16 bytes,
+// else every 32nd; -inf past the row's end.
+template <typename T>
+struct Eight;
 
+template <>
+struct Eight<__nv_bfloat16> {
+    static constexpr int kAhead = 4;             // chunks that a warp reads at once: 64 bytes a lane
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int at, int vocab, int lane, bool vectors) {
+        if (vectors && at + kChunk <= vocab) {
+            v = __ldg(reinterpret_cast<const uint4 *>(row + at) + lane);
+            return;
+        }
+        const uint16_t *bits = reinterpret_cast<const uint16_t *>(row);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = at + (vectors ? 8 * lane + i : lane + 32 * i);
+            w[i] = c < vocab ? __ldg(bits + c) : 0xff80u;
+        }
+        v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+    __device__ __forceinline__ void clear() { v = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    __device__ __forceinline__ float top() const {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ uint64_t two(int i) const {
+        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+
+template <>
+struct Eight<float> {
+    static constexpr int kAhead = 2;
+    float4 v[2];
+    __device__ __forceinline__ void load(const float *row, int at, int vocab, int lane, bool vectors) {
+        if (vectors && at + kChunk <= vocab) {
+            v[0] = __ldg(reinterpret_cast<const float4 *>(row + at) + lane);
+            v[1] = __ldg(reinterpret_cast<const float4 *>(row + at) + lane + 32);
+            return;
+        }
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = at + (vectors ? 4 * lane + i % 4 + i / 4 * 128 : lane + 32 * i);
+            x[i] = c < vocab ? __ldg(row + c) : -INFINITY;
+        }
+        v[0] = make_float4(x[0], x[1], x[2], x[3]);
+        v[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __device__ __forceinline__ void clear() {
+        v[0] = v[1] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+    __device__ __forceinline__ float top() const {
+        return fmaxf(fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w)),
+                     fmaxf(fmaxf(v[1].x, v[1].y), fmaxf(v[1].z, v[1].w)));
+    }
+    __device__ __forceinline__ uint64_t two(int i) const {
+        const float4 &q = v[i / 2];
+        return i % 2 ? pair(q.z, q.w) : pair(q.x, q.y);
+    }
+};
+
+// A warp's run: groups of chunks, the next group on its way while one is worked on.  The running maximum
+// is the warp's, so that a group needs one comparison and, seldom, one rescaling.
 template <typename T, bool VECTORS>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamParams p) {
+    constexpr int kAhead = Eight<T>::kAhead;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kScanThreads / 32) + threadIdx.x / 32;
-    const int64_t row = w / p.num_runs;
-    const int run = static_cast<int>(w - row * p.num_runs);
-    if (row >= static_cast<int64_t>(p.num_requests) * p.num_beams || !row_is_read(p, row)) return;
+    const int w = blockIdx.x * (kScanThreads / 32) + threadIdx.x / 32;
+    const int row = w / p.num_runs, run = w - row * p.num_runs;
+    if (row >= p.num_requests * p.num_beams || !row_is_read(p, row)) return;
     const T *logits = static_cast<const T *>(p.logits) + row * p.row_stride;
-    float *best = p.chunk_max + row * p.chunks;
+    float *best = p.chunk_max + static_cast<int64_t>(row) * p.chunks;
     const int c_end = min(p.chunks, (run + 1) * p.run_chunks);
-    float m = -INFINITY, s = 0.f, e = 0.f;
-    for (int c0 = run * p.run_chunks; c0 < c_end; c0 += kAhead) {
-        float x[kAhead][8];
+    auto fetch = [&](Eight<T> (&x)[kAhead], int c) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
-            if (c0 + a < c_end) load8<T, VECTORS>(logits, (c0 + a) * kChunk, p.vocab, lane, x[a]);
+            if (c + a < c_end)
+                x[a].load(logits, (c + a) * kChunk, p.vocab, lane, VECTORS);
+            else
+                x[a].clear();
+    };
+    float m = -INFINITY, s = 0.f, e = 0.f;
+    Eight<T> x[kAhead], next[kAhead];
+    int c = run * p.run_chunks;
+    fetch(x, c);
+    for (; c < c_end; c += kAhead) {
+        fetch(next, c + kAhead);
+        float mine = -INFINITY, top = m;
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-            if (c0 + a >= c_end) break;
-            float top = x[a][0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, x[a][i]);
-            top = warp_max(top);
-            if (lane == 0) best[c0 + a] = top;
-            if (top > m) {                       // the same in every lane
-                const float f = exp2_approx((m - top) * kLog2e);
-                s *= f, e *= f;
-                m = top;
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = exp2_approx((x[a][i] - base) * kLog2e);
-            add_compensated(s, e, ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7])));
+            const float t = warp_max(x[a].top());
+            top = fmaxf(top, t);
+            if (lane == a) mine = t;
         }
+        if (lane < kAhead && c + lane < c_end) best[c + lane] = mine;
+        if (top > m) {
+            const float f = exp2_approx((m - top) * kLog2e);
+            s *= f, e *= f;
+            m = top;
+        }
+        const float low = m == -INFINITY ? 0.f : -m;
+        const uint64_t low2 = pair(low, low), scale2 = pair(kLog2e, kLog2e);
+        uint64_t sum[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            uint64_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 z = split(mul2(add2(x[a].two(i), low2), scale2));
+                y[i] = pair(exp2_approx(z.x), exp2_approx(z.y));
+            }
+            sum[a] = add2(add2(y[0], y[1]), add2(y[2], y[3]));
+        }
+#pragma unroll
+        for (int d = 1; d < kAhead; d *= 2)
+#pragma unroll
+            for (int a = 0; a + d < kAhead; a += 2 * d) sum[a] = add2(sum[a], sum[a + d]);
+        const float2 both = split(sum[0]);
+        add_compensated(s, e, both.x + both.y);
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) x[a] = next[a];
     }
     s += e;
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) p.runs[row * p.num_runs + run] = make_float2(m, s);
+    if (lane == 0) p.runs[static_cast<int64_t>(row) * p.num_runs + run] = make_float2(m, s);
 }
 
 // ---- the pick ---------------------------------------------------------------------------
@@ -176,73 +265,44 @@ __device__ __forceinline__ uint64_t key_of(float x, const Offset &o) {
     return static_cast<uint64_t>(ordered(top)) << 32 | ordered(rest);
 }
 
-__device__ __forceinline__ float score_of(uint64_t key) {
-    const uint32_t b = static_cast<uint32_t>(key >> 32);
-    return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-}
+__device__ __forceinline__ uint32_t head_of(uint64_t key) { return static_cast<uint32_t>(key >> 32); }
 
-__device__ __forceinline__ Ranked shuffle_down_best(Ranked r, int d) {
-    Ranked o;
-    o.key = __shfl_xor_sync(0xffffffffu, r.key, d);
-    o.place = __shfl_xor_sync(0xffffffffu, r.place, d);
-    return before(o, r) ? o : r;
+__device__ __forceinline__ float score_of(uint64_t key) {
+    const uint32_t b = head_of(key);
+    return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
 }
 
 struct PickSpace {
     Ranked found[kMostCandidates];
-    Ranked groups[kPickThreads / 8];
-    Ranked bar;                              // a candidate is not behind it
+    __align__(16) uint32_t groups[kPickThreads / 8];
+    uint32_t bar;                            // head of the key that a candidate's reaches
+    int count[2];                            // candidates among the chunks, among the elements
     Ranked chosen[PA_MAX_BEAM_OUT];
-    int count;
+    Ranked warps[kPickThreads / 32];
+    uint32_t from[PA_MAX_BEAM_OUT];
     Offset offset[PA_MAX_BEAMS];
     int kind[PA_MAX_BEAMS];                  // 0: out, 1: live, 2: finished
 };
 
-// The `most` first of item(0) .. item(n - 1), in order, into sp.chosen; returns how many there are (items
-// of key 0 do not count).  Called by the whole CTA; places are all different.
-//
-// Each of 32 to 128 groups of threads finds its first item; the most-th of these is a bar that `most`
-// items pass, so that only items that pass it can be among the first.  They are few, and ranked by
-// counting.  Where too many pass (the items of few groups are before all others), the first are taken one
-// by one instead.
+__device__ __forceinline__ void note(PickSpace &sp, int stage, uint64_t key, uint32_t place) {
+    const int at = atomicAdd(&sp.count[stage], 1);
+    if (at < kMostCandidates) sp.found[at] = {key, place};
+}
+
+// The `most` first of the candidates into sp.chosen, in order; returns how many there are.  Each warp
+// counts who is before its candidates.  Where there were more candidates than room, the first of item(0)
+// .. item(n - 1) are taken one by one instead (items of key 0 are none).
 template <typename Item>
-__device__ int pick(PickSpace &sp, int n, int most, const Item &item) {
-    const int tid = threadIdx.x;
-    // groups at least twice `most`, so that the bar is not pulled down by an unlucky group
-    const int lanes = most <= 16 ? 32 : most <= 32 ? 16 : 8;
-    const int groups = kPickThreads / lanes;
-    Ranked first = {0, 0xffffffffu};
-    for (int i = tid; i < n; i += kPickThreads) {
-        const Ranked r = item(i);
-        if (before(r, first)) first = r;
-    }
-    for (int d = 1; d < lanes; d <<= 1) first = shuffle_down_best(first, d);
-    if (tid % lanes == 0) sp.groups[tid / lanes] = first;
-    if (tid == 0) sp.count = 0, sp.bar = {1, 0xffffffffu};
-    __syncthreads();
-    if (tid < groups) {
-        const Ranked mine = sp.groups[tid];
-        int rank = 0;
-        for (int g = 0; g < groups; ++g) rank += before(sp.groups[g], mine);
-        if (mine.key && rank == most - 1) sp.bar = mine;
-    }
-    __syncthreads();
-    const Ranked bar = sp.bar;
-    for (int i = tid; i < n; i += kPickThreads) {
-        const Ranked r = item(i);
-        if (r.key && !before(bar, r)) {
-            const int at = atomicAdd(&sp.count, 1);
-            if (at < kMostCandidates) sp.found[at] = r;
-        }
-    }
-    __syncthreads();
-    const int count = sp.count;
+__device__ int rank(PickSpace &sp, int stage, int n, int most, const Item &item) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const int count = sp.count[stage];
     if (count <= kMostCandidates) {
-        for (int i = tid; i < count; i += kPickThreads) {
+        for (int i = warp; i < count; i += kPickThreads / 32) {
             const Ranked mine = sp.found[i];
-            int rank = 0;
-            for (int j = 0; j < count; ++j) rank += before(sp.found[j], mine);
-            if (rank < most) sp.chosen[rank] = mine;
+            int r = 0;
+            for (int j = 0; j < count; j += 32)
+                r += __popc(__ballot_sync(0xffffffffu, j + lane < count && before(sp.found[min(j + lane, count - 1)], mine)));
+            if (lane == 0 && r < most) sp.chosen[r] = mine;
         }
         __syncthreads();
         return min(count, most);
@@ -254,30 +314,55 @@ __device__ int pick(PickSpace &sp, int n, int most, const Item &item) {
             const Ranked r = item(i);
             if (before(last, r) && before(r, next)) next = r;
         }
-        for (int d = 1; d < 32; d <<= 1) next = shuffle_down_best(next, d);
-        if (tid % 32 == 0) sp.groups[tid / 32] = next;
-        __syncthreads();
-        if (tid < 32) {
-            next = sp.groups[tid];
-            for (int d = 1; d < 32; d <<= 1) next = shuffle_down_best(next, d);
-            if (tid == 0) sp.chosen[k] = next;
+        for (int round = 0; round < 2; ++round) {
+            for (int d = 1; d < 32; d <<= 1) {
+                Ranked o;
+                o.key = __shfl_xor_sync(0xffffffffu, next.key, d);
+                o.place = __shfl_xor_sync(0xffffffffu, next.place, d);
+                if (before(o, next)) next = o;
+            }
+            if (round) break;
+            if (lane == 0) sp.warps[warp] = next;
+            __syncthreads();
+            next = sp.warps[lane];
         }
-        __syncthreads();
-        last = sp.chosen[k];
+        __syncthreads();                     // before the next round's warps are written
+        last = next;                         // the same in all threads
         if (!last.key) return k;
+        if (tid == 0) sp.chosen[k] = last;
     }
+    __syncthreads();
     return most;
 }
 
+// One CTA a request.  A bar keeps the candidates few in both stages: `num_out` items are known whose keys'
+// heads (the score in fp32) reach it, so that no item below it is among the first.
+//   Chunks: every group of 8 to 32 threads finds the largest head among its chunks; the num_out-th largest
+//   of these is the bar (there are twice as many groups as num_out, so that an unlucky group does not pull
+//   it down).
+//   Elements: the bar is the head of the last chosen chunk.
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ PickSpace sp;
-    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int kPer = 8;                  // chunks that a thread keeps in registers
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.num_beams;
-    // cum - logsumexp of every beam
-    for (int b = tid / 32; b < p.num_beams; b += kPickThreads / 32) {
+    const int chunks = p.chunks, n = p.num_beams * chunks, most = p.num_out;
+    const float *best = p.chunk_max + row0 * chunks;
+    float x[kPer];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = base + k * kPickThreads + tid;
+            x[k] = i < n ? best[i] : -INFINITY;
+        }
+    };
+    fetch(0);
+    if (tid < 2) sp.count[tid] = 0;
+    // cum - logsumexp of every beam, a warp each
+    for (int b = warp; b < p.num_beams; b += kPickThreads / 32) {
         const float cum = p.cum[row0 + b];
         const bool finished = p.finished && p.finished[row0 + b];
         int kind = cum == -INFINITY ? 0 : finished ? 2 : 1;
@@ -300,10 +385,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
             bad = !(m < INFINITY) || s != s;
             if (m == -INFINITY) kind = 0;      // every token is ruled out
             // log of s = 2^n f, f within [0.7, 1.5): the large part exactly, the small one in fp32
-            int n;
-            float f = frexpf(s, &n);
-            if (f < 0.70710678f) f *= 2.f, n -= 1;
-            const double off = cum - n * 0.6931471805599453 - static_cast<double>(logf(f));
+            int exponent;
+            float f = frexpf(s, &exponent);
+            if (f < 0.70710678f) f *= 2.f, exponent -= 1;
+            const double off = cum - exponent * 0.6931471805599453 - static_cast<double>(logf(f));
             const float hi = static_cast<float>(off);
             offset = {m, hi, static_cast<float>(off - hi)};
         }
@@ -315,34 +400,80 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         }
     }
     __syncthreads();
-    const int chunks = p.chunks;
-    const float *best = p.chunk_max + row0 * chunks;
-    const int kept = pick(sp, p.num_beams * chunks, p.num_out, [&](int i) -> Ranked {
-        const int b = i / chunks;
+    // the key of chunk i, whose maximum is v; b: its beam
+    auto chunk_key = [&](int i, float v) -> uint64_t {
+        const int b = static_cast<int>(static_cast<uint64_t>(i) * p.per_chunk >> 40);
         const int kind = sp.kind[b];
-        if (kind == 1) return {key_of(best[i], sp.offset[b]), static_cast<uint32_t>(i)};
-        if (kind == 2 && i == b * chunks) return {key_of(0.f, sp.offset[b]), static_cast<uint32_t>(i)};
-        return {0, static_cast<uint32_t>(i)};
-    });
-    __shared__ uint32_t from[PA_MAX_BEAM_OUT];
-    if (tid < kept) from[tid] = sp.chosen[tid].place;
+        if (kind == 1) return key_of(v, sp.offset[b]);
+        return kind == 2 && i == b * chunks ? key_of(0.f, sp.offset[b]) : 0;   // a finished beam has one item
+    };
+    uint32_t first = 0;
+    for (int base = 0; base < n; base += kPer * kPickThreads) {
+        if (base) fetch(base);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = base + k * kPickThreads + tid;
+            if (i < n) first = max(first, head_of(chunk_key(i, x[k])));
+        }
+    }
+    const int lanes = most <= 16 ? 32 : most <= 32 ? 16 : 8, groups = kPickThreads / lanes;
+    for (int d = 1; d < lanes; d <<= 1) first = max(first, __shfl_xor_sync(0xffffffffu, first, d));
+    if (tid % lanes == 0) sp.groups[tid / lanes] = first;
+    if (tid == 0) sp.bar = 1;
+    __syncthreads();
+    if (tid < groups) {
+        const uint32_t mine = sp.groups[tid];
+        int r = 0;
+        for (int g = 0; g < groups; g += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sp.groups + g);
+            r += (v.x > mine || (v.x == mine && g < tid)) + (v.y > mine || (v.y == mine && g + 1 < tid)) +
+                 (v.z > mine || (v.z == mine && g + 2 < tid)) + (v.w > mine || (v.w == mine && g + 3 < tid));
+        }
+        if (mine && r == most - 1) sp.bar = mine;
+    }
+    __syncthreads();
+    uint32_t bar = sp.bar;
+    for (int base = 0; base < n; base += kPer * kPickThreads) {
+        if (n > kPer * kPickThreads) fetch(base);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = base + k * kPickThreads + tid;
+            if (i >= n) continue;
+            const uint64_t key = chunk_key(i, x[k]);
+            if (head_of(key) >= bar) note(sp, 0, key, i);
+        }
+    }
+    __syncthreads();
+    const int kept = rank(sp, 0, n, most, [&](int i) -> Ranked { return {chunk_key(i, best[i]), static_cast<uint32_t>(i)}; });
+    // sp.chosen and sp.found are used again: what is needed of them first
+    bar = kept == most ? head_of(sp.chosen[most - 1].key) : 1;
+    if (tid < kept) sp.from[tid] = sp.chosen[tid].place;
     __syncthreads();
     const T *logits = static_cast<const T *>(p.logits) + row0 * p.row_stride;
-    const int got = pick(sp, kept * kChunk, p.num_out, [&](int i) -> Ranked {
-        const int c = static_cast<int>(from[i / kChunk]);
-        const int b = c / chunks;
-        const int token = (c - b * chunks) * kChunk + i % kChunk;
+    auto element = [&](int i) -> Ranked {
+        const int c = static_cast<int>(sp.from[i / kChunk]);
+        const int b = static_cast<int>(static_cast<uint64_t>(c) * p.per_chunk >> 40);
+        const uint32_t start = static_cast<uint32_t>(b) * p.vocab;
         if (sp.kind[b] == 2) {
-            // one candidate of the whole beam
             if (i % kChunk) return {0, 0xffffffffu};
-            return {key_of(0.f, sp.offset[b]), static_cast<uint32_t>(b) * p.vocab + p.end_token};
+            return {key_of(0.f, sp.offset[b]), start + p.end_token};
         }
+        const int token = (c - b * chunks) * kChunk + i % kChunk;
         if (token >= p.vocab) return {0, 0xffffffffu};
-        const float x = static_cast<float>(logits[b * p.row_stride + token]);
-        return {key_of(x, sp.offset[b]), static_cast<uint32_t>(b) * p.vocab + token};
-    });
-    if (tid < p.num_out) {
-        const int64_t at = static_cast<int64_t>(blockIdx.x) * p.num_out + tid;
+        return {key_of(static_cast<float>(logits[b * p.row_stride + token]), sp.offset[b]), start + token};
+    };
+    for (int k = warp; k < kept; k += kPickThreads / 32) {
+        Ranked r[kChunk / 32];
+#pragma unroll
+        for (int i = 0; i < kChunk / 32; ++i) r[i] = element(k * kChunk + i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < kChunk / 32; ++i)
+            if (head_of(r[i].key) >= bar) note(sp, 1, r[i].key, r[i].place);
+    }
+    __syncthreads();
+    const int got = rank(sp, 1, kept * kChunk, most, element);
+    if (tid < most) {
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * most + tid;
         const bool real = tid < got;
         const uint32_t place = real ? sp.chosen[tid].place : 0;
         p.scores[at] = real ? score_of(sp.chosen[tid].key) : -INFINITY;
@@ -391,6 +522,8 @@ extern "C" int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, co
         return api_fail(PA_ERR_UNSUPPORTED, "logits_dtype %d", logits_dtype);
     if (stride_row < vocab && num_requests * static_cast<int64_t>(num_beams) > 1)
         return api_fail(PA_ERR_INVALID, "stride_row %lld < vocab %d", static_cast<long long>(stride_row), vocab);
+    if (static_cast<int64_t>(num_requests) * num_beams > INT32_MAX - kScanThreads)
+        return api_fail(PA_ERR_UNSUPPORTED, "num_requests %d * num_beams %d", num_requests, num_beams);
     if (stride_row > (INT64_C(1) << 40))
         return api_fail(PA_ERR_UNSUPPORTED, "stride_row %lld", static_cast<long long>(stride_row));
     if (finished && (end_token < 0 || end_token >= vocab))
@@ -432,12 +565,12 @@ extern "C" int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, co
     p.num_out = num_out;
     p.end_token = end_token;
     p.chunks = static_cast<int>(chunks_of(vocab));
-    // runs: about the 64 warps that an SM holds, for each SM; short ones where there is little to read
-    const int64_t share = (rows * p.chunks + 152 * 64 - 1) / (152 * 64);
-    p.run_chunks = static_cast<int>(share < p.chunks ? share : p.chunks);
+    // i < 2^21 chunks of a request and chunks <= 2^16: exact
+    p.per_chunk = ((UINT64_C(1) << 40) + p.chunks - 1) / p.chunks;
+    // the rows' chunks in one wave of warps, each row in equal runs
+    const int64_t per_row = kScanWarps / rows;
+    p.run_chunks = per_row <= 1 ? p.chunks : static_cast<int>((p.chunks + per_row - 1) / per_row);
     p.num_runs = (p.chunks + p.run_chunks - 1) / p.run_chunks;
-    const int64_t scan_ctas = (rows * p.num_runs + kScanThreads / 32 - 1) / (kScanThreads / 32);
-    if (scan_ctas > INT32_MAX) return api_fail(PA_ERR_UNSUPPORTED, "%lld rows", static_cast<long long>(rows));
     p.chunk_max = static_cast<float *>(workspace);
     p.runs = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                         round256(static_cast<size_t>(rows) * p.chunks * sizeof(float)));

@@ -27,6 +27,12 @@ namespace pa {
 namespace {
 
 constexpr int kMaxPairs = 128;
+// rope_kernel: threads of a CTA, their units, tokens whose rows it has in hand or on their way
+constexpr int kMaxThreads = 256;
+constexpr int kUnits = 2;
+constexpr int kStages = 2;
+constexpr int kCtasPerSm = 3;
+constexpr int kAnyChannels = 8192;           // of rope_any_kernel's CTA
 
 struct Rows {                   // [token][head][head_dim] by element strides
     const void *base;
@@ -38,9 +44,10 @@ struct RopeParams {
     uint8_t *k_cache, *v_cache;
     const int64_t *positions, *slots;
     const uint64_t *turns;
-    int64_t num_blocks, s_block, s_head, s_token;
+    int64_t tokens, num_blocks, s_block, s_head, s_token;
     int nq, nk, nv, head_dim, pairs, inverse;
     float factor, k_scale, v_scale;
+    float k_inverse, v_inverse;          // 1 / scale where that is exact (a power of two), else 0
     int *status;
 };
 
@@ -54,37 +61,49 @@ __device__ __forceinline__ float2 turn_of(uint64_t frequency, int64_t position, 
     return make_float2(c * factor, (inverse ? -s : s) * factor);
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+// Two fp32 in one register pair, for the instructions that work on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)   // the first source goes to the upper half
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ float2 split(uint64_t a) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
 }
 
-// E4M3 codes of x / scale: the quotient in fp32, to nearest even, saturated at +-448.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint16_t h[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                : "=h"(h[j])
-                : "f"(__fdiv_rn(x[4 * i + 2 * j + 1], scale)), "f"(__fdiv_rn(x[4 * i + 2 * j], scale)));
-        w[i] = static_cast<uint32_t>(h[0]) | (static_cast<uint32_t>(h[1]) << 16);
-    }
-    return make_uint2(w[0], w[1]);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ float2 floats_of(uint32_t two) {
+    return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t bf16_of(float2 x) {
+    uint32_t w;                          // the first source goes to the upper half
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x.y), "f"(x.x));
+    return w;
+}
+
+// The E4M3 codes of x / scale: the quotient in fp32, to nearest even, saturated at +-448.  A scale that is a
+// power of two has its reciprocal in inverse (else 0): the product is that quotient.
+__device__ __forceinline__ uint32_t codes_of(float2 x, float scale, float inverse) {
+    const float2 y = inverse != 0.f ? split(mul2(pair(x.x, x.y), pair(inverse, inverse)))
+                                    : make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale));
+    uint16_t w;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(y.y), "f"(y.x));
+    return w;
 }
 
 __device__ __forceinline__ const __nv_bfloat16 *row_of(const Rows &r, int64_t t, int h) {
@@ -100,166 +119,254 @@ __device__ __forceinline__ const __nv_bfloat16 *source(const RopeParams &p, int6
     return row_of(p.v, t, h - p.nk);
 }
 
-// Eight results to channel c of head h: a row of q_out or k_out, or of the cache at `at` (element offset
-// of the token's slot).
-template <int KIND>
-__device__ __forceinline__ void put8(const RopeParams &p, int64_t t, int h, int c, int64_t at, const float (&x)[8],
-                                     const uint4 &raw, bool turned) {
-    if (KIND == kRope || h < p.nq) {
-        const __nv_bfloat16 *row = h < p.nq ? row_of(p.q_out, t, h) : row_of(p.k_out, t, h - p.nq);
-        *reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(row) + c) = turned ? pack8(x) : raw;
-        return;
-    }
-    h -= p.nq;
-    const bool is_k = h < p.nk;
-    uint8_t *pool = is_k ? p.k_cache : p.v_cache;
-    const int64_t to = at + (is_k ? h : h - p.nk) * p.s_head + c;
-    if (KIND == kAppendFp8)
-        *reinterpret_cast<uint2 *>(pool + to) = codes8(x, is_k ? p.k_scale : p.v_scale);
-    else
-        *reinterpret_cast<uint4 *>(pool + to * 2) = turned ? pack8(x) : raw;
-}
-
-// Element offset of a token's slot in the pools; false: the token is skipped (padding, or a slot outside
-// the pool, which is flagged).
-template <int KIND>
-__device__ __forceinline__ bool slot_of(const RopeParams &p, int64_t t, int64_t *at) {
-    *at = 0;
-    if (KIND == kRope) return true;
-    const int64_t slot = p.slots[t];
-    if (slot < 0) return false;
-    const int64_t page = slot / kBlockSize;
+// Element offset of a slot in the pools, -1 for a token that is skipped (padding, or a slot outside the
+// pool, which is flagged).
+__device__ __forceinline__ int64_t place_of(const RopeParams &p, int64_t slot) {
+    if (slot < 0) return -1;
+    const int64_t page = slot >> 4;
+    static_assert(kBlockSize == 16, "a slot's page");
     if (page >= p.num_blocks) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
-        return false;
+        return -1;
     }
-    *at = page * p.s_block + (slot - page * kBlockSize) * p.s_token;
-    return true;
+    return page * p.s_block + static_cast<int>(slot & 15) * p.s_token;
 }
 
-// Half layout with pairs a multiple of 8, and every interleaved one: 16 channels a unit.
+// Copies the 16 bytes at `from` to shared memory when they arrive; several pend in committed groups.
+__device__ __forceinline__ void send_for(uint4 *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+
+// What a thread moves of every token: 16 channels of one head, in two vectors of eight.
+struct Unit {
+    const __nv_bfloat16 *from;               // at token 0
+    uint8_t *to;                             // a row at token 0, or the head's rows in the pool
+    int from_token, to_token;                // strides in elements
+    bool live, to_rows, is_k, turned;
+};
+
+// Half layout with pairs a multiple of 8, and every interleaved one.  Grid: x = tokens (each CTA takes every
+// gridDim.x-th), y = groups of heads, kUnits * blockDim.x units each.  A thread's units lie in different
+// heads but at the same channels, so that they share the token's place and angles.
 template <int KIND, bool INTERLEAVED>
-__global__ void __launch_bounds__(1024) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ __align__(16) float2 turns[kMaxPairs];
-    const int64_t t = blockIdx.x;
-    const int per_head = p.head_dim / 16;            // 4, 8 or 16: blockDim is a multiple of it
-    const int u = threadIdx.x & (per_head - 1);
-    const int heads = p.nq + p.nk + p.nv;
-    const int step = blockDim.x / per_head;
-    int h = threadIdx.x / per_head;
-    const bool turned = 8 * u < p.pairs;
-    // the unit's two vectors
-    const int c0 = INTERLEAVED || !turned ? 16 * u : 8 * u;
-    const int c1 = INTERLEAVED || !turned ? 16 * u + 8 : p.pairs + 8 * u;
-    uint4 a, b;
-    if (h < heads) {
-        const __nv_bfloat16 *from = source<KIND>(p, t, h);
-        a = *reinterpret_cast<const uint4 *>(from + c0);
-        b = *reinterpret_cast<const uint4 *>(from + c1);
+    extern __shared__ uint4 rows[];                  // [kStages][kUnits][2][threads]
+    // two pairs' (cos, cos, sin, sin), where the reads of a warp's units fall side by side
+    __shared__ float4 turns[2][kMaxPairs / 2];
+    auto turns_at = [](int i) {              // of pairs i (even) and i + 1
+        return INTERLEAVED ? i / 2 % 2 * (kMaxPairs / 4) + i / 4 : i % 8 / 2 * (kMaxPairs / 8) + i / 8;
+    };
+    constexpr int kElem = KIND == kAppendFp8 ? 1 : 2;
+    const int tid = threadIdx.x, threads = blockDim.x;
+    auto mine_at = [&](int stage, int k) { return rows + ((stage * kUnits + k) * 2) * threads + tid; };
+    const int per_head = p.head_dim / 16;            // 4, 8 or 16: blockDim.x is a multiple of it
+    const int u = tid & (per_head - 1);
+    // the unit's two vectors of 8 channels: those of 8 pairs; interleaved, one in either half of the head;
+    // of the channels behind the turned ones, one in either half of them.  Neighbouring threads' are adjacent.
+    const bool paired = !INTERLEAVED && 8 * u < p.pairs;
+    const int c0 = INTERLEAVED || paired ? 8 * u : p.pairs + 8 * u;
+    const int c1 = (paired ? p.pairs : p.head_dim / 2) + 8 * u;
+    Unit unit[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+        Unit &x = unit[k];
+        int head = ((blockIdx.y * kUnits + k) * threads + tid) / per_head;
+        x.live = head < p.nq + p.nk + p.nv;
+        const bool is_q = head < p.nq;
+        x.is_k = !is_q && (KIND == kRope || head < p.nq + p.nk);
+        x.to_rows = KIND == kRope || is_q;
+        x.turned = (is_q || x.is_k) && (INTERLEAVED ? 4 * u < p.pairs : paired);
+        head -= is_q ? 0 : x.is_k ? p.nq : p.nq + p.nk;
+        const Rows &from = is_q ? p.q : x.is_k ? p.k : p.v, &to = is_q ? p.q_out : p.k_out;
+        x.from = static_cast<const __nv_bfloat16 *>(from.base) + head * from.head + c0;
+        x.from_token = static_cast<int>(from.token);
+        x.to_token = static_cast<int>(to.token);
+        x.to = x.to_rows ? static_cast<uint8_t *>(const_cast<void *>(to.base)) + (head * to.head + c0) * 2
+                         : (x.is_k ? p.k_cache : p.v_cache) + (head * p.s_head + c0) * kElem;
     }
-    int64_t at;
-    if (!slot_of<KIND>(p, t, &at)) return;           // the whole CTA
-    const int64_t position = p.positions[t];
-    for (int i = threadIdx.x; i < p.pairs; i += blockDim.x)
-        turns[i] = turn_of(p.turns[i], position, p.inverse != 0, p.factor);
-    __syncthreads();
-    float2 cs[8];
+    const int apart = c1 - c0;
+
+    // which pair's angle this thread works out; it moves from token to token, so that all warps take part
+    int mine = tid;
+    auto work_out = [&](int buffer, int64_t position) {
+        for (int i = mine; i < p.pairs; i += threads) {
+            const float2 w = turn_of(p.turns[i], position, p.inverse != 0, p.factor);
+            float *four = reinterpret_cast<float *>(&turns[buffer][turns_at(i & ~1)]);
+            four[i % 2] = w.x;
+            four[2 + i % 2] = w.y;
+        }
+        mine += p.pairs;
+        while (mine >= threads) mine -= threads;
+    };
+    const int tokens = static_cast<int>(p.tokens), step = gridDim.x;
+    int sent = blockIdx.x;                           // tokens <= 2^30, and so is step
+    auto send = [&](int stage) {
+        if (sent < tokens) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (8 * u + i < p.pairs) cs[i] = turns[8 * u + i];
-    for (; h < heads; h += step) {
-        const bool turn = turned && (KIND == kRope || h < p.nq + p.nk);
-        float x[8], y[8];
-        unpack8(a, x);
-        unpack8(b, y);
-        if (turn) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (8 * u + i >= p.pairs) continue;
-                // pair i of the unit: (x[i], y[i]), or two neighbours of x or y
-                float &r0 = !INTERLEAVED ? x[i] : i < 4 ? x[2 * i] : y[2 * i - 8];
-                float &r1 = !INTERLEAVED ? y[i] : i < 4 ? x[2 * i + 1] : y[2 * i - 7];
-                const float lo = r0, hi = r1;
-                r0 = __fmaf_rn(lo, cs[i].x, -hi * cs[i].y);
-                r1 = __fmaf_rn(hi, cs[i].x, lo * cs[i].y);
+            for (int k = 0; k < kUnits; ++k) {
+                if (!unit[k].live) continue;
+                const __nv_bfloat16 *from = unit[k].from + static_cast<int64_t>(sent) * unit[k].from_token;
+                send_for(mine_at(stage, k), from);
+                send_for(mine_at(stage, k) + threads, from + apart);
             }
         }
-        // values are rotated by their thread's u like the rest, but not turned
-        put8<KIND>(p, t, h, c0, at, x, a, turn);
-        put8<KIND>(p, t, h, c1, at, y, b, turn);
-        if (h + step < heads) {
-            const __nv_bfloat16 *from = source<KIND>(p, t, h + step);
-            a = *reinterpret_cast<const uint4 *>(from + c0);
-            b = *reinterpret_cast<const uint4 *>(from + c1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        sent += step;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) send(s);
+    int t = blockIdx.x;
+    int64_t slot = KIND == kRope ? 0 : p.slots[t];
+    work_out(0, p.positions[t]);
+    int64_t position = t + step < tokens ? p.positions[t + step] : 0;
+    __syncthreads();
+    for (int buffer = 0, stage = 0; t < tokens; buffer ^= 1, t += step) {
+        send(stage == 0 ? kStages - 1 : stage - 1);
+        const int64_t now = slot;
+        if (t + step < tokens) {
+            if (KIND != kRope) slot = p.slots[t + step];
+            work_out(buffer ^ 1, position);
+            if (t + 2 * step < tokens) position = p.positions[t + 2 * step];
         }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const int64_t at = KIND == kRope ? 0 : place_of(p, now);
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            if (!unit[k].live || at < 0) continue;
+            const uint4 a4 = *mine_at(stage, k), b4 = mine_at(stage, k)[threads];
+            uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+            const bool codes = KIND == kAppendFp8 && !unit[k].to_rows;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // two pairs: halves apart (a[j], b[j]), or the neighbours in two words of a or b
+                uint32_t &w0 = !INTERLEAVED ? a[j] : j < 2 ? a[2 * j] : b[2 * j - 4];
+                uint32_t &w1 = !INTERLEAVED ? b[j] : j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+                float2 x = floats_of(w0), y = floats_of(w1);
+                if (unit[k].turned) {
+                    const int of_pair = !INTERLEAVED ? 8 * u + 2 * j : (j < 2 ? 4 * u : p.head_dim / 4 + 4 * u) + j % 2 * 2;
+                    const float4 cs = turns[buffer][turns_at(of_pair)];
+                    if (INTERLEAVED) {
+                        const float2 x0 = x, y0 = y;
+                        if (of_pair < p.pairs)
+                            x = make_float2(__fmaf_rn(x0.x, cs.x, -x0.y * cs.z), __fmaf_rn(x0.y, cs.x, x0.x * cs.z));
+                        if (of_pair + 1 < p.pairs)
+                            y = make_float2(__fmaf_rn(y0.x, cs.y, -y0.y * cs.w), __fmaf_rn(y0.y, cs.y, y0.x * cs.w));
+                    } else {
+                        const uint64_t x2 = pair(x.x, x.y), y2 = pair(y.x, y.y), c2 = pair(cs.x, cs.y);
+                        const uint64_t s2 = pair(cs.z, cs.w), n2 = pair(-cs.z, -cs.w);
+                        x = split(fma2(x2, c2, mul2(y2, n2)));
+                        y = split(fma2(y2, c2, mul2(x2, s2)));
+                    }
+                    if (!codes) w0 = bf16_of(x), w1 = bf16_of(y);
+                }
+                if (codes) {
+                    const float scale = unit[k].is_k ? p.k_scale : p.v_scale;
+                    const float inverse = unit[k].is_k ? p.k_inverse : p.v_inverse;
+                    w0 = codes_of(x, scale, inverse), w1 = codes_of(y, scale, inverse);
+                }
+            }
+            uint8_t *to = unit[k].to + (unit[k].to_rows ? static_cast<int64_t>(t) * unit[k].to_token * 2 : at * kElem);
+            if (codes) {
+                *reinterpret_cast<uint2 *>(to) = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+                *reinterpret_cast<uint2 *>(to + apart) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+            } else {
+                *reinterpret_cast<uint4 *>(to) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(to + apart * 2) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        }
+        __syncthreads();                             // the next angles are there, these no longer read
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 }
 
-// Half layout with any other number of pairs: the second halves of the pairs start at any channel, so a
-// thread turns a pair, or passes a channel on, at a time.
+// Half layout with any other number of pairs, where the second channel of a pair starts at any 2 bytes.
+// Grid: x = tokens, y = groups of heads.  The heads' rows lie in shared memory whole; a thread makes eight
+// neighbouring results, each from its own channel and the one it is paired with.
 template <int KIND>
-__global__ void __launch_bounds__(256) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ uint4 rows[kAnyChannels / 8];
     __shared__ float2 turns[kMaxPairs];
     const int64_t t = blockIdx.x;
-    int64_t at;
-    if (!slot_of<KIND>(p, t, &at)) return;
+    const int64_t at = KIND == kRope ? 0 : place_of(p, p.slots[t]);
+    if (at < 0) return;                              // the whole CTA
+    const int per_head = p.head_dim / 8, first = blockIdx.y * (kAnyChannels / p.head_dim);
+    const int heads = min(kAnyChannels / p.head_dim, p.nq + p.nk + p.nv - first);
+    for (int i = threadIdx.x; i < heads * per_head; i += blockDim.x)
+        send_for(rows + i, source<KIND>(p, t, first + i / per_head) + i % per_head * 8);
+    asm volatile("cp.async.commit_group;" ::: "memory");
     const int64_t position = p.positions[t];
     for (int i = threadIdx.x; i < p.pairs; i += blockDim.x)
         turns[i] = turn_of(p.turns[i], position, p.inverse != 0, p.factor);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    auto put = [&](int h, int c, float x) {
+    for (int i = threadIdx.x; i < heads * per_head; i += blockDim.x) {
+        const int c0 = i % per_head * 8;
+        int h = first + i / per_head;
+        const uint4 own = rows[i];
+        const uint32_t w[4] = {own.x, own.y, own.z, own.w};
+        const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(rows) + (i / per_head) * p.head_dim;
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j] = floats_of(w[j]);
+            if (h >= p.nq + p.nk) continue;          // values are not turned
+            float *two = &y[j].x;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = c0 + 2 * j + k;
+                if (c >= 2 * p.pairs) continue;
+                const bool second = c >= p.pairs;
+                const float2 cs = turns[second ? c - p.pairs : c];
+                const float other = __bfloat162float(row[second ? c - p.pairs : c + p.pairs]);
+                two[k] = __fmaf_rn(two[k], cs.x, second ? other * cs.y : -other * cs.y);
+            }
+        }
         if (KIND == kRope || h < p.nq) {
-            const __nv_bfloat16 *row = h < p.nq ? row_of(p.q_out, t, h) : row_of(p.k_out, t, h - p.nq);
-            const_cast<__nv_bfloat16 *>(row)[c] = __float2bfloat16_rn(x);
-            return;
+            const __nv_bfloat16 *to = h < p.nq ? row_of(p.q_out, t, h) : row_of(p.k_out, t, h - p.nq);
+            *reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(to) + c0) =
+                make_uint4(bf16_of(y[0]), bf16_of(y[1]), bf16_of(y[2]), bf16_of(y[3]));
+            continue;
         }
-        h -= p.nq;
-        const bool is_k = h < p.nk;
+        const bool is_k = h < p.nq + p.nk;
         uint8_t *pool = is_k ? p.k_cache : p.v_cache;
-        const int64_t to = at + (is_k ? h : h - p.nk) * p.s_head + c;
+        const int64_t to = at + (h - p.nq - (is_k ? 0 : p.nk)) * p.s_head + c0;
         if (KIND == kAppendFp8) {
-            uint16_t code;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                : "=h"(code)
-                : "f"(0.f), "f"(__fdiv_rn(x, is_k ? p.k_scale : p.v_scale)));
-            pool[to] = static_cast<uint8_t>(code);
+            const float scale = is_k ? p.k_scale : p.v_scale, inverse = is_k ? p.k_inverse : p.v_inverse;
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = codes_of(y[j], scale, inverse);
+            *reinterpret_cast<uint2 *>(pool + to) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        } else if (is_k) {
+            *reinterpret_cast<uint4 *>(pool + to * 2) =
+                make_uint4(bf16_of(y[0]), bf16_of(y[1]), bf16_of(y[2]), bf16_of(y[3]));
         } else {
-            reinterpret_cast<__nv_bfloat16 *>(pool)[to] = __float2bfloat16_rn(x);
+            *reinterpret_cast<uint4 *>(pool + to * 2) = own;
         }
-    };
-    const int items = p.head_dim - p.pairs;          // pairs, then the channels behind them
-    const int turning = (p.nq + p.nk) * items;
-    for (int i = threadIdx.x; i < turning; i += blockDim.x) {
-        const int h = i / items, c = i - h * items;
-        const __nv_bfloat16 *from = source<KIND>(p, t, h);
-        if (c < p.pairs) {
-            const float lo = __bfloat162float(from[c]), hi = __bfloat162float(from[c + p.pairs]);
-            const float2 w = turns[c];
-            put(h, c, __fmaf_rn(lo, w.x, -hi * w.y));
-            put(h, c + p.pairs, __fmaf_rn(hi, w.x, lo * w.y));
-        } else {
-            put(h, c + p.pairs, __bfloat162float(from[c + p.pairs]));
-        }
-    }
-    for (int i = threadIdx.x; i < p.nv * p.head_dim; i += blockDim.x) {
-        const int h = p.nq + p.nk + i / p.head_dim, c = i & (p.head_dim - 1);
-        put(h, c, __bfloat162float(source<KIND>(p, t, h)[c]));
     }
 }
 
 template <int KIND>
-cudaError_t launch_rope(const RopeParams &p, int64_t tokens, bool interleaved, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(tokens));
-    if (!interleaved && p.pairs % 8) return launch_after(rope_pairs_kernel<KIND>, grid, 256, p, stream);
-    const int units = (p.nq + p.nk + p.nv) * (p.head_dim / 16);
-    int threads = (units + 31) / 32 * 32;
-    if (threads > 512) threads = 512;
-    return interleaved ? launch_after(rope_kernel<KIND, true>, grid, threads, p, stream)
-                       : launch_after(rope_kernel<KIND, false>, grid, threads, p, stream);
+cudaError_t launch_rope(const RopeParams &p, bool interleaved, cudaStream_t stream) {
+    const int channels = (p.nq + p.nk + p.nv) * p.head_dim;
+    if (!interleaved && p.pairs % 8)
+        return launch_after(rope_any_kernel<KIND>,
+                            dim3(static_cast<unsigned>(p.tokens),
+                                 static_cast<unsigned>((channels + kAnyChannels - 1) / kAnyChannels)),
+                            256, p, stream);
+    const int units = (channels / 16 + kUnits - 1) / kUnits;
+    const int groups = (units + kMaxThreads - 1) / kMaxThreads;
+    const int threads = ((units + groups - 1) / groups + 31) / 32 * 32;
+    // one wave: kCtasPerSm of the largest CTAs, or as many threads in smaller ones, fit an SM
+    const int per_sm = kCtasPerSm * kMaxThreads / threads < 32 ? kCtasPerSm * kMaxThreads / threads : 32;
+    const int64_t wave = (152 * per_sm + groups - 1) / groups;
+    const dim3 grid(static_cast<unsigned>(p.tokens < wave ? p.tokens : wave), static_cast<unsigned>(groups));
+    const size_t rows = static_cast<size_t>(kStages) * kUnits * 2 * threads * sizeof(uint4);
+    return interleaved ? launch_after(rope_kernel<KIND, true>, grid, threads, p, stream, rows)
+                       : launch_after(rope_kernel<KIND, false>, grid, threads, p, stream, rows);
 }
 
 // ---- argument checks --------------------------------------------------------------------
@@ -301,6 +408,8 @@ int check_rows(const char *name, const Rows &r, int64_t tokens, int heads, int h
     if (st < 0 || sh < 0 || st % 8 || sh % 8 || st > kMost || sh > kMost)
         return api_fail(PA_ERR_INVALID, "%s: strides (%lld, %lld) must be multiples of 16 bytes, not negative", name,
                         static_cast<long long>(r.token), static_cast<long long>(r.head));
+    if (st > INT32_MAX)
+        return api_fail(PA_ERR_UNSUPPORTED, "%s: token stride %lld", name, static_cast<long long>(st));
     if (!written) return PA_OK;
     const Extent e = extent_of(r, tokens, heads, head_dim);
     const int64_t inner = st >= sh ? sh : st, inner_count = st >= sh ? heads : tokens;
@@ -316,8 +425,8 @@ bool same_rows(const Rows &a, const Rows &b, int64_t tokens, int heads) {
 
 int check_common(int64_t num_tokens, int nq, int nk, int head_dim, int rotary_dim, float factor) {
     if (num_tokens < 0) return api_fail(PA_ERR_INVALID, "num_tokens %lld", static_cast<long long>(num_tokens));
-    if (num_tokens > INT32_MAX)
-        return api_fail(PA_ERR_UNSUPPORTED, "num_tokens %lld > 2^31 - 1", static_cast<long long>(num_tokens));
+    if (num_tokens > (INT64_C(1) << 30))
+        return api_fail(PA_ERR_UNSUPPORTED, "num_tokens %lld > 2^30", static_cast<long long>(num_tokens));
     if (nq < 0 || nk < 0) return api_fail(PA_ERR_INVALID, "head counts (%d, %d)", nq, nk);
     if (nq > 65536 || nk > 65536) return api_fail(PA_ERR_UNSUPPORTED, "head counts (%d, %d) > 65536", nq, nk);
     if (head_dim != 64 && head_dim != 128 && head_dim != 256)
@@ -326,6 +435,12 @@ int check_common(int64_t num_tokens, int nq, int nk, int head_dim, int rotary_di
         return api_fail(PA_ERR_INVALID, "rotary_dim %d must be even, from 2 to head_dim %d", rotary_dim, head_dim);
     if (!std::isfinite(factor)) return api_fail(PA_ERR_INVALID, "attention_factor %g", static_cast<double>(factor));
     return PA_OK;
+}
+
+// 1 / scale of a power of two whose reciprocal is a normal fp32 too, else 0.
+float exact_inverse(float scale) {
+    int n;
+    return std::frexp(scale, &n) == 0.5f && n > -125 && n < 127 ? 1.f / scale : 0.f;
 }
 
 // Number of a pair that makes `turns` full turns within `len` positions, as a real number.
@@ -437,6 +552,7 @@ extern "C" int pa_rope(void *q_out, void *k_out, const void *q, const void *k, c
             if (x.of != y.of && may_overlap(to, extent_of(*y.to, num_tokens, y.heads, head_dim)))
                 return api_fail(PA_ERR_INVALID, "q_out and k_out overlap");
         }
+    p.tokens = num_tokens;
     p.positions = positions;
     p.turns = turns;
     p.nq = num_q_heads;
@@ -445,7 +561,7 @@ extern "C" int pa_rope(void *q_out, void *k_out, const void *q, const void *k, c
     p.pairs = rotary_dim / 2;
     p.inverse = inverse ? 1 : 0;
     p.factor = attention_factor;
-    const cudaError_t e = launch_rope<kRope>(p, num_tokens, interleaved != 0, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_rope<kRope>(p, interleaved != 0, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : api_cuda_fail(e, "rope launch");
 }
 
@@ -497,6 +613,7 @@ extern "C" int pa_rope_append(void *q_out, const void *q, const void *k, const v
     }
     p.k_cache = static_cast<uint8_t *>(k_cache);
     p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.tokens = num_tokens;
     p.positions = positions;
     p.slots = slot_mapping;
     p.turns = turns;
@@ -511,10 +628,12 @@ extern "C" int pa_rope_append(void *q_out, const void *q, const void *k, const v
     p.factor = attention_factor;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.k_inverse = exact_inverse(k_scale);
+    p.v_inverse = exact_inverse(v_scale);
     rc = api_status_ptr(&p.status);
     if (rc) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = kv_dtype == PA_KV_FP8_E4M3 ? launch_rope<kAppendFp8>(p, num_tokens, interleaved != 0, s)
-                                                     : launch_rope<kAppend>(p, num_tokens, interleaved != 0, s);
+    const cudaError_t e = kv_dtype == PA_KV_FP8_E4M3 ? launch_rope<kAppendFp8>(p, interleaved != 0, s)
+                                                     : launch_rope<kAppend>(p, interleaved != 0, s);
     return e == cudaSuccess ? PA_OK : api_cuda_fail(e, "rope_append launch");
 }
