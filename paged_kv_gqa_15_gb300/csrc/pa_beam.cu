@@ -29,6 +29,7 @@ constexpr int kChunk = 256;                  // logits whose maximum is kept
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = 152 * 32;         // that are on the GPU at a time
 constexpr int kPickThreads = 1024;
+constexpr int kGroups = 2 * PA_MAX_BEAM_OUT; // of its threads, whose best scores make a bar
 constexpr int kMostCandidates = 1024;        // ranked by counting; more of them take the slow way
 
 struct BeamParams {
@@ -52,10 +53,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// The warp's largest x that is a number (-inf if there is none).
+// The warp's largest x that is a number.
 __device__ __forceinline__ float warp_max(float x) {
     float y;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(fmaxf(x, -INFINITY)));
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -105,21 +106,22 @@ template <>
 struct Eight<__nv_bfloat16> {
     static constexpr int kAhead = 4;             // chunks that a warp reads at once: 64 bytes a lane
     uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int at, int vocab, int lane, bool vectors) {
-        if (vectors && at + kChunk <= vocab) {
-            v = __ldg(reinterpret_cast<const uint4 *>(row + at) + lane);
+    // the chunk that starts at `chunk`, of which `left` logits are in the row
+    template <bool VECTORS, bool WHOLE>
+    __device__ __forceinline__ void load(const __nv_bfloat16 *chunk, int left, int lane) {
+        if (VECTORS && WHOLE) {
+            v = __ldg(reinterpret_cast<const uint4 *>(chunk) + lane);
             return;
         }
-        const uint16_t *bits = reinterpret_cast<const uint16_t *>(row);
+        const uint16_t *bits = reinterpret_cast<const uint16_t *>(chunk);
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = at + (vectors ? 8 * lane + i : lane + 32 * i);
-            w[i] = c < vocab ? __ldg(bits + c) : 0xff80u;
+            const int c = VECTORS ? 8 * lane + i : lane + 32 * i;
+            w[i] = WHOLE || c < left ? __ldg(bits + c) : 0xff80u;
         }
         v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
-    __device__ __forceinline__ void clear() { v = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ __forceinline__ float top() const {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
         const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
@@ -135,23 +137,21 @@ template <>
 struct Eight<float> {
     static constexpr int kAhead = 2;
     float4 v[2];
-    __device__ __forceinline__ void load(const float *row, int at, int vocab, int lane, bool vectors) {
-        if (vectors && at + kChunk <= vocab) {
-            v[0] = __ldg(reinterpret_cast<const float4 *>(row + at) + lane);
-            v[1] = __ldg(reinterpret_cast<const float4 *>(row + at) + lane + 32);
+    template <bool VECTORS, bool WHOLE>
+    __device__ __forceinline__ void load(const float *chunk, int left, int lane) {
+        if (VECTORS && WHOLE) {
+            v[0] = __ldg(reinterpret_cast<const float4 *>(chunk) + lane);
+            v[1] = __ldg(reinterpret_cast<const float4 *>(chunk) + lane + 32);
             return;
         }
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = at + (vectors ? 4 * lane + i % 4 + i / 4 * 128 : lane + 32 * i);
-            x[i] = c < vocab ? __ldg(row + c) : -INFINITY;
+            const int c = VECTORS ? 4 * lane + i % 4 + i / 4 * 128 : lane + 32 * i;
+            x[i] = WHOLE || c < left ? __ldg(chunk + c) : -INFINITY;
         }
         v[0] = make_float4(x[0], x[1], x[2], x[3]);
         v[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-    __device__ __forceinline__ void clear() {
-        v[0] = v[1] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
     __device__ __forceinline__ float top() const {
         return fmaxf(fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w)),
@@ -177,20 +177,36 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     const T *logits = static_cast<const T *>(p.logits) + row * p.row_stride;
     float *best = p.chunk_max + static_cast<int64_t>(row) * p.chunks;
     const int c_end = min(p.chunks, (run + 1) * p.run_chunks);
-    auto fetch = [&](Eight<T> (&x)[kAhead], int c) {
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-            if (c + a < c_end)
-                x[a].load(logits, (c + a) * kChunk, p.vocab, lane, VECTORS);
-            else
-                x[a].clear();
-    };
-    float m = -INFINITY, s = 0.f, e = 0.f;
-    Eight<T> x[kAhead], next[kAhead];
     int c = run * p.run_chunks;
-    fetch(x, c);
-    for (; c < c_end; c += kAhead) {
-        fetch(next, c + kAhead);
+    // groups of whole chunks, then what is left chunk by chunk
+    const int whole = min(c_end, p.vocab / kChunk), groups = max(0, whole - c) / kAhead;
+    float m = -INFINITY, s = 0.f, e = 0.f;
+    auto rise = [&](float top) {                 // to a larger maximum
+        const float f = exp2_approx((m - top) * kLog2e);
+        s *= f, e *= f;
+        m = top;
+    };
+    auto sum_of = [&](const Eight<T> &x, uint64_t low) {
+        const uint64_t scale = pair(kLog2e, kLog2e);
+        uint64_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 z = split(mul2(add2(x.two(i), low), scale));
+            y[i] = pair(exp2_approx(z.x), exp2_approx(z.y));
+        }
+        return add2(add2(y[0], y[1]), add2(y[2], y[3]));
+    };
+    const T *from = logits + static_cast<int64_t>(c) * kChunk;
+    Eight<T> x[kAhead], next[kAhead];
+    auto fetch = [&](Eight<T> (&to)[kAhead]) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) to[a].template load<VECTORS, true>(from + a * kChunk, kChunk, lane);
+        from += kAhead * kChunk;
+    };
+    if (groups > 0) fetch(x);
+#pragma unroll 2
+    for (int g = 0; g < groups; ++g, c += kAhead) {
+        if (g + 1 < groups) fetch(next);
         float mine = -INFINITY, top = m;
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
@@ -198,25 +214,12 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
             top = fmaxf(top, t);
             if (lane == a) mine = t;
         }
-        if (lane < kAhead && c + lane < c_end) best[c + lane] = mine;
-        if (top > m) {
-            const float f = exp2_approx((m - top) * kLog2e);
-            s *= f, e *= f;
-            m = top;
-        }
+        if (lane < kAhead) best[c + lane] = mine;
+        if (top > m) rise(top);
         const float low = m == -INFINITY ? 0.f : -m;
-        const uint64_t low2 = pair(low, low), scale2 = pair(kLog2e, kLog2e);
         uint64_t sum[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            uint64_t y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 z = split(mul2(add2(x[a].two(i), low2), scale2));
-                y[i] = pair(exp2_approx(z.x), exp2_approx(z.y));
-            }
-            sum[a] = add2(add2(y[0], y[1]), add2(y[2], y[3]));
-        }
+        for (int a = 0; a < kAhead; ++a) sum[a] = sum_of(x[a], pair(low, low));
 #pragma unroll
         for (int d = 1; d < kAhead; d *= 2)
 #pragma unroll
@@ -225,6 +228,19 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         add_compensated(s, e, both.x + both.y);
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) x[a] = next[a];
+    }
+    for (; c < c_end; ++c) {
+        const T *chunk = logits + static_cast<int64_t>(c) * kChunk;
+        if (c < whole)
+            x[0].template load<VECTORS, true>(chunk, kChunk, lane);
+        else
+            x[0].template load<VECTORS, false>(chunk, p.vocab - c * kChunk, lane);
+        const float top = warp_max(x[0].top());
+        if (lane == 0) best[c] = top;
+        if (top > m) rise(top);
+        const float low = m == -INFINITY ? 0.f : -m;
+        const float2 both = split(sum_of(x[0], pair(low, low)));
+        add_compensated(s, e, both.x + both.y);
     }
     s += e;
 #pragma unroll
@@ -267,26 +283,30 @@ __device__ __forceinline__ uint64_t key_of(float x, const Offset &o) {
 
 __device__ __forceinline__ uint32_t head_of(uint64_t key) { return static_cast<uint32_t>(key >> 32); }
 
-__device__ __forceinline__ float score_of(uint64_t key) {
-    const uint32_t b = head_of(key);
-    return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+__device__ __forceinline__ float float_of(uint32_t ordered_bits) {
+    return __uint_as_float(ordered_bits & 0x80000000u ? ordered_bits & 0x7fffffffu : ~ordered_bits);
 }
 
+enum { kOut = 0, kLive = 1, kFinished = 2 };
+
 struct PickSpace {
-    Ranked found[kMostCandidates];
-    __align__(16) uint32_t groups[kPickThreads / 8];
-    uint32_t bar;                            // head of the key that a candidate's reaches
-    int count[2];                            // candidates among the chunks, among the elements
-    Ranked chosen[PA_MAX_BEAM_OUT];
+    uint64_t key[kMostCandidates];           // the candidates
+    uint32_t place[kMostCandidates];
+    int count[2];                            // how many, among the chunks and among the elements
+    __align__(16) uint32_t groups[kGroups];
+    uint32_t bar;
+    uint32_t reach;                          // largest |hi| of the beams, as bits
+    uint64_t chosen_key[PA_MAX_BEAM_OUT];
+    uint32_t chosen[PA_MAX_BEAM_OUT], from[PA_MAX_BEAM_OUT];
     Ranked warps[kPickThreads / 32];
-    uint32_t from[PA_MAX_BEAM_OUT];
     Offset offset[PA_MAX_BEAMS];
-    int kind[PA_MAX_BEAMS];                  // 0: out, 1: live, 2: finished
+    float2 shift[PA_MAX_BEAMS];              // of a live beam: (top, hi); of the others (0, -inf)
+    int kind[PA_MAX_BEAMS];
 };
 
 __device__ __forceinline__ void note(PickSpace &sp, int stage, uint64_t key, uint32_t place) {
     const int at = atomicAdd(&sp.count[stage], 1);
-    if (at < kMostCandidates) sp.found[at] = {key, place};
+    if (at < kMostCandidates) sp.key[at] = key, sp.place[at] = place;
 }
 
 // The `most` first of the candidates into sp.chosen, in order; returns how many there are.  Each warp
@@ -298,11 +318,11 @@ __device__ int rank(PickSpace &sp, int stage, int n, int most, const Item &item)
     const int count = sp.count[stage];
     if (count <= kMostCandidates) {
         for (int i = warp; i < count; i += kPickThreads / 32) {
-            const Ranked mine = sp.found[i];
+            const Ranked mine = {sp.key[i], sp.place[i]};
             int r = 0;
-            for (int j = 0; j < count; j += 32)
-                r += __popc(__ballot_sync(0xffffffffu, j + lane < count && before(sp.found[min(j + lane, count - 1)], mine)));
-            if (lane == 0 && r < most) sp.chosen[r] = mine;
+            for (int j = lane; j < count; j += 32) r += before({sp.key[j], sp.place[j]}, mine);
+            r = __reduce_add_sync(0xffffffffu, r);
+            if (lane == 0 && r < most) sp.chosen_key[r] = mine.key, sp.chosen[r] = mine.place;
         }
         __syncthreads();
         return min(count, most);
@@ -329,24 +349,65 @@ __device__ int rank(PickSpace &sp, int stage, int n, int most, const Item &item)
         __syncthreads();                     // before the next round's warps are written
         last = next;                         // the same in all threads
         if (!last.key) return k;
-        if (tid == 0) sp.chosen[k] = last;
+        if (tid == 0) sp.chosen_key[k] = last.key, sp.chosen[k] = last.place;
     }
     __syncthreads();
     return most;
 }
 
-// One CTA a request.  A bar keeps the candidates few in both stages: `num_out` items are known whose keys'
-// heads (the score in fp32) reach it, so that no item below it is among the first.
-//   Chunks: every group of 8 to 32 threads finds the largest head among its chunks; the num_out-th largest
-//   of these is the bar (there are twice as many groups as num_out, so that an unlucky group does not pull
-//   it down).
-//   Elements: the bar is the head of the last chosen chunk.
+// cum - logsumexp of one beam, by a warp.
+__device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, int64_t row, int b) {
+    const int lane = threadIdx.x & 31;
+    const float2 *runs = p.runs + row * p.num_runs;
+    const float cum = p.cum[row];
+    const bool finished = p.finished && p.finished[row];
+    float m = -INFINITY;                     // of a beam that is not live: of anything, and not used
+    for (int i = lane; i < p.num_runs; i += 32) m = fmaxf(m, runs[i].x);
+    m = warp_max(m);
+    float s = 0.f, e = 0.f;
+    for (int i = lane; i < p.num_runs; i += 32) {
+        const float2 r = runs[i];
+        // an empty run (its maximum -inf) has a sum of 0, or NaN
+        add_compensated(s, e, r.y * (r.x == m ? 1.f : exp2_approx((r.x - m) * kLog2e)));
+    }
+    s += e;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane) return;
+    int kind = cum == -INFINITY ? kOut : finished ? kFinished : kLive;
+    const bool bad = !(cum < INFINITY) || (kind == kLive && (!(m < INFINITY) || s != s));
+    if (bad) atomicOr(p.status, kStatusInvalid);
+    if (bad || (kind == kLive && m == -INFINITY)) kind = kOut;      // or every token is ruled out
+    Offset offset = {0.f, cum, 0.f};
+    if (kind == kLive) {
+        // log of s = 2^n f, f within [0.7, 1.5): the large part exactly, the small one in fp32
+        int n;
+        float f = frexpf(s, &n);
+        if (f < 0.70710678f) f *= 2.f, n -= 1;
+        const double off = cum - n * 0.6931471805599453 - static_cast<double>(logf(f));
+        const float hi = static_cast<float>(off);
+        offset = {m, hi, static_cast<float>(off - hi)};
+    }
+    sp.kind[b] = kind;
+    sp.offset[b] = offset;
+    sp.shift[b] = kind == kLive ? make_float2(offset.top, offset.hi) : make_float2(0.f, -INFINITY);
+    if (kind != kOut) atomicMax(&sp.reach, __float_as_uint(fabsf(offset.hi)));
+}
+
+// One CTA a request.  The num_out first chunks by their maxima, then the num_out first of those chunks'
+// elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings, off by 2^-23
+// of |score| + 2 |hi| at most.  Every thread belongs to one of kGroups groups, and the num_out-th largest of
+// the groups' best scores is a bar that num_out items reach; an item below it by more than both may be off
+// (2^-20 of |bar| + |hi|) cannot be among the first.  The few others get their key and are ranked by
+// counting.  Elements are measured against the score of the last chosen chunk.
+//
+// Bound by latency: six barriers, three loads in a row (runs, logits, and the chunk maxima beside them).
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ PickSpace sp;
-    constexpr int kPer = 8;                  // chunks that a thread keeps in registers
+    constexpr int kPer = 4;                  // chunks that a thread keeps in registers
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.num_beams;
     const int chunks = p.chunks, n = p.num_beams * chunks, most = p.num_out;
@@ -360,125 +421,113 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         }
     };
     fetch(0);
+    if (tid < kGroups) sp.groups[tid] = 0;
     if (tid < 2) sp.count[tid] = 0;
-    // cum - logsumexp of every beam, a warp each
-    for (int b = warp; b < p.num_beams; b += kPickThreads / 32) {
-        const float cum = p.cum[row0 + b];
-        const bool finished = p.finished && p.finished[row0 + b];
-        int kind = cum == -INFINITY ? 0 : finished ? 2 : 1;
-        Offset offset = {0.f, cum, 0.f};
-        bool bad = !(cum < INFINITY);
-        if (kind == 1 && !bad) {
-            const float2 *runs = p.runs + (row0 + b) * p.num_runs;
-            float m = -INFINITY;
-            for (int i = lane; i < p.num_runs; i += 32) m = fmaxf(m, runs[i].x);
-            m = warp_max(m);
-            float s = 0.f, e = 0.f;
-            for (int i = lane; i < p.num_runs; i += 32) {
-                const float2 r = runs[i];
-                // an empty run (its maximum -inf) has a sum of 0, or NaN
-                add_compensated(s, e, r.y * (r.x == m ? 1.f : exp2_approx((r.x - m) * kLog2e)));
-            }
-            s += e;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            bad = !(m < INFINITY) || s != s;
-            if (m == -INFINITY) kind = 0;      // every token is ruled out
-            // log of s = 2^n f, f within [0.7, 1.5): the large part exactly, the small one in fp32
-            int exponent;
-            float f = frexpf(s, &exponent);
-            if (f < 0.70710678f) f *= 2.f, exponent -= 1;
-            const double off = cum - exponent * 0.6931471805599453 - static_cast<double>(logf(f));
-            const float hi = static_cast<float>(off);
-            offset = {m, hi, static_cast<float>(off - hi)};
-        }
-        if (bad) kind = 0;
-        if (lane == 0) {
-            if (bad) atomicOr(p.status, kStatusInvalid);
-            sp.kind[b] = kind;
-            sp.offset[b] = offset;
-        }
-    }
+    if (tid == 0) sp.bar = 0, sp.reach = 0;
     __syncthreads();
-    // the key of chunk i, whose maximum is v; b: its beam
-    auto chunk_key = [&](int i, float v) -> uint64_t {
-        const int b = static_cast<int>(static_cast<uint64_t>(i) * p.per_chunk >> 40);
-        const int kind = sp.kind[b];
-        if (kind == 1) return key_of(v, sp.offset[b]);
-        return kind == 2 && i == b * chunks ? key_of(0.f, sp.offset[b]) : 0;   // a finished beam has one item
-    };
-    uint32_t first = 0;
-    for (int base = 0; base < n; base += kPer * kPickThreads) {
-        if (base) fetch(base);
+    for (int b = warp; b < p.num_beams; b += kPickThreads / 32) join_runs(p, sp, row0 + b, b);
+    __syncthreads();
+    auto beam_of = [&](int i) { return static_cast<int>(static_cast<uint64_t>(i) * p.per_chunk >> 40); };
+    // the scores of the fetched chunks; -inf for nothing
+    auto score = [&](int base) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = base + k * kPickThreads + tid;
-            if (i < n) first = max(first, head_of(chunk_key(i, x[k])));
+            const float2 shift = sp.shift[min(beam_of(base + k * kPickThreads + tid), p.num_beams - 1)];
+            const float y = (x[k] - shift.x) + shift.y;
+            x[k] = x[k] > -INFINITY && shift.y > -INFINITY ? y : -INFINITY;
         }
+    };
+    float first = -INFINITY;
+    for (int base = 0; base < n; base += kPer * kPickThreads) {
+        if (base) fetch(base);
+        score(base);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) first = fmaxf(first, x[k]);
     }
-    const int lanes = most <= 16 ? 32 : most <= 32 ? 16 : 8, groups = kPickThreads / lanes;
-    for (int d = 1; d < lanes; d <<= 1) first = max(first, __shfl_xor_sync(0xffffffffu, first, d));
-    if (tid % lanes == 0) sp.groups[tid / lanes] = first;
-    if (tid == 0) sp.bar = 1;
+    const bool ends = tid < p.num_beams && sp.kind[tid] == kFinished;      // this thread's finished beam
+    if (ends) first = fmaxf(first, sp.offset[tid].hi);
+    if (first > -INFINITY) atomicMax(&sp.groups[tid % kGroups], ordered(first));
     __syncthreads();
-    if (tid < groups) {
+    if (tid < kGroups) {
         const uint32_t mine = sp.groups[tid];
         int r = 0;
-        for (int g = 0; g < groups; g += 4) {
+#pragma unroll 4
+        for (int g = 0; g < kGroups; g += 4) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sp.groups + g);
             r += (v.x > mine || (v.x == mine && g < tid)) + (v.y > mine || (v.y == mine && g + 1 < tid)) +
                  (v.z > mine || (v.z == mine && g + 2 < tid)) + (v.w > mine || (v.w == mine && g + 3 < tid));
         }
-        if (mine && r == most - 1) sp.bar = mine;
+        if (r == most - 1) sp.bar = mine;
     }
     __syncthreads();
-    uint32_t bar = sp.bar;
+    const float reach = __uint_as_float(sp.reach);
+    auto below = [&](uint32_t bar) {         // what surely lies under a bar (0: there is none) lies under this
+        const float y = float_of(bar);
+        return bar ? y - (fabsf(y) + reach) * 0x1p-20f : -INFINITY;
+    };
+    float low = below(sp.bar);
+    auto chunk = [&](int i) -> Ranked {
+        const int b = beam_of(i);
+        const uint32_t place = i;
+        if (sp.kind[b] == kLive) return {key_of(best[i], sp.offset[b]), place};
+        return {sp.kind[b] == kFinished && i == b * chunks ? key_of(0.f, sp.offset[b]) : 0, place};
+    };
     for (int base = 0; base < n; base += kPer * kPickThreads) {
-        if (n > kPer * kPickThreads) fetch(base);
-#pragma unroll
+        if (n > kPer * kPickThreads) fetch(base), score(base);
         for (int k = 0; k < kPer; ++k) {
-            const int i = base + k * kPickThreads + tid;
-            if (i >= n) continue;
-            const uint64_t key = chunk_key(i, x[k]);
-            if (head_of(key) >= bar) note(sp, 0, key, i);
+            const float y = k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
+            if (!(y >= low) || y == -INFINITY) continue;
+            const Ranked r = chunk(base + k * kPickThreads + tid);
+            if (r.key) note(sp, 0, r.key, r.place);
         }
     }
+    if (ends && sp.offset[tid].hi >= low) note(sp, 0, key_of(0.f, sp.offset[tid]), tid * chunks);
     __syncthreads();
-    const int kept = rank(sp, 0, n, most, [&](int i) -> Ranked { return {chunk_key(i, best[i]), static_cast<uint32_t>(i)}; });
-    // sp.chosen and sp.found are used again: what is needed of them first
-    bar = kept == most ? head_of(sp.chosen[most - 1].key) : 1;
-    if (tid < kept) sp.from[tid] = sp.chosen[tid].place;
+    const int kept = rank(sp, 0, n, most, chunk);
+    // the candidates and the chosen make room for the elements
+    const uint32_t bar = kept == most ? head_of(sp.chosen_key[most - 1]) : 0;
+    if (tid < kept) sp.from[tid] = sp.chosen[tid];
     __syncthreads();
+    low = below(bar);
+    // a pair's place in the order: beam, then token
+    static_assert(PA_MAX_BEAM_VOCAB <= 1 << 24 && PA_MAX_BEAMS <= 1 << 8, "a beam and a token in 32 bits");
     const T *logits = static_cast<const T *>(p.logits) + row0 * p.row_stride;
     auto element = [&](int i) -> Ranked {
-        const int c = static_cast<int>(sp.from[i / kChunk]);
-        const int b = static_cast<int>(static_cast<uint64_t>(c) * p.per_chunk >> 40);
-        const uint32_t start = static_cast<uint32_t>(b) * p.vocab;
-        if (sp.kind[b] == 2) {
-            if (i % kChunk) return {0, 0xffffffffu};
-            return {key_of(0.f, sp.offset[b]), start + p.end_token};
-        }
+        const int c = static_cast<int>(sp.from[i / kChunk]), b = beam_of(c);
+        const uint32_t beam = static_cast<uint32_t>(b) << 24;
+        if (sp.kind[b] == kFinished) return {i % kChunk ? 0 : key_of(0.f, sp.offset[b]), beam | p.end_token};
         const int token = (c - b * chunks) * kChunk + i % kChunk;
         if (token >= p.vocab) return {0, 0xffffffffu};
-        return {key_of(static_cast<float>(logits[b * p.row_stride + token]), sp.offset[b]), start + token};
+        return {key_of(static_cast<float>(logits[b * p.row_stride + token]), sp.offset[b]), beam | token};
     };
     for (int k = warp; k < kept; k += kPickThreads / 32) {
-        Ranked r[kChunk / 32];
-#pragma unroll
-        for (int i = 0; i < kChunk / 32; ++i) r[i] = element(k * kChunk + i * 32 + lane);
+        const int c = static_cast<int>(sp.from[k]), b = beam_of(c);
+        const float2 shift = sp.shift[b];
+        const int token = (c - b * chunks) * kChunk + lane;
+        const T *row = logits + b * p.row_stride + token;
+        float y[kChunk / 32];
 #pragma unroll
         for (int i = 0; i < kChunk / 32; ++i)
-            if (head_of(r[i].key) >= bar) note(sp, 1, r[i].key, r[i].place);
+            y[i] = token + 32 * i < p.vocab && shift.y > -INFINITY ? static_cast<float>(row[32 * i]) : -INFINITY;
+        uint32_t passed = 0;
+#pragma unroll
+        for (int i = 0; i < kChunk / 32; ++i)
+            if (y[i] > -INFINITY && (y[i] - shift.x) + shift.y >= low) passed |= 1u << i;
+        if (sp.kind[b] == kFinished && lane == 0) passed = 1;
+        for (; passed; passed &= passed - 1) {
+            const Ranked r = element(k * kChunk + 32 * (__ffs(passed) - 1) + lane);
+            if (r.key && head_of(r.key) >= bar) note(sp, 1, r.key, r.place);
+        }
     }
     __syncthreads();
     const int got = rank(sp, 1, kept * kChunk, most, element);
     if (tid < most) {
         const int64_t at = static_cast<int64_t>(blockIdx.x) * most + tid;
         const bool real = tid < got;
-        const uint32_t place = real ? sp.chosen[tid].place : 0;
-        p.scores[at] = real ? score_of(sp.chosen[tid].key) : -INFINITY;
-        p.beams[at] = real ? static_cast<int>(place / p.vocab) : -1;
-        p.tokens[at] = real ? static_cast<int>(place % p.vocab) : -1;
+        const uint32_t place = sp.chosen[tid];
+        p.scores[at] = real ? float_of(head_of(sp.chosen_key[tid])) : -INFINITY;
+        p.beams[at] = real ? static_cast<int>(place >> 24) : -1;
+        p.tokens[at] = real ? static_cast<int>(place & 0xffffffu) : -1;
     }
 }
 

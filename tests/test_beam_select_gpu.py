@@ -101,6 +101,14 @@ def test_equal_rows_and_equal_logits(dtype, V):
     check(wide[:, :V], np.full((R, B), -3.25), 14, ties=True)
 
 
+def test_more_equal_chunks_than_are_ranked():
+    for B, V, K in ((4, 300000, 16), (1, 1 << 20, 3), (32, 20000, 64)):
+        check(torch.full((B, V), -2.5, dtype=torch.bfloat16), np.full((1, B), -1.0), K, ties=True)
+        x = torch.full((B, V), -2.5, dtype=torch.float32)
+        x[:, V // 2:] = -2.25                          # the better half: still too many
+        check(x, np.full((1, B), -1.0), K, ties=True)
+
+
 def test_first_step_finished_and_dead_beams():
     R, B, V, K = 4, 4, 3001, 8
     x = normal(R * B, V, 13, torch.float32)
