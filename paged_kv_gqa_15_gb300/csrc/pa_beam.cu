@@ -29,7 +29,7 @@ constexpr int kChunk = 256;                  // logits whose maximum is kept
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = 152 * 32;         // that are on the GPU at a time
 constexpr int kPickThreads = 1024;
-constexpr int kGroups = 2 * PA_MAX_BEAM_OUT; // of its threads, whose best scores make a bar
+constexpr int kGroups = 2 * PA_MAX_BEAM_OUT; // of its threads at most, whose best scores make a bar
 constexpr int kMostCandidates = 1024;        // ranked by counting; more of them take the slow way
 
 struct BeamParams {
@@ -361,15 +361,23 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     const float2 *runs = p.runs + row * p.num_runs;
     const float cum = p.cum[row];
     const bool finished = p.finished && p.finished[row];
-    float m = -INFINITY;                     // of a beam that is not live: of anything, and not used
-    for (int i = lane; i < p.num_runs; i += 32) m = fmaxf(m, runs[i].x);
+    // all at once up to 128 runs; those of a beam that is not live are of anything, and not used
+    constexpr int kPer = 4;
+    float2 r[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        r[k] = lane + 32 * k < p.num_runs ? runs[lane + 32 * k] : make_float2(-INFINITY, 0.f);
+    float m = fmaxf(fmaxf(r[0].x, r[1].x), fmaxf(r[2].x, r[3].x));
+    for (int i = lane + 32 * kPer; i < p.num_runs; i += 32) m = fmaxf(m, runs[i].x);
     m = warp_max(m);
     float s = 0.f, e = 0.f;
-    for (int i = lane; i < p.num_runs; i += 32) {
-        const float2 r = runs[i];
-        // an empty run (its maximum -inf) has a sum of 0, or NaN
-        add_compensated(s, e, r.y * (r.x == m ? 1.f : exp2_approx((r.x - m) * kLog2e)));
-    }
+    // an empty run (its maximum -inf) has a sum of 0, or NaN
+    auto add = [&](float2 run) {
+        add_compensated(s, e, run.y * (run.x == m ? 1.f : exp2_approx((run.x - m) * kLog2e)));
+    };
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) add(r[k]);
+    for (int i = lane + 32 * kPer; i < p.num_runs; i += 32) add(runs[i]);
     s += e;
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -380,13 +388,17 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     if (bad || (kind == kLive && m == -INFINITY)) kind = kOut;      // or every token is ruled out
     Offset offset = {0.f, cum, 0.f};
     if (kind == kLive) {
-        // log of s = 2^n f, f within [0.7, 1.5): the large part exactly, the small one in fp32
+        // s = 2^n f with f within [0.7, 1.5), so that log f, rounded to fp32, is off by 2^-26 at most; n log 2 in
+        // two parts, the first of 12 bits (its products with n are exact), and the sums with their errors
         int n;
         float f = frexpf(s, &n);
         if (f < 0.70710678f) f *= 2.f, n -= 1;
-        const double off = cum - n * 0.6931471805599453 - static_cast<double>(logf(f));
-        const float hi = static_cast<float>(off);
-        offset = {m, hi, static_cast<float>(off - hi)};
+        constexpr float kLn2Hi = 0.693115234375f, kLn2Lo = static_cast<float>(0.69314718055994531 - 0.693115234375);
+        const float large = -n * kLn2Hi, small = -n * kLn2Lo - logf(f);
+        const float hi = cum + large, z = hi - cum;
+        const float lo = (cum - (hi - z)) + (large - z) + small;
+        const float top = hi + lo;
+        offset = {m, top, lo - (top - hi)};
     }
     sp.kind[b] = kind;
     sp.offset[b] = offset;
@@ -396,10 +408,11 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
 
 // One CTA a request.  The num_out first chunks by their maxima, then the num_out first of those chunks'
 // elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings, off by 2^-23
-// of |score| + 2 |hi| at most.  Every thread belongs to one of kGroups groups, and the num_out-th largest of
+// of |score| + 2 |hi| at most.  Every thread belongs to one of a few groups, and the num_out-th largest of
 // the groups' best scores is a bar that num_out items reach; an item below it by more than both may be off
 // (2^-20 of |bar| + |hi|) cannot be among the first.  The few others get their key and are ranked by
-// counting.  Elements are measured against the score of the last chosen chunk.
+// counting.  There are twice as many groups as num_out, at least a warp's lanes, so that the bar is seldom
+// much below the num_out-th best item.  Elements are measured against the score of the last chosen chunk.
 //
 // Bound by latency: six barriers, three loads in a row (runs, logits, and the chunk maxima beside them).
 template <typename T>
@@ -411,6 +424,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.num_beams;
     const int chunks = p.chunks, n = p.num_beams * chunks, most = p.num_out;
+    const int groups = most <= 16 ? 32 : most <= 32 ? 64 : kGroups;
     const float *best = p.chunk_max + row0 * chunks;
     float x[kPer];
     auto fetch = [&](int base) {
@@ -446,13 +460,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     }
     const bool ends = tid < p.num_beams && sp.kind[tid] == kFinished;      // this thread's finished beam
     if (ends) first = fmaxf(first, sp.offset[tid].hi);
-    if (first > -INFINITY) atomicMax(&sp.groups[tid % kGroups], ordered(first));
+    if (first > -INFINITY) atomicMax(&sp.groups[tid % groups], ordered(first));
     __syncthreads();
-    if (tid < kGroups) {
+    if (tid < groups) {
         const uint32_t mine = sp.groups[tid];
         int r = 0;
-#pragma unroll 4
-        for (int g = 0; g < kGroups; g += 4) {
+        for (int g = 0; g < groups; g += 4) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sp.groups + g);
             r += (v.x > mine || (v.x == mine && g < tid)) + (v.y > mine || (v.y == mine && g + 1 < tid)) +
                  (v.z > mine || (v.z == mine && g + 2 < tid)) + (v.w > mine || (v.w == mine && g + 3 < tid));
