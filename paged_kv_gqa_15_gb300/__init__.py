@@ -448,10 +448,10 @@ def pa_tree_decode(out, q, k_cache, v_cache, block_tables, seq_lens, qo_indptr, 
 
 
 def _all_pools(key_caches, value_caches, layout):
-    """The pools [k_0, v_0, k_1, ...] of all layers, of one geometry, and that geometry:
+    """The pools of all layers in one list, of one geometry, and that geometry:
     (num_blocks, kv heads, block size, head_dim), strides of a block, head and token."""
     assert len(key_caches) == len(value_caches) > 0, "every layer has a key and a value pool"
-    pools = [t for kv in zip(key_caches, value_caches) for t in kv]
+    pools = [*key_caches, *value_caches]
     geometry = _pool_geometry(pools[0], layout), pool_strides(pools[0], layout)
     # a model has two pools a layer, so the checks go over whole lists
     n = len(pools)
@@ -584,21 +584,26 @@ def rope_table_of(frequencies, device="cuda"):
 _INT64 = torch.int64
 
 
-def _head_rows(x, tokens=None, head_dim=None):
-    """(tokens, heads, head_dim, strides of a token and a head) of x [tokens, heads, head_dim]."""
-    t, heads, hd = x.shape
-    st, sh, one = x.stride()
-    assert x.dtype is _BF16 and (one == 1 or x.numel() == 0) and t == (t if tokens is None else tokens) and \
-        hd == (hd if head_dim is None else head_dim), \
-        "q, k, v and their outputs must be bf16 [tokens, heads, head_dim] of one token count and " \
-        "head_dim, with a contiguous head_dim"
-    return t, heads, hd, st, sh
+_HEADS = "q, k, v and their outputs must be bf16 [tokens, heads, head_dim] of one token count and " \
+    "head_dim, with a contiguous head_dim; q_out must be like q, k_out like k, k and v like the pools"
+_PER_TOKEN = "positions, slots and frequencies must be dense int64 tensors, one entry a token or pair"
 
 
-def _check_int64(n, *arrays):
-    for t in arrays:
-        assert t.dtype is _INT64 and t.is_contiguous() and t.numel() == n, \
-            "positions, slots and frequencies must be dense int64 tensors, one entry a token or pair"
+def _turned_rows(out, x, tokens, head_dim):
+    """(heads, strides of a token and a head of out and of x), x [tokens, heads, head_dim]."""
+    shape = x.shape
+    t, heads, hd = shape
+    out_token, out_head, out_step = out.stride()
+    token, head, step = x.stride()
+    assert x.dtype is out.dtype is _BF16 and out.shape == shape and t == tokens and hd == head_dim and \
+        step == out_step == 1, _HEADS
+    return heads, out_token, out_head, token, head
+
+
+def _pairs_of(turns):
+    n, = turns.shape
+    assert turns.dtype is _INT64 and turns.is_contiguous(), _PER_TOKEN
+    return n
 
 
 def pa_rope(q_out, k_out, q, k, positions, turns, interleaved=False, attention_factor=1.0,
@@ -607,23 +612,21 @@ def pa_rope(q_out, k_out, q, k, positions, turns, interleaved=False, attention_f
     may be q and k themselves; k and k_out may be None.  turns and attention_factor are those of
     rope_table; the first 2 * len(turns) channels turn.  Slices of a fused projection are taken as
     they are.  inverse: by the negated angles, the gradient of the call without it."""
-    t, nq, hd, qt, qh = _head_rows(q)
-    _, heads, _, qot, qoh = _head_rows(q_out, t, hd)
-    assert heads == nq and (k is None) == (k_out is None), "q_out must be like q, k_out like k"
+    t, _, hd = q.shape
+    nq, qot, qoh, qt, qh = _turned_rows(q_out, q, t, hd)
     nk = kt = kh = kot = koh = 0
     more = ()
+    assert (k is None) == (k_out is None), _HEADS
     if k is not None:
-        _, nk, _, kt, kh = _head_rows(k, t, hd)
-        _, heads, _, kot, koh = _head_rows(k_out, t, hd)
-        assert heads == nk, "q_out must be like q, k_out like k"
+        nk, kot, koh, kt, kh = _turned_rows(k_out, k, t, hd)
         more = (k_out, k)
-    _check_int64(t, positions)
-    _check_int64(turns.numel(), turns)
+    pairs = _pairs_of(turns)
+    assert positions.dtype is _INT64 and positions.shape == (t,) and positions.is_contiguous(), _PER_TOKEN
     device, qo, qi, pos, table, *more = _addresses(q_out, q, positions, turns, *more)
     ko, ki = more or (None, None)
-    _check(load().pa_rope(qo, ko, qi, ki, pos, table, t, nq, nk, hd, 2 * turns.numel(), qot, qoh, kot,
-                          koh, qt, qh, kt, kh, 1 if interleaved else 0, 1 if inverse else 0,
-                          float(attention_factor), _stream(stream, device)))
+    _check(load().pa_rope(qo, ko, qi, ki, pos, table, t, nq, nk, hd, 2 * pairs, qot, qoh, kot, koh, qt, qh,
+                          kt, kh, 1 if interleaved else 0, 1 if inverse else 0, attention_factor,
+                          _stream(stream, device)))
 
 
 def pa_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, turns, layout="HND",
@@ -632,26 +635,26 @@ def pa_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, tu
     turned into its slots of the cache, v into them as it is.  A token with a negative slot is
     padding and leaves its row of q_out as it was.  q and q_out may be None."""
     nb, nkv, bs, hd, sb, sh, st, kind = _kv_pools(k_cache, v_cache, layout)
-    t, heads, _, kt, kh = _head_rows(k, None, hd)
-    _, vheads, _, vt, vh = _head_rows(v, t, hd)
-    assert heads == vheads == nkv and (q is None) == (q_out is None), \
-        "k and v must have the pools' heads, q_out must be like q"
+    shape = k.shape
+    t, heads, wide = shape
+    kt, kh, step = k.stride()
+    vt, vh, also = v.stride()
+    assert heads == nkv and wide == hd and v.shape == shape and step == also == 1 and \
+        k.dtype is v.dtype is _BF16 and (q is None) == (q_out is None), _HEADS
     nq = qt = qh = qot = qoh = 0
     more = ()
     if q is not None:
-        _, nq, _, qt, qh = _head_rows(q, t, hd)
-        _, heads, _, qot, qoh = _head_rows(q_out, t, hd)
-        assert heads == nq, "k and v must have the pools' heads, q_out must be like q"
+        nq, qot, qoh, qt, qh = _turned_rows(q_out, q, t, hd)
         more = (q_out, q)
-    _check_int64(t, slot_mapping, positions)
-    _check_int64(turns.numel(), turns)
+    pairs = _pairs_of(turns)
+    assert positions.dtype is slot_mapping.dtype is _INT64 and positions.shape == slot_mapping.shape == (t,) and \
+        positions.is_contiguous() and slot_mapping.is_contiguous(), _PER_TOKEN
     device, ki, vi, kc, vc, slots, pos, table, *more = _addresses(k, v, k_cache, v_cache, slot_mapping,
                                                                   positions, turns, *more)
     qo, qi = more or (None, None)
-    _check(load().pa_rope_append(qo, qi, ki, vi, kc, vc, slots, pos, table, t, nq, nkv, hd,
-                                 2 * turns.numel(), bs, nb, qot, qoh, qt, qh, kt, kh, vt, vh, sb, sh, st,
-                                 1 if interleaved else 0, float(attention_factor), kind, float(k_scale),
-                                 float(v_scale), _stream(stream, device)))
+    _check(load().pa_rope_append(qo, qi, ki, vi, kc, vc, slots, pos, table, t, nq, nkv, hd, 2 * pairs, bs, nb,
+                                 qot, qoh, qt, qh, kt, kh, vt, vh, sb, sh, st, 1 if interleaved else 0,
+                                 attention_factor, kind, k_scale, v_scale, _stream(stream, device)))
 
 
 def beam_select_workspace_size(num_requests, num_beams, vocab) -> int:

@@ -5,12 +5,13 @@
 // Only the page that the next tokens go to is a slot's own, and its rows so far are copied, in every pool.
 //
 // Both are permutations in place, a slot being the parent of some while it takes over another.  One thread
-// owns one 16-byte chunk of one row of the page, for all slots of a request (or one column of their tables):
-// it reads what every moving slot needs, then writes.  Nobody else touches its chunks: no barrier, no second
+// takes one 16-byte chunk of one row of the page, for all slots of a request (or one column of their tables):
+// it reads what every moving slot needs, then writes.  Nobody else touches these chunks: no barrier, no second
 // buffer.
 //
 // Bound by memory for many layers (each moved row is read and written once), by the chain lengths -> page
-// ids -> rows for few.
+// ids -> rows for few.  So a CTA goes through that chain once for several pools where there
+// are many, and only over the rows that there are.
 #include <cstring>
 
 #include "../../include/pa.h"
@@ -28,12 +29,13 @@ struct ReorderParams {
     int32_t *block_tables;
     const int32_t *seq_lens, *parents;
     int64_t num_blocks, b_block, b_head, b_token;   // strides in bytes
-    int num_pools, num_beams, num_kv_heads, max_blocks, chunks;
-    int copy_ctas;                                  // of a request; one more moves its tables
+    int num_pools, num_beams, num_kv_heads, max_blocks;
+    int chunk_bits;                                 // a row's chunks: 1 << chunk_bits
+    int pools_per_cta, copy_ctas;                   // copy_ctas of a request; one more moves its tables
     int *status;
 };
 
-// Grid: x = pools' chunks, then the tables; y = request.  BEAMS: an upper bound of num_beams.
+// Grid: x = shares of the pools, then the tables; y = request.  BEAMS: an upper bound of num_beams.
 template <int BEAMS>
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -87,24 +89,35 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         }
         return;
     }
-    // a thread's chunk: pool, kv head, row of the page, 16 bytes
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + tid;
-    const int c = static_cast<int>(i % p.chunks);
-    const int row = static_cast<int>(i / p.chunks % kBlockSize);
-    const int64_t rest = i / p.chunks / kBlockSize;
-    const int h = static_cast<int>(rest % p.num_kv_heads);
-    const int64_t pool = rest / p.num_kv_heads;
-    if (pool >= p.num_pools) return;
-    uint8_t *base = p.pools[pool] + h * p.b_head + row * p.b_token + c * 16;
-    uint4 v[BEAMS];
+    int rows = 0;
+    for (int j = 0; j < n; ++j)
+        if (parent[j] != j) rows = max(rows, len[j] % kBlockSize);
+    const int items = (p.num_kv_heads * rows) << p.chunk_bits;
+    const int pool0 = blockIdx.x * p.pools_per_cta, pool1 = min(p.num_pools, pool0 + p.pools_per_cta);
+    constexpr int kAhead = BEAMS <= 4 ? 2 : 1;      // chunks of a thread that are read before any is written
+    for (int pool = pool0; pool < pool1; ++pool)
+        for (int i0 = tid; i0 < items; i0 += kAhead * kThreads) {
+            uint4 v[kAhead][BEAMS];
+            uint8_t *at[kAhead];
+            int row[kAhead];
 #pragma unroll
-    for (int j = 0; j < BEAMS; ++j)
-        if (j < n && parent[j] != j && row < len[j] % kBlockSize)
-            v[j] = *reinterpret_cast<const uint4 *>(base + page[parent[j]] * p.b_block);
+            for (int a = 0; a < kAhead; ++a) {
+                const int i = i0 + a * kThreads;
+                const int r = i >> p.chunk_bits, h = r / rows;
+                row[a] = i < items ? r - h * rows : kBlockSize;
+                at[a] = p.pools[pool] + h * p.b_head + row[a] * p.b_token + (i & ((1 << p.chunk_bits) - 1)) * 16;
 #pragma unroll
-    for (int j = 0; j < BEAMS; ++j)
-        if (j < n && parent[j] != j && row < len[j] % kBlockSize)
-            *reinterpret_cast<uint4 *>(base + page[j] * p.b_block) = v[j];
+                for (int j = 0; j < BEAMS; ++j)
+                    if (j < n && parent[j] != j && row[a] < len[j] % kBlockSize)
+                        v[a][j] = *reinterpret_cast<const uint4 *>(at[a] + page[parent[j]] * p.b_block);
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                for (int j = 0; j < BEAMS; ++j)
+                    if (j < n && parent[j] != j && row[a] < len[j] % kBlockSize)
+                        *reinterpret_cast<uint4 *>(at[a] + page[j] * p.b_block) = v[a][j];
+        }
 }
 
 }  // namespace
@@ -158,14 +171,16 @@ extern "C" int pa_beam_reorder(void *const *pools, int num_pools, int32_t *block
     p.num_beams = num_beams;
     p.num_kv_heads = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
-    p.chunks = head_dim * elem / 16;
+    for (int chunks = head_dim * elem / 16; chunks > 1; chunks /= 2) ++p.chunk_bits;
     rc = api_status_ptr(&p.status);
     if (rc) return rc;
     for (int at = 0; at == 0 || at < num_pools; at += kMaxPools) {
         p.num_pools = num_pools - at < kMaxPools ? num_pools - at : kMaxPools;
         for (int i = 0; i < p.num_pools; ++i) p.pools[i] = static_cast<uint8_t *>(pools[at + i]);
-        const int64_t threads = static_cast<int64_t>(p.num_pools) * num_kv_heads * kBlockSize * p.chunks;
-        p.copy_ctas = static_cast<int>((threads + kThreads - 1) / kThreads);
+        // enough CTAs to even out requests of more and fewer rows: two waves of eight an SM
+        const int64_t share = (static_cast<int64_t>(p.num_pools) * num_requests + 152 * 16 - 1) / (152 * 16);
+        p.pools_per_cta = static_cast<int>(share < p.num_pools ? share : p.num_pools);
+        p.copy_ctas = p.num_pools ? (p.num_pools + p.pools_per_cta - 1) / p.pools_per_cta : 0;
         // the tables move with the first launch
         const dim3 grid(static_cast<unsigned>(p.copy_ctas + (at == 0)), static_cast<unsigned>(num_requests));
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
