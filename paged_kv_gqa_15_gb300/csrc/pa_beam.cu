@@ -296,6 +296,7 @@ struct PickSpace {
     __align__(16) uint32_t groups[kGroups];
     uint32_t bar;
     uint32_t reach;                          // largest |hi| of the beams, as bits
+    int live;                                // beams whose chunks take part
     uint64_t chosen_key[PA_MAX_BEAM_OUT];
     uint32_t chosen[PA_MAX_BEAM_OUT], from[PA_MAX_BEAM_OUT];
     Ranked warps[kPickThreads / 32];
@@ -355,6 +356,23 @@ __device__ int rank(PickSpace &sp, int stage, int n, int most, const Item &item)
     return most;
 }
 
+// The most-th largest of the groups' values into sp.bar (0 if there are not so many).  By the whole CTA.
+__device__ __noinline__ void raise_bar(PickSpace &sp, int groups, int most) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid < groups) {
+        const uint32_t mine = sp.groups[tid];
+        int r = 0;
+        for (int g = 0; g < groups; g += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sp.groups + g);
+            r += (v.x > mine || (v.x == mine && g < tid)) + (v.y > mine || (v.y == mine && g + 1 < tid)) +
+                 (v.z > mine || (v.z == mine && g + 2 < tid)) + (v.w > mine || (v.w == mine && g + 3 < tid));
+        }
+        if (r == most - 1) sp.bar = mine;
+    }
+    __syncthreads();
+}
+
 // cum - logsumexp of one beam, by a warp.
 __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, int64_t row, int b) {
     const int lane = threadIdx.x & 31;
@@ -403,6 +421,7 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     sp.kind[b] = kind;
     sp.offset[b] = offset;
     sp.shift[b] = kind == kLive ? make_float2(offset.top, offset.hi) : make_float2(0.f, -INFINITY);
+    if (kind == kLive) atomicAdd(&sp.live, 1);
     if (kind != kOut) atomicMax(&sp.reach, __float_as_uint(fabsf(offset.hi)));
 }
 
@@ -437,7 +456,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     fetch(0);
     if (tid < kGroups) sp.groups[tid] = 0;
     if (tid < 2) sp.count[tid] = 0;
-    if (tid == 0) sp.bar = 0, sp.reach = 0;
+    if (tid == 0) sp.bar = 0, sp.reach = 0, sp.live = 0;
     __syncthreads();
     for (int b = warp; b < p.num_beams; b += kPickThreads / 32) join_runs(p, sp, row0 + b, b);
     __syncthreads();
@@ -461,18 +480,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     const bool ends = tid < p.num_beams && sp.kind[tid] == kFinished;      // this thread's finished beam
     if (ends) first = fmaxf(first, sp.offset[tid].hi);
     if (first > -INFINITY) atomicMax(&sp.groups[tid % groups], ordered(first));
-    __syncthreads();
-    if (tid < groups) {
-        const uint32_t mine = sp.groups[tid];
-        int r = 0;
-        for (int g = 0; g < groups; g += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(sp.groups + g);
-            r += (v.x > mine || (v.x == mine && g < tid)) + (v.y > mine || (v.y == mine && g + 1 < tid)) +
-                 (v.z > mine || (v.z == mine && g + 2 < tid)) + (v.w > mine || (v.w == mine && g + 3 < tid));
-        }
-        if (r == most - 1) sp.bar = mine;
-    }
-    __syncthreads();
+    raise_bar(sp, groups, most);
     const float reach = __uint_as_float(sp.reach);
     auto below = [&](uint32_t bar) {         // what surely lies under a bar (0: there is none) lies under this
         const float y = float_of(bar);
@@ -513,20 +521,42 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         if (token >= p.vocab) return {0, 0xffffffffu};
         return {key_of(static_cast<float>(logits[b * p.row_stride + token]), sp.offset[b]), beam | token};
     };
-    for (int k = warp; k < kept; k += kPickThreads / 32) {
+    // the scores of a lane's elements of chosen chunk k, and its beam's one item if that is finished
+    auto scores_of = [&](int k, float (&y)[kChunk / 32]) {
         const int c = static_cast<int>(sp.from[k]), b = beam_of(c);
         const float2 shift = sp.shift[b];
         const int token = (c - b * chunks) * kChunk + lane;
         const T *row = logits + b * p.row_stride + token;
-        float y[kChunk / 32];
 #pragma unroll
         for (int i = 0; i < kChunk / 32; ++i)
             y[i] = token + 32 * i < p.vocab && shift.y > -INFINITY ? static_cast<float>(row[32 * i]) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kChunk / 32; ++i)
+            if (y[i] > -INFINITY) y[i] = (y[i] - shift.x) + shift.y;
+        if (sp.kind[b] == kFinished && lane == 0) y[0] = sp.offset[b].hi;
+    };
+    float y[kChunk / 32];
+    if (sp.live * chunks < 4 * most) {
+        // few chunks to choose from: the last chosen one says little, so the elements get a bar of their own
+        if (tid < groups) sp.groups[tid] = 0;
+        if (tid == 0) sp.bar = 0;
+        __syncthreads();
+        first = -INFINITY;
+        for (int k = warp; k < kept; k += kPickThreads / 32) {
+            scores_of(k, y);
+#pragma unroll
+            for (int i = 0; i < kChunk / 32; ++i) first = fmaxf(first, y[i]);
+        }
+        if (first > -INFINITY) atomicMax(&sp.groups[tid % groups], ordered(first));
+        raise_bar(sp, groups, most);
+        low = fmaxf(low, below(sp.bar));
+    }
+    for (int k = warp; k < kept; k += kPickThreads / 32) {
+        scores_of(k, y);
         uint32_t passed = 0;
 #pragma unroll
         for (int i = 0; i < kChunk / 32; ++i)
-            if (y[i] > -INFINITY && (y[i] - shift.x) + shift.y >= low) passed |= 1u << i;
-        if (sp.kind[b] == kFinished && lane == 0) passed = 1;
+            if (y[i] > -INFINITY && y[i] >= low) passed |= 1u << i;
         for (; passed; passed &= passed - 1) {
             const Ranked r = element(k * kChunk + 32 * (__ffs(passed) - 1) + lane);
             if (r.key && head_of(r.key) >= bar) note(sp, 1, r.key, r.place);

@@ -289,40 +289,49 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ R
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ uint4 rows[kAnyChannels / 8];
-    __shared__ float2 turns[kMaxPairs];
+    // of pair i at [i % 8][i / 8]: neighbouring threads read side by side
+    __shared__ float2 turns[8][kMaxPairs / 8 + 1];
     const int64_t t = blockIdx.x;
     const int64_t at = KIND == kRope ? 0 : place_of(p, p.slots[t]);
     if (at < 0) return;                              // the whole CTA
-    const int per_head = p.head_dim / 8, first = blockIdx.y * (kAnyChannels / p.head_dim);
-    const int heads = min(kAnyChannels / p.head_dim, p.nq + p.nk + p.nv - first);
-    for (int i = threadIdx.x; i < heads * per_head; i += blockDim.x)
-        send_for(rows + i, source<KIND>(p, t, first + i / per_head) + i % per_head * 8);
+    const int head_bits = p.head_dim == 64 ? 3 : p.head_dim == 128 ? 4 : 5;      // a head's vectors
+    const int per_cta = (kAnyChannels / 8) >> head_bits, first = blockIdx.y * per_cta;
+    const int vectors = min(per_cta, p.nq + p.nk + p.nv - first) << head_bits;
+    for (int i = threadIdx.x; i < vectors; i += blockDim.x)
+        send_for(rows + i, source<KIND>(p, t, first + (i >> head_bits)) + (i & ((1 << head_bits) - 1)) * 8);
     asm volatile("cp.async.commit_group;" ::: "memory");
     const int64_t position = p.positions[t];
     for (int i = threadIdx.x; i < p.pairs; i += blockDim.x)
-        turns[i] = turn_of(p.turns[i], position, p.inverse != 0, p.factor);
+        turns[i % 8][i / 8] = turn_of(p.turns[i], position, p.inverse != 0, p.factor);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    for (int i = threadIdx.x; i < heads * per_head; i += blockDim.x) {
-        const int c0 = i % per_head * 8;
-        int h = first + i / per_head;
+    // a thread's channels are the same in all its heads: blockDim.x is a multiple of a head's vectors
+    const int c0 = (threadIdx.x & ((1 << head_bits) - 1)) * 8;
+    // for each channel its partner (itself: not turned), and its own and the partner's factor
+    int partner[8];
+    float2 cs[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = c0 + j, i = c < p.pairs ? c : c - p.pairs;
+        const bool turned = c < 2 * p.pairs;
+        partner[j] = turned ? (c < p.pairs ? c + p.pairs : i) : c;
+        cs[j] = turned ? turns[i & 7][i >> 3] : make_float2(1.f, 0.f);
+        if (c < p.pairs) cs[j].y = -cs[j].y;
+    }
+    for (int i = threadIdx.x; i < vectors; i += blockDim.x) {
+        const int h = first + (i >> head_bits);
         const uint4 own = rows[i];
         const uint32_t w[4] = {own.x, own.y, own.z, own.w};
-        const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(rows) + (i / per_head) * p.head_dim;
+        const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(rows) + (i >> head_bits) * p.head_dim;
         float2 y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = floats_of(w[j]);
-            if (h >= p.nq + p.nk) continue;          // values are not turned
-            float *two = &y[j].x;
+        for (int j = 0; j < 4; ++j) y[j] = floats_of(w[j]);
+        if (h < p.nq + p.nk) {                       // values are not turned
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = c0 + 2 * j + k;
-                if (c >= 2 * p.pairs) continue;
-                const bool second = c >= p.pairs;
-                const float2 cs = turns[second ? c - p.pairs : c];
-                const float other = __bfloat162float(row[second ? c - p.pairs : c + p.pairs]);
-                two[k] = __fmaf_rn(two[k], cs.x, second ? other * cs.y : -other * cs.y);
+            for (int j = 0; j < 8; ++j) {
+                float &x = j % 2 ? y[j / 2].y : y[j / 2].x;
+                const float turn = __fmaf_rn(x, cs[j].x, __bfloat162float(row[partner[j]]) * cs[j].y);
+                if (partner[j] != c0 + j) x = turn;
             }
         }
         if (KIND == kRope || h < p.nq) {
