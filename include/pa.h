@@ -514,7 +514,8 @@ int pa_rope(void *q_out, void *k_out, const void *q, const void *k, const int64_
  * pa_rope_append -- pa_rope and pa_write_cache in one pass: q turned into q_out, k turned
  * into the cache at slot_mapping, v into the cache as it is.  An FP8 pool takes the E4M3
  * codes of the turned fp32 values (k_scale, v_scale as in pa_write_cache).
- *   q, k, v, q_out  as in pa_rope (num_q_heads may be 0; k, v share num_kv_heads)
+ *   q, k, v, q_out  as in pa_rope (num_q_heads may be 0; k, v share num_kv_heads); none of
+ *                   them lies in the caches
  *   slot_mapping    [num_tokens] int64; a token whose slot is negative is padding: nothing of
  *                   it is written, its row of q_out included.  A slot outside the pool is
  *                   treated the same and sets PA_ERR_DEVICE_BOUNDS.
@@ -579,16 +580,17 @@ int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, const void *l
  *   - the L % block_size rows of the page that its next token goes to become p's rows, bit
  *     for bit.  That page, block_tables[j][L / block_size], must be named by no other
  *     sequence; the entry stays.
- * All sequences move at once: p's rows and ids are those before the call.  parents < 0 (-1)
- * or the sequence itself leaves it as it is.  After a prompt whose pages the beams share,
+ * All sequences move at once: p's rows and ids are those before the call.  A sequence that
+ * is its own parent stays as it is.  So does one with parents -1, which is out of the
+ * search: its page may be another's by now.  After a prompt whose pages the beams share,
  * parents 0 and a page of its own at L / block_size make each beam's copy of the last one.
  *   pools         HOST array of num_pools device pointers, as in pa_tree_commit
  *   block_tables  [num_requests * num_beams][max_blocks_per_seq], changed in place
  *   seq_lens      [num_requests * num_beams]; parents [num_requests][num_beams] int32
  * A sequence is left as it is and PA_ERR_DEVICE_BOUNDS set where its parent is no beam of
  * the request or has another length, the length is negative or passes the table, or (unless L %
- * block_size is 0) its own or its parent's page is not in the pool or its own is another
- * beam's too.  Pages that no sequence names any more are the caller's to find.  One launch
+ * block_size is 0) its own or its parent's page is not in the pool or its own is that of
+ * another beam in the search.  Pages that no sequence names any more are the caller's to find.  One launch
  * per 128 pools.
  */
 int pa_beam_reorder(void *const *pools, int num_pools, int32_t *block_tables,

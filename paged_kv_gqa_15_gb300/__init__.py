@@ -696,7 +696,7 @@ def pa_beam_select(scores, beams, tokens, logits, cum_scores, workspace, finishe
 def pa_beam_reorder(key_caches, value_caches, block_tables, seq_lens, parents, layout="HND",
                     stream=None):
     """The cache follows the chosen beams: sequence j of each request goes on from what sequence
-    parents[r, j] (int32 [R, B]; negative: left as it is) held, in every layer's pools.  The full
+    parents[r, j] (int32 [R, B]; -1: out of the search) held, in every layer's pools.  The full
     pages' ids move in block_tables [R * B, blocks] (in place), the rows of the page that the next
     token goes to, each sequence's own, are copied.  Layers that share a cache list it once."""
     pools, (nb, nkv, bs, hd), (sb, sh, st) = _all_pools(key_caches, value_caches, layout)

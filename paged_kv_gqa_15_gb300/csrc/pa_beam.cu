@@ -290,15 +290,15 @@ __device__ __forceinline__ float float_of(uint32_t ordered_bits) {
 enum { kOut = 0, kLive = 1, kFinished = 2 };
 
 struct PickSpace {
-    uint64_t key[kMostCandidates];           // the candidates
-    uint32_t place[kMostCandidates];
-    int count[2];                            // how many, among the chunks and among the elements
+    uint64_t key[2][kMostCandidates];        // the candidates among the chunks, among the elements
+    uint32_t place[2][kMostCandidates];
+    int count[2];
     __align__(16) uint32_t groups[kGroups];
     uint32_t bar;
     uint32_t reach;                          // largest |hi| of the beams, as bits
     int live;                                // beams whose chunks take part
     uint64_t chosen_key[PA_MAX_BEAM_OUT];
-    uint32_t chosen[PA_MAX_BEAM_OUT], from[PA_MAX_BEAM_OUT];
+    uint32_t chosen[PA_MAX_BEAM_OUT], from[PA_MAX_BEAM_OUT];   // the first pairs, the chunks that hold them
     Ranked warps[kPickThreads / 32];
     Offset offset[PA_MAX_BEAMS];
     float2 shift[PA_MAX_BEAMS];              // of a live beam: (top, hi); of the others (0, -inf)
@@ -307,7 +307,7 @@ struct PickSpace {
 
 __device__ __forceinline__ void note(PickSpace &sp, int stage, uint64_t key, uint32_t place) {
     const int at = atomicAdd(&sp.count[stage], 1);
-    if (at < kMostCandidates) sp.key[at] = key, sp.place[at] = place;
+    if (at < kMostCandidates) sp.key[stage][at] = key, sp.place[stage][at] = place;
 }
 
 // The `most` first of the candidates into sp.chosen, in order; returns how many there are.  Each warp
@@ -319,9 +319,9 @@ __device__ int rank(PickSpace &sp, int stage, int n, int most, const Item &item)
     const int count = sp.count[stage];
     if (count <= kMostCandidates) {
         for (int i = warp; i < count; i += kPickThreads / 32) {
-            const Ranked mine = {sp.key[i], sp.place[i]};
+            const Ranked mine = {sp.key[stage][i], sp.place[stage][i]};
             int r = 0;
-            for (int j = lane; j < count; j += 32) r += before({sp.key[j], sp.place[j]}, mine);
+            for (int j = lane; j < count; j += 32) r += before({sp.key[stage][j], sp.place[stage][j]}, mine);
             r = __reduce_add_sync(0xffffffffu, r);
             if (lane == 0 && r < most) sp.chosen_key[r] = mine.key, sp.chosen[r] = mine.place;
         }
@@ -425,15 +425,16 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     if (kind != kOut) atomicMax(&sp.reach, __float_as_uint(fabsf(offset.hi)));
 }
 
-// One CTA a request.  The num_out first chunks by their maxima, then the num_out first of those chunks'
-// elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings, off by 2^-23
+// One CTA a request.  The chunks that can be among the num_out first by their maxima, then the num_out first of
+// those chunks' elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings, off by 2^-23
 // of |score| + 2 |hi| at most.  Every thread belongs to one of a few groups, and the num_out-th largest of
 // the groups' best scores is a bar that num_out items reach; an item below it by more than both may be off
 // (2^-20 of |bar| + |hi|) cannot be among the first.  The few others get their key and are ranked by
 // counting.  There are twice as many groups as num_out, at least a warp's lanes, so that the bar is seldom
-// much below the num_out-th best item.  Elements are measured against the score of the last chosen chunk.
+// much below the num_out-th best item.  The chunks' bar holds for the elements too.
 //
-// Bound by latency: six barriers, three loads in a row (runs, logits, and the chunk maxima beside them).
+// Bound by latency: seven barriers, two loads in a row (the runs with the chunk maxima, the logits).  Shared
+// memory is read side by side or by all alike, and the code is short: it runs once, from a cold cache.
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -504,17 +505,21 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     }
     if (ends && sp.offset[tid].hi >= low) note(sp, 0, key_of(0.f, sp.offset[tid]), tid * chunks);
     __syncthreads();
-    const int kept = rank(sp, 0, n, most, chunk);
-    // the candidates and the chosen make room for the elements
-    const uint32_t bar = kept == most ? head_of(sp.chosen_key[most - 1]) : 0;
-    if (tid < kept) sp.from[tid] = sp.chosen[tid];
-    __syncthreads();
-    low = below(bar);
+    // the candidates themselves while they are few, else the first of them
+    int kept = sp.count[0];
+    const uint32_t *from = sp.place[0];
+    if (kept > PA_MAX_BEAM_OUT) {
+        kept = rank(sp, 0, n, most, chunk);
+        from = sp.from;
+        if (tid < kept) sp.from[tid] = sp.chosen[tid];
+        if (kept == most) low = fmaxf(low, below(head_of(sp.chosen_key[most - 1])));
+        __syncthreads();                             // sp.chosen is used again
+    }
     // a pair's place in the order: beam, then token
     static_assert(PA_MAX_BEAM_VOCAB <= 1 << 24 && PA_MAX_BEAMS <= 1 << 8, "a beam and a token in 32 bits");
     const T *logits = static_cast<const T *>(p.logits) + row0 * p.row_stride;
     auto element = [&](int i) -> Ranked {
-        const int c = static_cast<int>(sp.from[i / kChunk]), b = beam_of(c);
+        const int c = static_cast<int>(from[i / kChunk]), b = beam_of(c);
         const uint32_t beam = static_cast<uint32_t>(b) << 24;
         if (sp.kind[b] == kFinished) return {i % kChunk ? 0 : key_of(0.f, sp.offset[b]), beam | p.end_token};
         const int token = (c - b * chunks) * kChunk + i % kChunk;
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     };
     // the scores of a lane's elements of chosen chunk k, and its beam's one item if that is finished
     auto scores_of = [&](int k, float (&y)[kChunk / 32]) {
-        const int c = static_cast<int>(sp.from[k]), b = beam_of(c);
+        const int c = static_cast<int>(from[k]), b = beam_of(c);
         const float2 shift = sp.shift[b];
         const int token = (c - b * chunks) * kChunk + lane;
         const T *row = logits + b * p.row_stride + token;
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     };
     float y[kChunk / 32];
     if (sp.live * chunks < 4 * most) {
-        // few chunks to choose from: the last chosen one says little, so the elements get a bar of their own
+        // of few chunks, the maximum of the num_out-th says little: the elements get a bar of their own
         if (tid < groups) sp.groups[tid] = 0;
         if (tid == 0) sp.bar = 0;
         __syncthreads();
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
             if (y[i] > -INFINITY && y[i] >= low) passed |= 1u << i;
         for (; passed; passed &= passed - 1) {
             const Ranked r = element(k * kChunk + 32 * (__ffs(passed) - 1) + lane);
-            if (r.key && head_of(r.key) >= bar) note(sp, 1, r.key, r.place);
+            if (r.key) note(sp, 1, r.key, r.place);
         }
     }
     __syncthreads();

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ int parent[BEAMS], page[BEAMS], len[BEAMS];
+    __shared__ bool searched[BEAMS];                // in the search: its page is its own
     const int tid = threadIdx.x, n = p.num_beams;
     const int64_t slot0 = static_cast<int64_t>(blockIdx.y) * n;
     int32_t *tables = p.block_tables + slot0 * p.max_blocks;
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
     if (tid < n) {
         const int L = p.seq_lens[slot0 + tid];
         len[tid] = L;
+        searched[tid] = p.parents[slot0 + tid] >= 0;
         page[tid] = -1;
         if (L >= 0 && L / kBlockSize < p.max_blocks) {
             const int id = tables[static_cast<int64_t>(tid) * p.max_blocks + L / kBlockSize];
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
             bad = L < 0 || L > p.max_blocks * kBlockSize || len[from] != L;
             if (!bad && L % kBlockSize) {
                 bad = page[tid] < 0 || page[from] < 0;
-                for (int i = 0; i < n; ++i) bad |= i != tid && page[i] == page[tid];
+                for (int i = 0; i < n; ++i) bad |= i != tid && searched[i] && page[i] == page[tid];
             }
             moves = !bad;
         }

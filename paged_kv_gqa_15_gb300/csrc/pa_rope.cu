@@ -39,6 +39,11 @@ struct Rows {                   // [token][head][head_dim] by element strides
     int64_t token, head;
 };
 
+// A division by scale: factors a little under and over 1 / scale.
+struct Quotient {
+    float scale, low, high;
+};
+
 struct RopeParams {
     Rows q, k, v, q_out, k_out;          // v: append only; k_out: pa_rope only
     uint8_t *k_cache, *v_cache;
@@ -46,8 +51,8 @@ struct RopeParams {
     const uint64_t *turns;
     int64_t tokens, num_blocks, s_block, s_head, s_token;
     int nq, nk, nv, head_dim, pairs, inverse;
-    float factor, k_scale, v_scale;
-    float k_inverse, v_inverse;          // 1 / scale where that is exact (a power of two), else 0
+    float factor;
+    Quotient k_by, v_by;
     int *status;
 };
 
@@ -96,14 +101,26 @@ __device__ __forceinline__ uint32_t bf16_of(float2 x) {
     return w;
 }
 
-// The E4M3 codes of x / scale: the quotient in fp32, to nearest even, saturated at +-448.  A scale that is a
-// power of two has its reciprocal in inverse (else 0): the product is that quotient.
-__device__ __forceinline__ uint32_t codes_of(float2 x, float scale, float inverse) {
-    const float2 y = inverse != 0.f ? split(mul2(pair(x.x, x.y), pair(inverse, inverse)))
-                                    : make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale));
-    uint16_t w;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(y.y), "f"(y.x));
+__device__ __forceinline__ uint32_t e4m3_of(float2 x) {
+    uint16_t w;                          // the first source goes to the upper byte; saturated at +-448
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w) : "f"(x.y), "f"(x.x));
     return w;
+}
+
+// The E4M3 codes of x / scale, the quotient rounded to fp32 first, as the cache write makes them.  The
+// factors lie 2^-21 to either side of 1 / scale, so the products enclose that quotient: where both have one
+// code it is the quotient's, else (one pair in 2^15) the division decides.  A power of two has its
+// reciprocal in both.
+//   Here: the lower product's codes; bits in `unsure` where the other's differ.
+__device__ __forceinline__ uint32_t codes_of(float2 x, const Quotient &by, uint32_t &unsure) {
+    const uint64_t two = pair(x.x, x.y);
+    const uint32_t w = e4m3_of(split(mul2(two, pair(by.low, by.low))));
+    unsure |= w ^ e4m3_of(split(mul2(two, pair(by.high, by.high))));
+    return w;
+}
+
+__device__ __forceinline__ uint8_t code_of_quotient(float x, float scale) {
+    return static_cast<uint8_t>(e4m3_of(make_float2(__fdiv_rn(x, scale), 0.f)));
 }
 
 __device__ __forceinline__ const __nv_bfloat16 *row_of(const Rows &r, int64_t t, int h) {
@@ -148,7 +165,8 @@ struct Unit {
 // Half layout with pairs a multiple of 8, and every interleaved one.  Grid: x = tokens (each CTA takes every
 // gridDim.x-th), y = groups of heads, kUnits * blockDim.x units each.  A thread's units lie in different
 // heads but at the same channels, so that they share the token's place and angles.
-template <int KIND, bool INTERLEAVED>
+// PARTIAL: a vector may hold interleaved pairs of which some turn and some do not.
+template <int KIND, bool INTERLEAVED, bool PARTIAL>
 __global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -237,38 +255,66 @@ __global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) rope_kernel(const __g
             if (!unit[k].live || at < 0) continue;
             const uint4 a4 = *mine_at(stage, k), b4 = mine_at(stage, k)[threads];
             uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
-            const bool codes = KIND == kAppendFp8 && !unit[k].to_rows;
+            const bool codes = KIND == kAppendFp8 && !unit[k].to_rows, turned = unit[k].turned;
+            float2 x[4], y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // two pairs: halves apart (a[j], b[j]), or the neighbours in two words of a or b
-                uint32_t &w0 = !INTERLEAVED ? a[j] : j < 2 ? a[2 * j] : b[2 * j - 4];
-                uint32_t &w1 = !INTERLEAVED ? b[j] : j < 2 ? a[2 * j + 1] : b[2 * j - 3];
-                float2 x = floats_of(w0), y = floats_of(w1);
-                if (unit[k].turned) {
-                    const int of_pair = !INTERLEAVED ? 8 * u + 2 * j : (j < 2 ? 4 * u : p.head_dim / 4 + 4 * u) + j % 2 * 2;
-                    const float4 cs = turns[buffer][turns_at(of_pair)];
-                    if (INTERLEAVED) {
-                        const float2 x0 = x, y0 = y;
-                        if (of_pair < p.pairs)
-                            x = make_float2(__fmaf_rn(x0.x, cs.x, -x0.y * cs.z), __fmaf_rn(x0.y, cs.x, x0.x * cs.z));
-                        if (of_pair + 1 < p.pairs)
-                            y = make_float2(__fmaf_rn(y0.x, cs.y, -y0.y * cs.w), __fmaf_rn(y0.y, cs.y, y0.x * cs.w));
-                    } else {
-                        const uint64_t x2 = pair(x.x, x.y), y2 = pair(y.x, y.y), c2 = pair(cs.x, cs.y);
-                        const uint64_t s2 = pair(cs.z, cs.w), n2 = pair(-cs.z, -cs.w);
-                        x = split(fma2(x2, c2, mul2(y2, n2)));
-                        y = split(fma2(y2, c2, mul2(x2, s2)));
-                    }
-                    if (!codes) w0 = bf16_of(x), w1 = bf16_of(y);
-                }
-                if (codes) {
-                    const float scale = unit[k].is_k ? p.k_scale : p.v_scale;
-                    const float inverse = unit[k].is_k ? p.k_inverse : p.v_inverse;
-                    w0 = codes_of(x, scale, inverse), w1 = codes_of(y, scale, inverse);
+            for (int j = 0; j < 4; ++j) x[j] = floats_of(a[j]), y[j] = floats_of(b[j]);
+            if (!INTERLEAVED && turned) {
+                // two pairs: one half of each in a word of a, the other in that of b
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 cs = turns[buffer][turns_at(8 * u + 2 * j)];
+                    const uint64_t x2 = pair(x[j].x, x[j].y), y2 = pair(y[j].x, y[j].y), c2 = pair(cs.x, cs.y);
+                    const uint64_t s2 = pair(cs.z, cs.w), n2 = pair(-cs.z, -cs.w);
+                    x[j] = split(fma2(x2, c2, mul2(y2, n2)));
+                    y[j] = split(fma2(y2, c2, mul2(x2, s2)));
                 }
             }
-            uint8_t *to = unit[k].to + (unit[k].to_rows ? static_cast<int64_t>(t) * unit[k].to_token * 2 : at * kElem);
+            if (INTERLEAVED && turned) {
+                // a pair a word
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int first = c0 / 2 + v * (apart / 2), pairs = p.pairs - first;
+                    if (pairs <= 0) continue;
+                    const float4 cs[2] = {turns[buffer][turns_at(first)], turns[buffer][turns_at(first + 2)]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (PARTIAL && j >= pairs) continue;
+                        float2 &z = v ? y[j] : x[j];
+                        const float c = j % 2 ? cs[j / 2].y : cs[j / 2].x, s = j % 2 ? cs[j / 2].w : cs[j / 2].z;
+                        z = make_float2(__fmaf_rn(z.x, c, -z.y * s), __fmaf_rn(z.y, c, z.x * s));
+                    }
+                }
+            }
+            uint32_t unsure = 0;
             if (codes) {
+                const Quotient &by = unit[k].is_k ? p.k_by : p.v_by;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = codes_of(x[j], by, unsure), b[j] = codes_of(y[j], by, unsure);
+            } else if (turned) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = bf16_of(x[j]), b[j] = bf16_of(y[j]);
+            }
+            uint8_t *to = unit[k].to + (unit[k].to_rows ? static_cast<int64_t>(t) * unit[k].to_token * 2 : at * kElem);
+            if (codes && unsure) {
+                // seldom: one channel after another, its value once more and divided
+                const float scale = unit[k].is_k ? p.k_by.scale : p.v_by.scale;
+                const __nv_bfloat16 *near = reinterpret_cast<const __nv_bfloat16 *>(mine_at(stage, k));
+                const __nv_bfloat16 *far = near + 8 * threads;
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e) {
+                    const bool back = INTERLEAVED ? e & 1 : e >= 8;        // the pair's second channel
+                    const int of_pair = INTERLEAVED ? (e < 8 ? c0 / 2 : c1 / 2 - 4) + e / 2 : 8 * u + e % 8;
+                    float x = __bfloat162float(e < 8 ? near[e] : far[e - 8]);
+                    if (unit[k].turned && of_pair < p.pairs) {
+                        const int o = INTERLEAVED ? e ^ 1 : e ^ 8;
+                        const float y = __bfloat162float(o < 8 ? near[o] : far[o - 8]);
+                        const float *cs = reinterpret_cast<const float *>(&turns[buffer][turns_at(of_pair & ~1)]) + of_pair % 2;
+                        x = __fmaf_rn(x, cs[0], __fmul_rn(y, back ? cs[2] : -cs[2]));
+                    }
+                    to[e < 8 ? e : apart + e - 8] = code_of_quotient(x, scale);
+                }
+            } else if (codes) {
                 *reinterpret_cast<uint2 *>(to) = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
                 *reinterpret_cast<uint2 *>(to + apart) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
             } else {
@@ -344,11 +390,15 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ R
         uint8_t *pool = is_k ? p.k_cache : p.v_cache;
         const int64_t to = at + (h - p.nq - (is_k ? 0 : p.nk)) * p.s_head + c0;
         if (KIND == kAppendFp8) {
-            const float scale = is_k ? p.k_scale : p.v_scale, inverse = is_k ? p.k_inverse : p.v_inverse;
-            uint32_t c[4];
+            const Quotient &by = is_k ? p.k_by : p.v_by;
+            uint32_t c[4], unsure = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = codes_of(y[j], scale, inverse);
+            for (int j = 0; j < 4; ++j) c[j] = codes_of(y[j], by, unsure);
             *reinterpret_cast<uint2 *>(pool + to) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+            if (unsure)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    pool[to + j] = code_of_quotient(j % 2 ? y[j / 2].y : y[j / 2].x, by.scale);
         } else if (is_k) {
             *reinterpret_cast<uint4 *>(pool + to * 2) =
                 make_uint4(bf16_of(y[0]), bf16_of(y[1]), bf16_of(y[2]), bf16_of(y[3]));
@@ -374,8 +424,9 @@ cudaError_t launch_rope(const RopeParams &p, bool interleaved, cudaStream_t stre
     const int64_t wave = (152 * per_sm + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(p.tokens < wave ? p.tokens : wave), static_cast<unsigned>(groups));
     const size_t rows = static_cast<size_t>(kStages) * kUnits * 2 * threads * sizeof(uint4);
-    return interleaved ? launch_after(rope_kernel<KIND, true>, grid, threads, p, stream, rows)
-                       : launch_after(rope_kernel<KIND, false>, grid, threads, p, stream, rows);
+    if (!interleaved) return launch_after(rope_kernel<KIND, false, false>, grid, threads, p, stream, rows);
+    return p.pairs % 4 ? launch_after(rope_kernel<KIND, true, true>, grid, threads, p, stream, rows)
+                       : launch_after(rope_kernel<KIND, true, false>, grid, threads, p, stream, rows);
 }
 
 // ---- argument checks --------------------------------------------------------------------
@@ -446,10 +497,15 @@ int check_common(int64_t num_tokens, int nq, int nk, int head_dim, int rotary_di
     return PA_OK;
 }
 
-// 1 / scale of a power of two whose reciprocal is a normal fp32 too, else 0.
-float exact_inverse(float scale) {
+// Outside the range where the factors and products are sure to be normal numbers, factors that never
+// agree: every quotient is divided.
+Quotient quotient_by(float scale) {
     int n;
-    return std::frexp(scale, &n) == 0.5f && n > -125 && n < 127 ? 1.f / scale : 0.f;
+    const bool exact = std::frexp(scale, &n) == 0.5f;
+    if (!(n > -100 && n < 100)) return {scale, -1.f, 1.f};
+    const double inverse = 1.0 / scale;
+    return {scale, static_cast<float>(exact ? inverse : inverse * (1 - 0x1p-21)),
+            static_cast<float>(exact ? inverse : inverse * (1 + 0x1p-21))};
 }
 
 // Number of a pair that makes `turns` full turns within `len` positions, as a real number.
@@ -635,10 +691,8 @@ extern "C" int pa_rope_append(void *q_out, const void *q, const void *k, const v
     p.head_dim = head_dim;
     p.pairs = rotary_dim / 2;
     p.factor = attention_factor;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.k_inverse = exact_inverse(k_scale);
-    p.v_inverse = exact_inverse(v_scale);
+    p.k_by = quotient_by(k_scale);
+    p.v_by = quotient_by(v_scale);
     rc = api_status_ptr(&p.status);
     if (rc) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -132,6 +132,13 @@ def test_moves_that_cannot_be_made_are_flagged():
     run(length(1, 2147483647), [0, 1])
 
 
+def test_pages_of_a_beam_out_of_the_search_may_be_anothers():
+    bits, pools, table, lens, _ = make(1, 4, [37], 2, 64, 1, seed=10)
+    table[3] = table[0]                              # retired; its pages have gone to the first
+    check(bits, pools, table, lens, np.array([[1, 2, 0, -1]]))
+    assert pa.device_status() == 0
+
+
 def test_shared_prompt_becomes_a_beam_each():
     """After one prefill: every beam's table names the prompt's pages and, for the page that its next
     token goes to, one of its own; parents 0 give each its copy of the rows there."""

@@ -229,6 +229,26 @@ def test_append_at_position_zero_is_the_cache_write():
         assert torch.equal(vc.view(torch.uint8), vw.view(torch.uint8)) and torch.equal(q_out, q)
 
 
+@pytest.mark.parametrize("scale", [0.0123, 0.1, 1 / 3, 3.0, 2.0 ** -9, 7e-5, 1.0, 447.0, 1e-38, 3e38, 2.0 ** -120])
+def test_codes_are_those_of_the_division(scale):
+    """Every bf16 value, at position 0: the codes of the cache write, which divides; borders between
+    codes and quotients next to them among them."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).to(DEV)
+    x = bits.view(512, 2, 64).contiguous()
+    finite = torch.isfinite(x.float())
+    turns, _ = pa.rope_table(64)
+    for interleaved, table in ((False, turns), (True, turns), (False, pa.rope_table(6)[0])):
+        kc, vc, kw, vw = (torch.zeros((32, 2, 16, 64), dtype=torch.uint8, device=DEV) for _ in range(4))
+        y = torch.where(finite, x, torch.zeros_like(x))      # a pair of infinity and 0 turns to NaN
+        slots = torch.arange(512, device=DEV)
+        pa.pa_rope_append(None, None, y, x, kc, vc, slots, torch.zeros_like(slots), table, interleaved=interleaved,
+                          k_scale=scale, v_scale=scale)
+        pa.pa_write_cache(y, x, kw, vw, slots, k_scale=scale, v_scale=scale)
+        differ = kc != kw                                    # -0 turned is +0 where its partner is not negative
+        assert ((kc | kw)[differ] == 0x80).all()
+        assert torch.equal(vc, vw)
+
+
 def test_slots_outside_the_pool_are_flagged():
     kc, vc = pools(3, 2, 64, False, "HND", 51)
     before = kc.clone(), vc.clone()
