@@ -555,10 +555,10 @@ size_t pa_beam_select_workspace_size(int num_requests, int num_beams, int vocab)
  *   logits      [num_requests * num_beams] rows of vocab values of logits_dtype, stride_row
  *               elements apart (rows of any alignment; multiples of 16 bytes are faster).
  *               -inf rules a token out.
- *   cum_scores  [num_requests][num_beams] fp32.  -inf takes a beam out: its logits are not
- *               read (a first step has one beam at 0 and the others at -inf).
+ *   cum_scores  [num_requests][num_beams] fp32.  -inf takes a beam out, whatever its logits
+ *               hold (a first step has one beam at 0 and the others at -inf).
  *   finished    [num_requests][num_beams] bytes, or NULL.  A beam with a nonzero flag offers
- *               one pair, end_token at the score cum_scores; its logits are not read.
+ *               one pair, end_token at the score cum_scores, whatever its logits hold.
  *   scores      [num_requests][num_out] fp32, beams and tokens [num_requests][num_out] int32,
  *               written whole: behind the pairs there are, -inf, -1 and -1.  A pair whose
  *               score rounds to -inf is none.

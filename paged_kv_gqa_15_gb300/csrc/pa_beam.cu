@@ -97,6 +97,16 @@ __device__ __forceinline__ bool row_is_read(const BeamParams &p, int64_t row) {
     return p.cum[row] > -INFINITY && !(p.finished && p.finished[row]);
 }
 
+// 16 bytes that are read once.  (Volatile: the first of them are asked for before the warp knows that it
+// has to read them.)
+__device__ __forceinline__ uint4 stream(const uint4 *from) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(from));
+    return v;
+}
+
 // A lane's eight logits of one chunk as they lie in memory: adjacent ones where rows start at 16 bytes,
 // else every 32nd; -inf past the row's end.
 template <typename T>
@@ -109,18 +119,18 @@ struct Eight<__nv_bfloat16> {
     // the chunk that starts at `chunk`, of which `left` logits are in the row
     template <bool VECTORS, bool WHOLE>
     __device__ __forceinline__ void load(const __nv_bfloat16 *chunk, int left, int lane) {
-        if (VECTORS && WHOLE) {
-            v = __ldg(reinterpret_cast<const uint4 *>(chunk) + lane);
-            return;
-        }
-        const uint16_t *bits = reinterpret_cast<const uint16_t *>(chunk);
-        uint32_t w[8];
+        if constexpr (VECTORS && WHOLE) {
+            v = stream(reinterpret_cast<const uint4 *>(chunk) + lane);
+        } else {
+            const uint16_t *bits = reinterpret_cast<const uint16_t *>(chunk);
+            uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = VECTORS ? 8 * lane + i : lane + 32 * i;
-            w[i] = WHOLE || c < left ? __ldg(bits + c) : 0xff80u;
+            for (int i = 0; i < 8; ++i) {
+                const int c = VECTORS ? 8 * lane + i : lane + 32 * i;
+                w[i] = WHOLE || c < left ? __ldg(bits + c) : 0xff80u;
+            }
+            v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
         }
-        v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
     __device__ __forceinline__ float top() const {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
@@ -139,16 +149,20 @@ struct Eight<float> {
     float4 v[2];
     template <bool VECTORS, bool WHOLE>
     __device__ __forceinline__ void load(const float *chunk, int left, int lane) {
-        if (VECTORS && WHOLE) {
-            v[0] = __ldg(reinterpret_cast<const float4 *>(chunk) + lane);
-            v[1] = __ldg(reinterpret_cast<const float4 *>(chunk) + lane + 32);
-            return;
-        }
         float x[8];
+        if constexpr (VECTORS && WHOLE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = VECTORS ? 4 * lane + i % 4 + i / 4 * 128 : lane + 32 * i;
-            x[i] = WHOLE || c < left ? __ldg(chunk + c) : -INFINITY;
+            for (int i = 0; i < 2; ++i) {
+                const uint4 w = stream(reinterpret_cast<const uint4 *>(chunk) + lane + 32 * i);
+                x[4 * i] = __uint_as_float(w.x), x[4 * i + 1] = __uint_as_float(w.y);
+                x[4 * i + 2] = __uint_as_float(w.z), x[4 * i + 3] = __uint_as_float(w.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = VECTORS ? 4 * lane + i % 4 + i / 4 * 128 : lane + 32 * i;
+                x[i] = WHOLE || c < left ? __ldg(chunk + c) : -INFINITY;
+            }
         }
         v[0] = make_float4(x[0], x[1], x[2], x[3]);
         v[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     const int w = blockIdx.x * (kScanThreads / 32) + threadIdx.x / 32;
     const int row = w / p.num_runs, run = w - row * p.num_runs;
-    if (row >= p.num_requests * p.num_beams || !row_is_read(p, row)) return;
+    if (row >= p.num_requests * p.num_beams) return;
     const T *logits = static_cast<const T *>(p.logits) + row * p.row_stride;
     float *best = p.chunk_max + static_cast<int64_t>(row) * p.chunks;
     const int c_end = min(p.chunks, (run + 1) * p.run_chunks);
@@ -203,7 +217,8 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         for (int a = 0; a < kAhead; ++a) to[a].template load<VECTORS, true>(from + a * kChunk, kChunk, lane);
         from += kAhead * kChunk;
     };
-    if (groups > 0) fetch(x);
+    if (groups > 0) fetch(x);                    // beside the row's cum and flag
+    if (!row_is_read(p, row)) return;
 #pragma unroll 2
     for (int g = 0; g < groups; ++g, c += kAhead) {
         if (g + 1 < groups) fetch(next);
