@@ -1,8 +1,8 @@
 // pa_beam.cu -- beam search's selection: per request the K best of all (beam, token) pairs by
 //   score(b, t) = cum[b] + x[b][t] - log sum_t exp x[b][t].
 //
-// Two kernels.  The scan reads every live row once: a warp takes a run of 256-element chunks, keeps the
-// run's maximum m and sum of exp(x - m), and writes each chunk's maximum (1 value for 256).  The pick, a CTA
+// Two kernels.  The scan reads every live row once: a warp takes a share of its 256-element chunks (a
+// run), keeps their maximum m and sum of exp(x - m), and writes each chunk's maximum (1 value for 256).  The pick, a CTA
 // per request, joins the runs' sums into each beam's log-sum-exp, ranks the chunks by their maxima, and
 // reads the K best chunks again: the K best elements lie in them (an element outside is outranked by the K
 // maxima of the chunks before its own).
@@ -42,7 +42,7 @@ struct BeamParams {
     float2 *runs;                            // [rows][num_runs]: maximum, sum of exp(x - maximum)
     int64_t row_stride;
     int num_requests, num_beams, vocab, num_out, end_token;
-    int chunks, run_chunks, num_runs;
+    int chunks, num_runs;
     uint64_t per_chunk;                      // 2^40 / chunks, rounded up: i * per_chunk >> 40 is i / chunks
     int *status;
 };
@@ -177,8 +177,9 @@ struct Eight<float> {
     }
 };
 
-// A warp's run: groups of chunks, the next group on its way while one is worked on.  The running maximum
-// is the warp's, so that a group needs one comparison and, seldom, one rescaling.
+// A row's groups of chunks go to num_runs warps in turn, so that they read it side by side; a warp's next
+// group is on its way while it works on one.  The running maximum is the warp's, so that a group needs one
+// comparison and, seldom, one rescaling.
 template <typename T, bool VECTORS>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamParams p) {
     constexpr int kAhead = Eight<T>::kAhead;
@@ -190,10 +191,8 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     if (row >= p.num_requests * p.num_beams) return;
     const T *logits = static_cast<const T *>(p.logits) + row * p.row_stride;
     float *best = p.chunk_max + static_cast<int64_t>(row) * p.chunks;
-    const int c_end = min(p.chunks, (run + 1) * p.run_chunks);
-    int c = run * p.run_chunks;
-    // groups of whole chunks, then what is left chunk by chunk
-    const int whole = min(c_end, p.vocab / kChunk), groups = max(0, whole - c) / kAhead;
+    // groups of whole chunks, shared out in turn; what is left after them is the next warp's
+    const int whole = p.vocab / kChunk, groups = whole / kAhead;
     float m = -INFINITY, s = 0.f, e = 0.f;
     auto rise = [&](float top) {                 // to a larger maximum
         const float f = exp2_approx((m - top) * kLog2e);
@@ -210,18 +209,19 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         }
         return add2(add2(y[0], y[1]), add2(y[2], y[3]));
     };
-    const T *from = logits + static_cast<int64_t>(c) * kChunk;
+    const T *from = logits + run * (kAhead * kChunk);
+    const int step = p.num_runs * (kAhead * kChunk);
     Eight<T> x[kAhead], next[kAhead];
     auto fetch = [&](Eight<T> (&to)[kAhead]) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) to[a].template load<VECTORS, true>(from + a * kChunk, kChunk, lane);
-        from += kAhead * kChunk;
+        from += step;
     };
-    if (groups > 0) fetch(x);                    // beside the row's cum and flag
+    if (run < groups) fetch(x);                  // beside the row's cum and flag
     if (!row_is_read(p, row)) return;
 #pragma unroll 2
-    for (int g = 0; g < groups; ++g, c += kAhead) {
-        if (g + 1 < groups) fetch(next);
+    for (int g = run; g < groups; g += p.num_runs) {
+        if (g + p.num_runs < groups) fetch(next);
         float mine = -INFINITY, top = m;
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
             top = fmaxf(top, t);
             if (lane == a) mine = t;
         }
-        if (lane < kAhead) best[c + lane] = mine;
+        if (lane < kAhead) best[g * kAhead + lane] = mine;
         if (top > m) rise(top);
         const float low = m == -INFINITY ? 0.f : -m;
         uint64_t sum[kAhead];
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) x[a] = next[a];
     }
-    for (; c < c_end; ++c) {
+    for (int c = run == groups % p.num_runs ? groups * kAhead : p.chunks; c < p.chunks; ++c) {
         const T *chunk = logits + static_cast<int64_t>(c) * kChunk;
         if (c < whole)
             x[0].template load<VECTORS, true>(chunk, kChunk, lane);
@@ -679,10 +679,11 @@ extern "C" int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, co
     p.chunks = static_cast<int>(chunks_of(vocab));
     // i < 2^21 chunks of a request and chunks <= 2^16: exact
     p.per_chunk = ((UINT64_C(1) << 40) + p.chunks - 1) / p.chunks;
-    // the rows' chunks in one wave of warps, each row in equal runs
+    // the rows in one wave of warps, a group of chunks each at least
     const int64_t per_row = kScanWarps / rows;
-    p.run_chunks = per_row <= 1 ? p.chunks : static_cast<int>((p.chunks + per_row - 1) / per_row);
-    p.num_runs = (p.chunks + p.run_chunks - 1) / p.run_chunks;
+    const int ahead = logits_dtype == PA_LOGITS_F32 ? Eight<float>::kAhead : Eight<__nv_bfloat16>::kAhead;
+    const int64_t most = (p.chunks + ahead - 1) / ahead;
+    p.num_runs = static_cast<int>(per_row < 1 ? 1 : per_row < most ? per_row : most);
     p.chunk_max = static_cast<float *>(workspace);
     p.runs = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                         round256(static_cast<size_t>(rows) * p.chunks * sizeof(float)));
