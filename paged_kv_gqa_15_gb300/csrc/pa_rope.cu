@@ -11,11 +11,13 @@
 // and costs three integer products instead of fp64 ones.  Its top 32 bits, as an fp32 number of half turns
 // (off by 2^-25 at most), go to sincospi.  Products and sums are fp32, each result is rounded once.
 //
-// Bound by memory: 2 bytes read and 2 written for each channel, a sincos per pair and token.  A CTA serves
-// one token: its threads send for the rows first, work out the token's cos and sin meanwhile (one pair
-// each, shared through shared memory by all heads), then turn and store.  A thread's unit is 16 channels:
-// two 16-byte vectors of the pairs 8 u .. 8 u + 7, so that a thread keeps its eight cos and sin for every
-// head it serves.
+// Bound by memory: 2 bytes read and 2 written for each channel, a sincos per pair and token.  rope_kernel's
+// CTAs go through the tokens with the next one's rows on their way (asynchronous copies into each thread's
+// own shared memory) and its angles worked out, one pair a thread, while one token is turned.  A thread
+// has two units of 16 channels in different heads at the same channels: they share a token's place and
+// angles, and 64 bytes a thread are on their way.  16384 tokens of 32 + 8 heads of 128 channels: 54 us,
+// 336 MB at 93 % of the copy rate; appended with 8 value heads 66 us (91 %), in E4M3 60 us (93 %); 7001
+// tokens of 16 + 8 + 8 heads of 256 in E4M3, 64 channels interleaved: 33 us (90 %).  64 tokens: 1.9 us.
 #include <cmath>
 #include <cstring>
 
@@ -27,7 +29,9 @@ namespace pa {
 namespace {
 
 constexpr int kMaxPairs = 128;
-// rope_kernel: threads of a CTA, their units, tokens whose rows it has in hand or on their way
+// rope_kernel: threads of a CTA, their units, tokens whose rows it has in hand or on their way.  Of 128 to
+// 384 threads, 1 and 2 units, 2 to 4 stages and 3 to 6 CTAs an SM the best for rotations (53.8 to 59 us over
+// the sweep) and E4M3; 5 CTAs of 192 threads append bf16 in 63 us instead of 66, but rotate in 56.
 constexpr int kMaxThreads = 256;
 constexpr int kUnits = 2;
 constexpr int kStages = 2;
@@ -329,7 +333,8 @@ __global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) rope_kernel(const __g
 
 // Half layout with any other number of pairs, where the second channel of a pair starts at any 2 bytes.
 // Grid: x = tokens, y = groups of heads.  The heads' rows lie in shared memory whole; a thread makes eight
-// neighbouring results, each from its own channel and the one it is paired with.
+// neighbouring results, each from its own channel and the one it is paired with.  Bound by its single
+// values from shared memory and by short CTAs: 93 us for 100 of 128 channels of the 16384 tokens above.
 template <int KIND>
 __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
