@@ -53,7 +53,8 @@ SCALINGS = [dict(), dict(scaling="linear", factor=4.0), dict(scaling="ntk", fact
     (33, 16, 8, 256, 256, False), (2, 64, 8, 128, 64, False), (5, 24, 8, 256, 64, True), (4, 7, 1, 64, 16, False),
     (6, 3, 3, 64, 20, False), (6, 3, 3, 64, 20, True), (5, 2, 1, 128, 6, False), (5, 2, 1, 128, 126, True),
     (9, 1, 1, 256, 254, False), (257, 2, 2, 64, 32, False), (3, 96, 8, 256, 256, False),
-    (2, 130, 1, 128, 128, True), (1000, 8, 1, 128, 128, False),
+    (2, 130, 1, 128, 128, True), (1000, 8, 1, 128, 128, False), (7000, 1, 1, 64, 64, True), (2500, 33, 7, 128, 128, False),
+    (1500, 5, 2, 256, 100, False),
 ])
 def test_rows(tokens, nq, nk, hd, rotary, interleaved):
     scaling = SCALINGS[(tokens + nq + rotary) % len(SCALINGS)]
@@ -170,6 +171,9 @@ def rows_of(pool, slots, layout):
     (1, 4, 2, 64, 64, False, "HND"), (1, 0, 1, 256, 256, True, "NHD"), (40, 32, 8, 128, 128, False, "HND"),
     (23, 7, 1, 128, 32, False, "NHD"), (23, 7, 1, 128, 34, False, "HND"), (17, 16, 8, 256, 64, True, "HND"),
     (300, 3, 3, 64, 10, True, "NHD"), (5, 64, 16, 128, 128, False, "HND"), (9, 2, 2, 256, 250, False, "NHD"),
+    # more tokens than CTAs at a time
+    (9001, 2, 1, 64, 64, False, "HND"), (4003, 20, 4, 128, 128, False, "NHD"), (3001, 16, 8, 256, 64, True, "HND"),
+    (2999, 8, 2, 128, 38, True, "HND"),
 ])
 def test_append(tokens, nq, nkv, hd, rotary, interleaved, layout, fp8):
     blocks = tokens // 16 + 3
@@ -185,7 +189,7 @@ def test_append(tokens, nq, nkv, hd, rotary, interleaved, layout, fp8):
     slots = rng.permutation(blocks * 16)[:tokens]
     skip = rng.random(tokens) < 0.2 if tokens > 1 else np.zeros(tokens, bool)
     given = torch.from_numpy(np.where(skip, -1 - rng.integers(0, 3, tokens), slots)).to(DEV)
-    ks, vs = (1 / 64, 1 / 50) if fp8 else (1.0, 1.0)
+    ks, vs = ((1 / 64, 1 / 50) if tokens % 2 else (0.0137, 1 / 32)) if fp8 else (1.0, 1.0)
     q_out = torch.full((tokens, nq, hd), 3.0, dtype=torch.bfloat16, device=DEV)
     before = kc.clone(), vc.clone()
     pa.pa_rope_append(q_out if nq else None, q if nq else None, k, v, kc, vc, given, torch.from_numpy(pos).to(DEV), turns,
