@@ -242,6 +242,26 @@ def test_one_workspace_in_two_replayed_graphs_and_a_side_stream():
     assert all(torch.equal(x, y) for x, y in zip(other, outs[1]))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,B,V", [(1, 4, 32000), (15, 3, 9001), (16, 3, 9001), (2, 32, 2048), (3, 1, 131072), (2, 5, 50001),
+                                   (1, 31, 70), (4, 8, 128000)])
+def test_captured_calls_give_the_same_bits(R, B, V, dtype):
+    """A call outside a capture may take one launch for two; scores, beams and tokens stay the same."""
+    x, cum = normal(R * B, V, R + V, dtype).to(DEV), torch.from_numpy(spread_cum(R, B, V).astype(np.float32)).to(DEV)
+    want = check(x, cum.cpu().numpy(), 9)
+    out = tuple(torch.zeros_like(t) for t in want)
+    space = pa.alloc_workspace(pa.beam_select_workspace_size(R, B, V), DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(x, cum, 9, space=space, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    mine = tuple(torch.zeros_like(t) for t in want)
+    call(x, cum, 9, space=space, out=mine, stream=torch.cuda.default_stream())
+    assert all(torch.equal(a, b) for a, b in zip(mine, want))
+
+
 def test_offsets_past_32_bits():
     """The last of many rows lies more than 2^31 elements behind the first."""
     R, B, V = 9, 32, 1 << 23
