@@ -564,7 +564,8 @@ size_t pa_beam_select_workspace_size(int num_requests, int num_beams, int vocab)
  *               score rounds to -inf is none.
  * A beam whose logits hold NaN or +inf, or whose cum_scores is one of them, offers nothing
  * and sets the PA_ERR_INVALID bit of the device status word.  The outputs share no memory
- * with what the call reads or one another.
+ * with what the call reads or one another.  Two launches; one where there are few requests
+ * and the stream is not being captured, with the same result.
  */
 int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, const void *logits,
                    const float *cum_scores, const uint8_t *finished, int end_token,
