@@ -2,8 +2,8 @@
 //   score(b, t) = cum[b] + x[b][t] - log sum_t exp x[b][t].
 //
 // Two kernels.  The scan reads every live row once: a warp takes a share of its 256-element chunks (a
-// run), keeps their maximum m and sum of exp(x - m), and writes each chunk's maximum (1 value for 256).  The pick, a CTA
-// per request, joins the runs' sums into each beam's log-sum-exp, finds the chunks that can be among the K
+// run), keeps their maximum m and sum of exp(x - m), and writes each chunk's maximum (1 value for 256).  The
+// pick, a CTA per request, joins the runs' sums into each beam's log-sum-exp, finds the chunks that can be among the K
 // best by their maxima, and reads those again: the K best elements lie in them (an element outside is
 // outranked by the K maxima of the chunks before its own).
 //
@@ -450,8 +450,8 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
 }
 
 // One CTA a request.  The chunks that can be among the num_out first by their maxima, then the num_out first of
-// those chunks' elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings, off by 2^-23
-// of |score| + 2 |hi| at most.  Every thread belongs to one of a few groups, and the num_out-th largest of
+// those chunks' elements.  Most items are sorted out by a score in plain fp32, (x - top) + hi: two roundings,
+// and lo left out, off by 2^-23 of |score| + |hi| at most.  Every thread belongs to one of a few groups, and the num_out-th largest of
 // the groups' best scores is a bar that num_out items reach; an item below it by more than both may be off
 // (2^-20 of |bar| + |hi|) cannot be among the first.  The few others get their key and are ranked by
 // counting.  There are twice as many groups as num_out, at least a warp's lanes, so that the bar is seldom
