@@ -112,8 +112,8 @@ __device__ __forceinline__ uint4 stream(const uint4 *from) {
     return v;
 }
 
-// A lane's eight logits of one chunk as they lie in memory: adjacent ones where rows start at 16 bytes,
-// else every 32nd; -inf past the row's end.
+// A lane's eight logits of one chunk: adjacent ones where all rows start at 16 bytes, else pairs of bf16 or
+// single fp32 values a warp's width apart; -inf past the row's end.
 template <typename T>
 struct Eight;
 
@@ -121,21 +121,37 @@ template <>
 struct Eight<__nv_bfloat16> {
     static constexpr int kAhead = 4;             // chunks that a warp reads at once: 64 bytes a lane
     uint4 v;
+    uint32_t last;                               // of a row that starts between two words
     // the chunk that starts at `chunk`, of which `left` logits are in the row
     template <bool VECTORS, bool WHOLE>
     __device__ __forceinline__ void load(const __nv_bfloat16 *chunk, int left, int lane) {
         if constexpr (VECTORS && WHOLE) {
             v = stream(reinterpret_cast<const uint4 *>(chunk) + lane);
+        } else if constexpr (WHOLE) {
+            // whole words; where the chunk starts in the middle of one, lane l has elements 2 l - 1 and 2 l of every
+            // 64, and the chunk's last one is fetched apart
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(chunk) & ~uintptr_t{3}) + lane;
+            v = make_uint4(__ldg(words), __ldg(words + 32), __ldg(words + 64), __ldg(words + 96));
+            if (lane == 0) last = __ldg(reinterpret_cast<const uint16_t *>(chunk) + kChunk - 1);
         } else {
             const uint16_t *bits = reinterpret_cast<const uint16_t *>(chunk);
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int c = VECTORS ? 8 * lane + i : lane + 32 * i;
-                w[i] = WHOLE || c < left ? __ldg(bits + c) : 0xff80u;
+                const int c = VECTORS ? 8 * lane + i : 2 * lane + i % 2 + i / 2 * 64;
+                w[i] = c < left ? __ldg(bits + c) : 0xff80u;
             }
             v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
         }
+    }
+    // of a whole chunk that starts in the middle of a word: elements 2 l and 2 l + 1, when they are there
+    __device__ __forceinline__ void settle(int lane) {
+        const uint32_t w[5] = {v.x, v.y, v.z, v.w, last};
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            u[j] = __funnelshift_r(w[j], __shfl_sync(0xffffffffu, lane ? w[j] : w[j + 1], (lane + 1) & 31), 16);
+        v = make_uint4(u[0], u[1], u[2], u[3]);
     }
     __device__ __forceinline__ float top() const {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
@@ -172,6 +188,7 @@ struct Eight<float> {
         v[0] = make_float4(x[0], x[1], x[2], x[3]);
         v[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
+    __device__ __forceinline__ void settle(int) {}
     __device__ __forceinline__ float top() const {
         return fmaxf(fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w)),
                      fmaxf(fmaxf(v[1].x, v[1].y), fmaxf(v[1].z, v[1].w)));
@@ -191,6 +208,8 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
     const int lane = threadIdx.x & 31;
     const T *logits = static_cast<const T *>(p.logits) + row * p.row_stride;
     float *best = p.chunk_max + static_cast<int64_t>(row) * p.chunks;
+    // whether the row, and so each of its chunks, starts in the middle of a word
+    const bool between = !VECTORS && sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(logits) & 2u);
     // groups of whole chunks, shared out in turn; what is left after them is the next warp's
     const int whole = p.vocab / kChunk, groups = whole / kAhead;
     float m = -INFINITY, s = 0.f, e = 0.f;
@@ -222,6 +241,9 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
 #pragma unroll 2
     for (int g = run; g < groups; g += p.num_runs) {
         if (g + p.num_runs < groups) fetch(next);
+        if (between)
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) x[a].settle(lane);
         float mine = -INFINITY, top = m;
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
@@ -246,10 +268,12 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
     }
     for (int c = run == groups % p.num_runs ? groups * kAhead : p.chunks; c < p.chunks; ++c) {
         const T *chunk = logits + static_cast<int64_t>(c) * kChunk;
-        if (c < whole)
+        if (c < whole) {
             x[0].template load<VECTORS, true>(chunk, kChunk, lane);
-        else
+            if (between) x[0].settle(lane);
+        } else {
             x[0].template load<VECTORS, false>(chunk, p.vocab - c * kChunk, lane);
+        }
         const float top = warp_max(x[0].top());
         if (lane == 0) best[c] = top;
         if (top > m) rise(top);
