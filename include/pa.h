@@ -591,8 +591,9 @@ int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, const void *l
  * A sequence is left as it is and PA_ERR_DEVICE_BOUNDS set where its parent is no beam of
  * the request or has another length, the length is negative or passes the table, or (unless L %
  * block_size is 0) its own or its parent's page is not in the pool or its own is that of
- * another beam in the search.  Pages that no sequence names any more are the caller's to find.  One launch
- * per 128 pools.
+ * another beam in the search.  Pages that no sequence names any more are the caller's to find.
+ * Where pa_block_table_sync keeps the table, the rows of its host copy are to be moved
+ * likewise, or the next upload of one brings back what it was.  One launch per 128 pools.
  */
 int pa_beam_reorder(void *const *pools, int num_pools, int32_t *block_tables,
                     const int32_t *seq_lens, const int32_t *parents, int num_requests,
