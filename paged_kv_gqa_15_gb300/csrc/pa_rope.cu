@@ -16,7 +16,7 @@
 // own shared memory) and its angles worked out, one pair a thread, while one token is turned.  A thread
 // has two units of 16 channels in different heads at the same channels: they share a token's place and
 // angles, and 64 bytes a thread are on their way.  16384 tokens of 32 + 8 heads of 128 channels: 54 us,
-// 336 MB at 93 % of the copy rate; appended with 8 value heads 66 us (91 %), in E4M3 60 us (93 %); 7001
+// 336 MB at 93 % of the copy rate; appended with 8 value heads 64 us (94 %), in E4M3 60 us (93 %); 7001
 // tokens of 16 + 8 + 8 heads of 256 in E4M3, 64 channels interleaved: 33 us (90 %).  64 tokens: 1.9 us.
 #include <cmath>
 #include <cstring>
@@ -28,14 +28,17 @@
 namespace pa {
 namespace {
 
+enum { kRope = 0, kAppend = 1, kAppendFp8 = 2 };
+
 constexpr int kMaxPairs = 128;
 // rope_kernel: threads of a CTA, their units, tokens whose rows it has in hand or on their way.  Of 128 to
-// 384 threads, 1 and 2 units, 2 to 4 stages and 3 to 6 CTAs an SM the best for rotations (53.8 to 59 us over
-// the sweep) and E4M3; 5 CTAs of 192 threads append bf16 in 63 us instead of 66, but rotate in 56.
+// 384 threads, 1 and 2 units and 2 to 4 stages the best.  CTAs of the most threads that an SM holds: 4 for bf16
+// appends (16384 tokens 64.4 us against 66.4 with 3, 12000 46.3 against 48.7; as many at 28 + 4 and 64 + 8
+// heads), 3 for rotations (54.0 against 55.3) and E4M3, which has no registers for 4 (33.4 against 36.3).
 constexpr int kMaxThreads = 256;
 constexpr int kUnits = 2;
 constexpr int kStages = 2;
-constexpr int kCtasPerSm = 3;
+constexpr int ctas_per_sm(int kind) { return kind == kAppend ? 4 : 3; }
 constexpr int kAnyChannels = 8192;           // of rope_any_kernel's CTA
 
 struct Rows {                   // [token][head][head_dim] by element strides
@@ -59,8 +62,6 @@ struct RopeParams {
     Quotient k_by, v_by;
     int *status;
 };
-
-enum { kRope = 0, kAppend = 1, kAppendFp8 = 2 };
 
 __device__ __forceinline__ float2 turn_of(uint64_t frequency, int64_t position, bool inverse, float factor) {
     const uint64_t turns = frequency * static_cast<uint64_t>(position);
@@ -171,7 +172,7 @@ struct Unit {
 // heads but at the same channels, so that they share the token's place and angles.
 // PARTIAL: a vector may hold interleaved pairs of which some turn and some do not.
 template <int KIND, bool INTERLEAVED, bool PARTIAL>
-__global__ void __launch_bounds__(kMaxThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kMaxThreads, ctas_per_sm(KIND)) rope_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ uint4 rows[];                  // [kStages][kUnits][2][threads]
@@ -424,8 +425,8 @@ cudaError_t launch_rope(const RopeParams &p, bool interleaved, cudaStream_t stre
     const int units = (channels / 16 + kUnits - 1) / kUnits;
     const int groups = (units + kMaxThreads - 1) / kMaxThreads;
     const int threads = ((units + groups - 1) / groups + 31) / 32 * 32;
-    // one wave: kCtasPerSm of the largest CTAs, or as many threads in smaller ones, fit an SM
-    const int per_sm = kCtasPerSm * kMaxThreads / threads < 32 ? kCtasPerSm * kMaxThreads / threads : 32;
+    // one wave: ctas_per_sm of the largest CTAs, or as many threads in smaller ones, fit an SM
+    const int fit = ctas_per_sm(KIND) * kMaxThreads / threads, per_sm = fit < 32 ? fit : 32;
     const int64_t wave = (152 * per_sm + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>(p.tokens < wave ? p.tokens : wave), static_cast<unsigned>(groups));
     const size_t rows = static_cast<size_t>(kStages) * kUnits * 2 * threads * sizeof(uint4);
