@@ -242,6 +242,30 @@ def test_one_workspace_in_two_replayed_graphs_and_a_side_stream():
     assert all(torch.equal(x, y) for x, y in zip(other, outs[1]))
 
 
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own; logits made and results taken by the kernels around the calls."""
+    shapes = [(3, 4, 20011, torch.bfloat16), (40, 4, 20000, torch.float32)]
+    sides, jobs = [torch.cuda.Stream() for _ in shapes], []
+    for R, B, V, dtype in shapes:
+        x = normal(R * B, V, R, dtype).to(DEV)
+        cum = torch.from_numpy(spread_cum(R, B, V).astype(np.float32)).to(DEV)
+        space = pa.alloc_workspace(pa.beam_select_workspace_size(R, B, V), DEV)
+        out = tuple(torch.zeros((R, 6), dtype=d, device=DEV) for d in (torch.float32, torch.int32, torch.int32))
+        want = [call(torch.roll(x, 17 * i, 1), cum, 6) for i in range(20)]
+        jobs.append((x, cum, space, out, want, [[] for _ in out]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for side, (x, cum, space, out, _, got) in zip(sides, jobs):
+            with torch.cuda.stream(side):
+                call(torch.roll(x, 17 * i, 1), cum, 6, space=space, out=out)
+                for g, o in zip(got, out):
+                    g.append(o.clone())
+    torch.cuda.synchronize()
+    for *_, want, got in jobs:
+        for i in range(20):
+            assert all(torch.equal(got[k][i], want[i][k]) for k in range(3))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("R,B,V", [(1, 4, 32000), (15, 3, 9001), (16, 3, 9001), (2, 32, 2048), (3, 1, 131072), (2, 5, 50001),
                                    (1, 31, 70), (4, 8, 128000)])
