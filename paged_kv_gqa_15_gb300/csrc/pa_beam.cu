@@ -655,7 +655,7 @@ int64_t chunks_of(int vocab) { return (static_cast<int64_t>(vocab) + kChunk - 1)
 
 template <typename T>
 cudaError_t launch_select(BeamParams &p, cudaStream_t stream) {
-    const bool vectors = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.row_stride % (16 / sizeof(T)) == 0;
+    const bool vectors = api_aligned(p.logits, 16) && p.row_stride % (16 / sizeof(T)) == 0;
     const int groups = (p.chunks + Eight<T>::kAhead - 1) / Eight<T>::kAhead;      // of a row, a warp's at least
     // A cluster's warps, with two groups each at most, for every request of one wave of clusters (16 fit; at 16
     // a call takes 9.4 us instead of 7).  One launch then saves 2.1 us of the host's 10.5, and costs the device 0.1 to
@@ -720,7 +720,9 @@ extern "C" int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, co
     if (!scores || !beams || !tokens || !logits || !cum_scores)
         return api_fail(PA_ERR_INVALID, "null pointer argument");
     const size_t elem = logits_dtype == PA_LOGITS_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(logits) % elem) return api_fail(PA_ERR_INVALID, "logits are not aligned to their type");
+    if (!api_aligned(logits, elem) || !api_aligned(scores, 4) || !api_aligned(beams, 4) || !api_aligned(tokens, 4) ||
+        !api_aligned(cum_scores, 4))
+        return api_fail(PA_ERR_INVALID, "logits, scores, beams, tokens or cum_scores are not aligned to their type");
     const int64_t outs = static_cast<int64_t>(num_requests) * num_out;
     const int64_t rows = static_cast<int64_t>(num_requests) * num_beams;
     const int32_t *written[3] = {reinterpret_cast<int32_t *>(scores), beams, tokens};
@@ -734,7 +736,7 @@ extern "C" int pa_beam_select(float *scores, int32_t *beams, int32_t *tokens, co
             over(logits, ((rows - 1) * stride_row + vocab) * elem))
             return api_fail(PA_ERR_INVALID, "scores, beams and tokens must overlap neither what the call reads nor one another");
     }
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+    if (!workspace || !api_aligned(workspace, 256) ||
         workspace_bytes < pa_beam_select_workspace_size(num_requests, num_beams, vocab))
         return api_fail(PA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed, 256-byte aligned", workspace_bytes,
                         pa_beam_select_workspace_size(num_requests, num_beams, vocab));

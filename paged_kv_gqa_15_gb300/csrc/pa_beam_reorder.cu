@@ -150,12 +150,14 @@ extern "C" int pa_beam_reorder(void *const *pools, int num_pools, int32_t *block
     if (num_requests == 0) return PA_OK;
     if (!block_tables || !seq_lens || !parents || (num_pools > 0 && !pools))
         return api_fail(PA_ERR_INVALID, "null pointer argument");
+    if (!api_aligned(block_tables, 4) || !api_aligned(seq_lens, 4) || !api_aligned(parents, 4))
+        return api_fail(PA_ERR_INVALID, "block_tables, seq_lens and parents must be 4-byte aligned");
     const int64_t slots = static_cast<int64_t>(num_requests) * num_beams;
     if (api_overlap(block_tables, slots * max_blocks_per_seq, seq_lens, slots) ||
         api_overlap(block_tables, slots * max_blocks_per_seq, parents, slots))
         return api_fail(PA_ERR_INVALID, "block_tables must not overlap seq_lens or parents");
     for (int i = 0; i < num_pools; ++i)
-        if (!pools[i] || (reinterpret_cast<uintptr_t>(pools[i]) & 15u))
+        if (!pools[i] || !api_aligned(pools[i], 16))
             return api_fail(PA_ERR_INVALID, "pools[%d] is NULL or not 16-byte aligned", i);
     // a pool listed twice would have its rows moved by two threads at once
     for (int i = 1; i < num_pools; ++i)

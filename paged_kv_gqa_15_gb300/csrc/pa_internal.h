@@ -152,6 +152,8 @@ inline bool api_overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + 4 * static_cast<uintptr_t>(m) && y < x + 4 * static_cast<uintptr_t>(n);
 }
+// Whether p is a multiple of `bytes` (a power of two).
+inline bool api_aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 int api_check_pool(int head_dim, int block_size, int64_t num_blocks, int num_kv_heads, int64_t sb,
                    int64_t sh, int64_t st, int kv_dtype);
 

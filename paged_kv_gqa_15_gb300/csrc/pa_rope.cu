@@ -467,7 +467,7 @@ bool may_overlap(const Extent &a, const Extent &b) {
 }
 
 int check_rows(const char *name, const Rows &r, int64_t tokens, int heads, int head_dim, bool written) {
-    if (!r.base || (reinterpret_cast<uintptr_t>(r.base) & 15u))
+    if (!r.base || !api_aligned(r.base, 16))
         return api_fail(PA_ERR_INVALID, "%s is NULL or not 16-byte aligned", name);
     const int64_t st = tokens > 1 ? r.token : 0, sh = heads > 1 ? r.head : 0;
     constexpr int64_t kMost = INT64_C(1) << 40;      // far beyond memory: offsets stay within 64 bits
@@ -595,6 +595,8 @@ extern "C" int pa_rope(void *q_out, void *k_out, const void *q, const void *k, c
     if (rc) return rc;
     if (num_tokens == 0 || num_q_heads + num_k_heads == 0) return PA_OK;
     if (!positions || !turns) return api_fail(PA_ERR_INVALID, "null pointer argument");
+    if (!api_aligned(positions, 8) || !api_aligned(turns, 8))
+        return api_fail(PA_ERR_INVALID, "positions and turns must be 8-byte aligned");
     RopeParams p;
     std::memset(&p, 0, sizeof p);
     p.q = {q, q_stride_token, q_stride_head};
@@ -657,7 +659,9 @@ extern "C" int pa_rope_append(void *q_out, const void *q, const void *k, const v
     if (num_tokens == 0) return PA_OK;
     if (!positions || !turns || !slot_mapping || !k_cache || !v_cache)
         return api_fail(PA_ERR_INVALID, "null pointer argument");
-    if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+    if (!api_aligned(positions, 8) || !api_aligned(turns, 8) || !api_aligned(slot_mapping, 8))
+        return api_fail(PA_ERR_INVALID, "positions, slot_mapping and turns must be 8-byte aligned");
+    if (!api_aligned(k_cache, 16) || !api_aligned(v_cache, 16))
         return api_fail(PA_ERR_INVALID, "the KV pools must be 16-byte aligned");
     RopeParams p;
     std::memset(&p, 0, sizeof p);

@@ -96,6 +96,7 @@ def rope(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), 1), (dict(T=1 << 31), 2), (dict(nq=-1), 1), (dict(nk=70000), 2), (dict(hd=96), 2), (dict(R=0), 1),
     (dict(R=63), 1), (dict(R=130), 1), (dict(m=float("nan")), 1), (dict(m=float("inf")), 1), (dict(pos=None), 1),
+    (dict(pos=at(4) + 4), 1), (dict(turns=at(5) + 4), 1),
     (dict(turns=None), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(k=at(3) + 8), 1), (dict(ko=at(1) + 2), 1),
     (dict(qt=1020), 1), (dict(kh=-128), 1), (dict(qt=1 << 60), 1), (dict(kot=0), 1), (dict(qoh=64), 1), (dict(qoh=0), 1),
     (dict(qot=512), 1),                                # a token's heads reach into the next token's
@@ -127,6 +128,7 @@ def append(lib, **kw):
     (dict(dt=1, vs=float("inf")), 1), (dict(dt=1, sb=4104), 1), (dict(slots=None), 1), (dict(kc=None), 1), (dict(vc=at(5) + 8), 1),
     (dict(q=None), 1), (dict(v=None), 1), (dict(k=at(2) + 4), 1), (dict(vt=100), 1), (dict(qo=at(1) + 16), 1),
     (dict(qo=at(2)), 1), (dict(qo=at(3)), 1), (dict(qot=256), 1), (dict(m=float("-inf")), 1), (dict(T=0), 0),
+    (dict(pos=at(7) + 4), 1), (dict(turns=at(8) + 1), 1), (dict(slots=at(6) + 4), 1),
 ])
 def test_append_refusals(lib, kw, code):
     assert append(lib, **kw) == code, lib.pa_last_error()
@@ -147,6 +149,7 @@ def select(lib, **kw):
     (dict(V=(1 << 24) + 1, sr=1 << 25), 2), (dict(dt=2), 2), (dict(dt=-1), 2), (dict(sr=999), 1), (dict(sr=-1), 1),
     (dict(sr=1 << 50), 2), (dict(fin=at(6), end=-1), 1), (dict(fin=at(6), end=1000), 1), (dict(sc=None), 1), (dict(bm=None), 1),
     (dict(tk=None), 1), (dict(lg=None), 1), (dict(cum=None), 1), (dict(lg=at(3) + 2), 1), (dict(lg=at(3) + 1, dt=1), 1),
+    (dict(sc=at(0) + 2), 1), (dict(bm=at(1) + 1), 1), (dict(tk=at(2) + 3), 1), (dict(cum=at(4) + 2), 1),
     (dict(ws=None), 4), (dict(ws=at(5) + 16), 4), (dict(bytes=0), 4), (dict(sc=at(4)), 1), (dict(bm=at(4) + 28), 1),
     (dict(bm=at(0) + 60), 1), (dict(tk=at(1)), 1), (dict(sc=at(2)), 1), (dict(tk=at(3) + 7999 * 4), 1),
     (dict(sc=at(6), fin=at(6) + 7), 1), (dict(sc=at(6) - 60, fin=at(6)), 1), (dict(R=0), 0), (dict(R=0, sc=None), 0),
@@ -176,7 +179,7 @@ def reorder(lib, **kw):
     (dict(pools=None), 1), (dict(bt=None), 1), (dict(sl=None), 1), (dict(of=None), 1),
     (dict(pools=(ctypes.c_void_p * 2)(at(0), at(1) + 8)), 1), (dict(pools=(ctypes.c_void_p * 2)(at(0), 0)), 1),
     (dict(pools=(ctypes.c_void_p * 2)(at(0), at(0))), 1), (dict(sl=at(2) + 8 * 4 * 4 - 4), 1), (dict(of=at(2) - 28), 1),
-    (dict(R=0), 0), (dict(R=0, pools=None), 0),
+    (dict(bt=at(2) + 2), 1), (dict(sl=at(3) + 1), 1), (dict(of=at(4) + 2), 1), (dict(R=0), 0), (dict(R=0, pools=None), 0),
 ])
 def test_reorder_refusals(lib, kw, code):
     assert reorder(lib, **kw) == code, lib.pa_last_error()
