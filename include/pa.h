@@ -496,7 +496,11 @@ int pa_rope_table_of(uint64_t *turns_h, const double *frequencies_h, int num_pai
  *   q, k          [num_tokens][heads][head_dim] bf16 by element strides (token, head), each
  *                 a multiple of 16 bytes; head_dim contiguous.  0 heads: not touched.
  *   q_out, k_out  the same shape by strides of their own; q_out may be q and k_out k with
- *                 the same strides (in place), else outputs share no memory with inputs
+ *                 the same strides (in place), else outputs share no memory with inputs or
+ *                 one another.  Slices of one buffer are seen to be apart where they lie
+ *                 beside one another in the stride of their tokens (or heads, if larger), or
+ *                 their rows do in a common divisor of all strides ([heads][3][head_dim]);
+ *                 other interleavings are refused
  *   positions     [num_tokens] int64, any value (negative ones turn back)
  *   turns         [rotary_dim / 2], device, from pa_rope_table
  *   inverse       != 0: by -a.  That is the gradient of the call with inverse == 0 (the

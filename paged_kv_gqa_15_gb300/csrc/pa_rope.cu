@@ -20,6 +20,7 @@
 // tokens of 16 + 8 + 8 heads of 256 in E4M3, 64 channels interleaved: 33 us (90 %).  64 tokens: 1.9 us.
 #include <cmath>
 #include <cstring>
+#include <numeric>
 
 #include "../../include/pa.h"
 #include "pa_device.cuh"
@@ -438,10 +439,11 @@ cudaError_t launch_rope(const RopeParams &p, bool interleaved, cudaStream_t stre
 // ---- argument checks --------------------------------------------------------------------
 
 // The elements of a [tokens][heads][head_dim] tensor in two levels: `outer` steps of runs that span
-// `span` elements.  The stride of an axis of length 1 counts as none.
+// `span` elements.  Every row (of head_dim) starts a whole number of `period`s behind the first; 0 where there is
+// one row.  The stride of an axis of length 1 counts as none.
 struct Extent {
     uintptr_t at;
-    int64_t outer, count, span;     // bytes but for count
+    int64_t outer, count, span, period, row;     // bytes but for count
 };
 
 Extent extent_of(const Rows &r, int64_t tokens, int heads, int head_dim) {
@@ -452,18 +454,26 @@ Extent extent_of(const Rows &r, int64_t tokens, int heads, int head_dim) {
     e.outer = 2 * (by_token ? st : sh);
     e.count = by_token ? tokens : heads;
     e.span = 2 * ((by_token ? (heads - 1) * sh : (tokens - 1) * st) + head_dim);
+    e.period = 2 * std::gcd(st, sh);
+    e.row = 2 * head_dim;
     return e;
 }
 
-// False where the two are seen to share no element: apart as a whole, or with the same outer stride and
-// runs beside one another (the slices of one projection's rows).
+// False where the two are seen to share no element: apart as a whole; with the same outer stride and
+// runs beside one another (the slices of one projection's rows); or with rows beside one another in a period
+// that both keep (the slices of each head's part of a projection).
 bool may_overlap(const Extent &a, const Extent &b) {
     const uintptr_t a_end = a.at + (a.count - 1) * a.outer + a.span, b_end = b.at + (b.count - 1) * b.outer + b.span;
     if (a_end <= b.at || b_end <= a.at) return false;
-    if (a.outer != b.outer || a.outer == 0) return true;
-    const int64_t s = a.outer;
-    const int64_t d = static_cast<int64_t>(b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s);
-    return !(d >= a.span && d + b.span <= s);
+    // whether runs of a and b, every s bytes, lie beside one another
+    auto beside = [&](int64_t s, int64_t run_a, int64_t run_b) {
+        if (s == 0) return false;
+        const uintptr_t u = static_cast<uintptr_t>(s);
+        const int64_t d = static_cast<int64_t>(b.at >= a.at ? (b.at - a.at) % u : (u - (a.at - b.at) % u) % u);
+        return d >= run_a && d + run_b <= s;
+    };
+    if (a.outer == b.outer && beside(a.outer, a.span, b.span)) return false;
+    return !beside(std::gcd(a.period, b.period), a.row, b.row);
 }
 
 int check_rows(const char *name, const Rows &r, int64_t tokens, int heads, int head_dim, bool written) {
