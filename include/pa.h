@@ -461,7 +461,7 @@ int pa_decode_pages(void *out, const void *q, const void *k_cache, const void *v
  *
  * Frequencies come as a table of rotary_dim / 2 numbers made once per model on the HOST
  * and copied to the device: entry i is the fraction of a turn per position, in units of
- * 2^-64.
+ * 2^-64, the nearest one (of bases beyond 2^900, to the 53 bits of a double).
  *
  * pa_rope_table writes the table and the attention factor of f_i = base^(-2 i / R) under a
  * scaling for long contexts by factor s:

@@ -530,6 +530,77 @@ double pair_of_turns(double turns, int rotary_dim, double base, double len) {
     return rotary_dim * std::log(len / (turns * kTwoPi)) / (2 * std::log(base));
 }
 
+// ---- frequencies, in twice a double's bits: an entry holds up to 62 of a frequency ---------
+
+// hi + lo, lo at most half a unit in hi's last place.
+struct Wide {
+    double hi, lo;
+};
+
+Wide plus(const Wide &a, const Wide &b) {
+    const double s = a.hi + b.hi, z = s - a.hi;
+    const double rest = (a.hi - (s - z)) + (b.hi - z) + (a.lo + b.lo);
+    const double hi = s + rest;
+    return {hi, rest - (hi - s)};
+}
+
+Wide times(const Wide &a, const Wide &b) {
+    const double x = a.hi * b.hi;
+    const double rest = std::fma(a.hi, b.hi, -x) + (a.hi * b.lo + a.lo * b.hi);
+    const double hi = x + rest;
+    return {hi, rest - (hi - x)};
+}
+
+Wide over(const Wide &a, const Wide &b) {
+    const double q = a.hi / b.hi;
+    const Wide left = plus(a, times(b, {-q, 0.0}));
+    return plus({q, 0.0}, {left.hi / b.hi, 0.0});
+}
+
+// The n-th root of b > 0: one step of Newton's iteration from the root in a double.  Where its powers or their
+// rounding errors leave a double's range the double stands.
+Wide root(double b, int n) {
+    const double x = std::pow(b, 1.0 / n);
+    if (std::fabs(std::log2(b)) > 900) return {x, 0.0};
+    Wide power = {x, 0.0};
+    for (int i = 1; i < n; ++i) power = times(power, {x, 0.0});
+    const Wide off = plus(over(power, {b, 0.0}), {-1.0, 0.0});        // n times the relative error
+    return plus({x, 0.0}, {-x * off.hi / n, 0.0});
+}
+
+// 1 / 2 pi, to 2^-165.
+constexpr double kTurnsPerRadian[3] = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57, -0x1.6447e493ad4cep-111};
+
+// x modulo 1 in units of 2^-128.
+unsigned __int128 fraction_of(double x) {
+    int e;
+    const double m = std::frexp(std::fabs(x), &e);
+    unsigned __int128 u = static_cast<uint64_t>(std::ldexp(m, 53));
+    e += 128 - 53;
+    u = e >= 128 ? 0 : e >= 0 ? u << e : e > -128 ? u >> -e : 0;
+    return x < 0 ? 0 - u : u;
+}
+
+unsigned __int128 fraction_of_product(double a, double b) {
+    const double x = a * b;
+    return fraction_of(x) + fraction_of(std::fma(a, b, -x));
+}
+
+// The table's entries: f radians a position as turns, the nearest multiple of 2^-64.
+int write_turns(uint64_t *turns_h, const Wide *f, int num_pairs) {
+    if (!turns_h) return api_fail(PA_ERR_INVALID, "null pointer argument");
+    for (int i = 0; i < num_pairs; ++i)
+        if (!std::isfinite(f[i].hi) || !std::isfinite(f[i].lo))
+            return api_fail(PA_ERR_INVALID, "frequency %d is not finite", i);
+    for (int i = 0; i < num_pairs; ++i) {
+        unsigned __int128 u = 0;
+        for (double part : {f[i].hi, f[i].lo})
+            for (double by : kTurnsPerRadian) u += fraction_of_product(part, by);
+        turns_h[i] = static_cast<uint64_t>((u + (static_cast<unsigned __int128>(1) << 63)) >> 64);
+    }
+    return PA_OK;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -538,15 +609,9 @@ extern "C" int pa_rope_table_of(uint64_t *turns_h, const double *frequencies_h, 
     if (num_pairs < 1 || num_pairs > kMaxPairs)
         return api_fail(PA_ERR_INVALID, "num_pairs %d not in [1, %d]", num_pairs, kMaxPairs);
     if (!turns_h || !frequencies_h) return api_fail(PA_ERR_INVALID, "null pointer argument");
-    for (int i = 0; i < num_pairs; ++i)
-        if (!std::isfinite(frequencies_h[i])) return api_fail(PA_ERR_INVALID, "frequency %d is not finite", i);
-    for (int i = 0; i < num_pairs; ++i) {
-        constexpr double kTwoPi = 6.283185307179586476925286766559;
-        const double turns = std::fabs(frequencies_h[i]) / kTwoPi;
-        const uint64_t part = static_cast<uint64_t>(std::nearbyint(std::ldexp(turns - std::floor(turns), 64)));
-        turns_h[i] = frequencies_h[i] < 0 ? 0 - part : part;
-    }
-    return PA_OK;
+    Wide f[kMaxPairs];
+    for (int i = 0; i < num_pairs; ++i) f[i] = {frequencies_h[i], 0.0};
+    return write_turns(turns_h, f, num_pairs);
 }
 
 extern "C" int pa_rope_table(uint64_t *turns_h, float *attention_factor_h, int rotary_dim, double base, int scaling,
@@ -568,28 +633,33 @@ extern "C" int pa_rope_table(uint64_t *turns_h, float *attention_factor_h, int r
     }
     const int n = rotary_dim / 2;
     const double len = static_cast<double>(original_len);
-    double f[kMaxPairs];
-    const double b = scaling == PA_ROPE_NTK ? base * std::pow(factor, rotary_dim / (rotary_dim - 2.0)) : base;
-    for (int i = 0; i < n; ++i) f[i] = std::pow(b, -2.0 * i / rotary_dim);
+    // base^(-i / n) as the powers of the n-th root; the scaled base's as those of two roots,
+    // (base s^(n / (n - 1)))^(-i / n) = base^(-i / n) s^(-i / (n - 1))
+    Wide step = over({1.0, 0.0}, root(base, n)), f[kMaxPairs];
+    if (scaling == PA_ROPE_NTK) step = times(step, over({1.0, 0.0}, root(factor, n - 1)));
+    f[0] = {1.0, 0.0};
+    for (int i = 1; i < n; ++i) f[i] = times(f[i - 1], step);
+    // f / factor where r is 0, f where it is 1
+    auto between = [&](const Wide &x, Wide r) {
+        r = r.hi <= 0 ? Wide{0.0, 0.0} : r.hi >= 1 ? Wide{1.0, 0.0} : r;
+        return times(x, plus(over(plus({1.0, 0.0}, {-r.hi, -r.lo}), {factor, 0.0}), r));
+    };
     float m = 1.f;
     if (scaling == PA_ROPE_LINEAR) {
-        for (int i = 0; i < n; ++i) f[i] /= factor;
+        for (int i = 0; i < n; ++i) f[i] = over(f[i], {factor, 0.0});
     } else if (scaling == PA_ROPE_BANDS) {
         for (int i = 0; i < n; ++i) {
-            const double turns = len * f[i] / 6.283185307179586476925286766559;
-            const double s = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
-            f[i] *= (1 - s) / factor + s;
+            const Wide turns = times(times(f[i], {len, 0.0}), {kTurnsPerRadian[0], kTurnsPerRadian[1]});
+            f[i] = between(f[i], over(plus(turns, {-low, 0.0}), plus({high, 0.0}, {-low, 0.0})));
         }
     } else if (scaling == PA_ROPE_YARN) {
         const double first = std::fmax(std::floor(pair_of_turns(high, rotary_dim, base, len)), 0.0);
         const double last = std::fmin(std::ceil(pair_of_turns(low, rotary_dim, base, len)), rotary_dim - 1.0);
-        for (int i = 0; i < n; ++i) {
-            const double s = std::fmin(std::fmax((i - first) / std::fmax(last - first, 0.001), 0.0), 1.0);
-            f[i] *= s / factor + (1 - s);
-        }
+        for (int i = 0; i < n; ++i)
+            f[i] = between(f[i], plus({1.0, 0.0}, over({first - i, 0.0}, {std::fmax(last - first, 0.001), 0.0})));
         if (factor > 1) m = static_cast<float>(0.1 * std::log(factor) + 1);
     }
-    const int rc = pa_rope_table_of(turns_h, f, n);
+    const int rc = write_turns(turns_h, f, n);
     if (rc == PA_OK && attention_factor_h) *attention_factor_h = m;
     return rc;
 }
