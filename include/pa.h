@@ -554,8 +554,8 @@ size_t pa_beam_select_workspace_size(int num_requests, int num_beams, int vocab)
  * pa_beam_select -- for every request the num_out best of all pairs (beam b, token t) by
  *   score = cum_scores[r][b] + x_t - log sum_u exp x_u,   x the beam's row of logits,
  * best first; equal scores go to the lower beam, then to the lower token.  Scores are
- * compared as sums of two fp32; a row's log-sum-exp is known to 2^-20, so pairs of two beams whose
- * scores are closer than that may come in either order.  Equal rows have equal sums.
+ * compared as sums of two fp32; a row's log-sum-exp is known to 2^-17, so pairs of two beams whose
+ * scores are closer than 2^-16 may come in either order.  Equal rows have equal sums.
  *   logits      [num_requests * num_beams] rows of vocab values of logits_dtype, stride_row
  *               elements apart (rows of any alignment; multiples of 16 bytes are faster).
  *               -inf rules a token out.

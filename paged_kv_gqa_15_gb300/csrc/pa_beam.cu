@@ -2,7 +2,7 @@
 //   score(b, t) = cum[b] + x[b][t] - log sum_t exp x[b][t].
 //
 // Two kernels.  The scan reads every live row once: a warp takes a share of its 256-element chunks (a
-// run), keeps their maximum m and sum of exp(x - m), and writes each chunk's maximum (1 value for 256).  The
+// run), keeps their sum of exp(x - m), m close to their maximum, and writes each chunk's maximum (1 value for 256).  The
 // pick, a CTA per request, joins the runs' sums into each beam's log-sum-exp, finds the chunks that can be among the K
 // best by their maxima, and reads those again: the K best elements lie in them (an element outside is
 // outranked by the K maxima of the chunks before its own).
@@ -10,8 +10,11 @@
 // Order.  Within a beam the order of scores is that of the logits, across beams it needs the sums, so a
 // score is kept as an unevaluated sum of two fp32 (48 bits: differences and sums with their rounding errors):
 // two logits next to each other in fp32 stay apart behind an offset of any usual size.  Equal scores go to
-// the lower beam, then the lower token.  The sums come from ex2.approx (2^-22 relative) in
-// compensated fp32, so that cum - logsumexp is known to better than 2^-20, and equal rows get equal sums:
+// the lower beam, then the lower token.  The sums come from ex2.approx (2^-22 relative) in compensated fp32.
+// An exponent (x - m) log2 e is rounded twice, and what a run, or the join of the runs, counts from another m is
+// multiplied once more; each such step is off by less than 2^-19 over the distances that 2^24 logits reach, four of them
+// are the most that matter, and the additions cost 2^-20: cum - logsumexp is known to 2^-17 (of usual rows to
+// 2^-21).  Equal rows get equal sums:
 // chunks and lanes are counted from the row's start.
 //
 // The scan is bound by reading the logits once (the chunk maxima add 1/128 of bf16 logits): 64 requests x 8
@@ -29,6 +32,7 @@ namespace pa {
 namespace {
 
 constexpr int kChunk = 256;                  // logits whose maximum is kept
+constexpr float kAbove = 8.f;                // what a run's largest logit may lie above the one it counts from
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = 152 * 32;         // that are on the GPU at a time
 constexpr int kPickThreads = 1024;
@@ -44,7 +48,7 @@ struct BeamParams {
     const float *cum;
     const uint8_t *finished;                 // or null
     float *chunk_max;                        // [rows][chunks]
-    float2 *runs;                            // [rows][num_runs]: maximum, sum of exp(x - maximum)
+    float2 *runs;                            // [rows][num_runs]: a logit m within kAbove of the maximum, sum of exp(x - m)
     int64_t row_stride;
     int num_requests, num_beams, vocab, num_out, end_token;
     int chunks, num_runs;
@@ -200,8 +204,10 @@ struct Eight<float> {
 };
 
 // A row's groups of chunks go to num_runs warps in turn, so that they read it side by side; a warp's next
-// group is on its way while it works on one.  The running maximum is the warp's, so that a group needs one
-// comparison and, seldom, one rescaling.
+// group is on its way while it works on one.  The logit m that exponents are counted from is the warp's, so that a
+// group needs one comparison and, seldom, one rescaling.  It is no more than kAbove below the largest logit so
+// far: every rescaling costs some 2^-20, and where m followed each new maximum a long row that rises from end to
+// end gathered hundreds of them.  By steps of kAbove, what has been rescaled three times is e^-24 of the sum.
 template <typename T, bool VECTORS>
 __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) {
     constexpr int kAhead = Eight<T>::kAhead;
@@ -213,7 +219,7 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
     // groups of whole chunks, shared out in turn; what is left after them is the next warp's
     const int whole = p.vocab / kChunk, groups = whole / kAhead;
     float m = -INFINITY, s = 0.f, e = 0.f;
-    auto rise = [&](float top) {                 // to a larger maximum
+    auto rise = [&](float top) {                 // to a larger logit
         const float f = exp2_approx((m - top) * kLog2e);
         s *= f, e *= f;
         m = top;
@@ -252,7 +258,7 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
             if (lane == a) mine = t;
         }
         if (lane < kAhead) best[g * kAhead + lane] = mine;
-        if (top > m) rise(top);
+        if (top > m + kAbove) rise(top);
         const float low = m == -INFINITY ? 0.f : -m;
         uint64_t sum[kAhead];
 #pragma unroll
@@ -276,7 +282,7 @@ __device__ __forceinline__ void scan_run(const BeamParams &p, int row, int run) 
         }
         const float top = warp_max(x[0].top());
         if (lane == 0) best[c] = top;
-        if (top > m) rise(top);
+        if (top > m + kAbove) rise(top);
         const float low = m == -INFINITY ? 0.f : -m;
         const float2 both = split(sum_of(x[0], pair(low, low)));
         add_compensated(s, e, both.x + both.y);
@@ -316,7 +322,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 
 // What a beam's logits have added to them to become scores: x - top + (hi + lo).
 struct Offset {
-    float top, hi, lo;                       // the largest logit; cum - log sum exp(x - top) as two fp32
+    float top, hi, lo;                       // a logit near the largest; cum - log sum exp(x - top) as two fp32
 };
 
 // The score of logit x as a key of two fp32; 0 where it is -inf (or not a number).
@@ -437,7 +443,7 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     for (int i = lane + 32 * kPer; i < p.num_runs; i += 32) m = fmaxf(m, runs[i].x);
     m = warp_max(m);
     float s = 0.f, e = 0.f;
-    // an empty run (its maximum -inf) has a sum of 0, or NaN
+    // an empty run (its m -inf) has a sum of 0, or NaN
     auto add = [&](float2 run) {
         add_compensated(s, e, run.y * (run.x == m ? 1.f : exp2_approx((run.x - m) * kLog2e)));
     };
@@ -454,8 +460,8 @@ __device__ __forceinline__ void join_runs(const BeamParams &p, PickSpace &sp, in
     if (bad || (kind == kLive && m == -INFINITY)) kind = kOut;      // or every token is ruled out
     Offset offset = {0.f, cum, 0.f};
     if (kind == kLive) {
-        // s = 2^n f with f within [0.7, 1.5), so that log f, rounded to fp32, is off by 2^-26 at most; n log 2 in
-        // two parts, the first of 12 bits (its products with n are exact), and the sums with their errors
+        // s = 2^n f with f within [0.7071, 1.4143), so that log f, off by its last place, is off by 2^-25 at most; n
+        // log 2 in two parts, the first of 12 bits (its products with n are exact), and the sums with their errors
         int n;
         float f = frexpf(s, &n);
         if (f < 0.70710678f) f *= 2.f, n -= 1;
