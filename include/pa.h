@@ -522,7 +522,8 @@ int pa_rope(void *q_out, void *k_out, const void *q, const void *k, const int64_
  *                   them lies in the caches
  *   slot_mapping    [num_tokens] int64; a token whose slot is negative is padding: nothing of
  *                   it is written, its row of q_out included.  A slot outside the pool is
- *                   treated the same and sets PA_ERR_DEVICE_BOUNDS.
+ *                   treated the same and sets PA_ERR_DEVICE_BOUNDS.  Of two tokens with the
+ *                   same slot in one call, each channel there is one's or the other's
  */
 int pa_rope_append(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
                    void *v_cache, const int64_t *slot_mapping, const int64_t *positions,

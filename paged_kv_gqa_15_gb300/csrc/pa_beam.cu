@@ -12,14 +12,14 @@
 // two logits next to each other in fp32 stay apart behind an offset of any usual size.  Equal scores go to
 // the lower beam, then the lower token.  The sums come from ex2.approx (2^-22 relative) in compensated fp32.
 // An exponent (x - m) log2 e is rounded twice, and what a run, or the join of the runs, counts from another m is
-// multiplied once more; each such step is off by less than 2^-19 over the distances that 2^24 logits reach, four of them
-// are the most that matter, and the additions cost 2^-20: cum - logsumexp is known to 2^-17 (of usual rows to
-// 2^-21).  Equal rows get equal sums:
+// multiplied once more: each step is off by 1.3 x 2^-20 over a distance of 8 and 1.7 over 12, ex2 included.  At most
+// three steps behind an element's own matter (what lies e^-24 below is nothing even of 2^24 logits); they cost 5 x
+// 2^-20 in all, the additions and the logarithm 1.2: cum - logsumexp is known to 2^-17.  Equal rows get equal sums:
 // chunks and lanes are counted from the row's start.
 //
 // The scan is bound by reading the logits once (the chunk maxima add 1/128 of bf16 logits): 64 requests x 8
 // beams x 128000 bf16, 131 MB, in about 21 us, 93 % of the copy rate; the pick behind it is a chain of 6 us.
-// The call takes 27 us; 4 beams x 32000 fp32 6.1, 12 x 5 x 50001 fp32 8.0.  Few requests that are not being
+// The call takes 27 us; captured, 4 beams x 32000 fp32 6.3, 12 x 5 x 50001 fp32 8.3.  Few requests that are not being
 // captured take one launch instead of the two.
 #include <cmath>
 #include <cstring>
@@ -665,9 +665,9 @@ cudaError_t launch_select(BeamParams &p, cudaStream_t stream) {
     const int groups = (p.chunks + Eight<T>::kAhead - 1) / Eight<T>::kAhead;      // of a row, a warp's at least
     // A cluster's warps, with two groups each at most, for every request of one wave of clusters (16 fit; at 16
     // a call takes 9.4 us instead of 7).  One launch then saves 2.1 us of the host's 10.5, and costs the device 0.1 to
-    // 1.9 us (4 beams x 32000 fp32 6.2 -> 6.7, 4 x 128000 bf16 6.6 -> 8.5), which such a call waits for
-    // less than for the host; a captured one has no host to wait for and keeps its two launches.
-    // The runs are the same, so the results are.
+    // 1.6 us (4 beams x 32000 fp32 6.5 -> 7.1, 4 x 128000 bf16 7.4 -> 8.7, 16 x 128000 7.9 -> 9.5), which a stream that
+    // waits for the host does not notice (one with work queued up does); a captured call has no host to wait for
+    // and keeps its two launches.  The runs are the same, so the results are.
     const int warps = kCluster * kPickThreads / 32;
     if (p.num_requests <= kSmallRequests && p.num_beams * groups <= 2 * warps) {
         p.num_runs = groups < warps / p.num_beams ? groups : warps / p.num_beams;
@@ -679,7 +679,9 @@ cudaError_t launch_select(BeamParams &p, cudaStream_t stream) {
                            : launch_after(beam_small_kernel<T, false>, grid, kPickThreads, p, stream);
         }
     } else {
-        // the rows in one wave of warps
+        // the rows in one wave of warps.  Rows are not divided unevenly: 2432 to 4863 of them leave up to half of the
+        // warps idle, and past 4864 the last ones are read alone (32 beams x 16000 bf16: 76 requests 21.1 us, 77
+        // 27.3, 152 32.7, 153 44.2)
         const int64_t per_row = kScanWarps / (static_cast<int64_t>(p.num_requests) * p.num_beams);
         p.num_runs = static_cast<int>(per_row < 1 ? 1 : per_row < groups ? per_row : groups);
     }
